@@ -26,6 +26,13 @@
  *   - mi_fp4_quantize         bf16/fp16/fp32 -> NVFP4 codes + UE4M3 scales, the producer of
  *                             the NVFP4 operands (mm_nvfp4_lora, the paragraph after the
  *                             formula, and its alpha parameter)
+ *   - mi_fp8_quantize         bf16/fp16/fp32 -> e4m3 codes with one fp32 scale per 1 x 128 or
+ *                             128 x 128 block, optionally of silu(gate) * up
+ *   - mi_add_rmsnorm_fp8      residual addition + RMS norm with that 8-bit output
+ *   - mi_mm_fp8_block         GEMM of such operands, and
+ *   - mi_grouped_mm_fp8_block its ragged per-expert form
+ *   - mi_moe_combine_rows     permuted rows -> token rows with the routing weights, and
+ *   - mi_moe_combine_rows_backward  its gradients
  *
  * Conventions shared by every entry point
  *   - All tensor pointers are DEVICE pointers owned by the caller.  The library
@@ -438,6 +445,122 @@ MI_API mi_status mi_nvfp4_dequant_bf16(const uint8_t* codes, const uint8_t* sf, 
 MI_API mi_status mi_fp4_quantize(const void* x, int64_t batch, int64_t rows, int64_t k,
                           mi_dtype x_dtype, const float* global_scale, uint8_t* codes,
                           uint8_t* sf, size_t sf_bytes, void* stream);
+
+/*
+ * 8-bit block-scaled operands.  Codes are e4m3 (the "fn" form: largest value
+ * 448, no infinity, codes 0x7f and 0xff are NaN), one fp32 scale per block of 128
+ * consecutive columns: a value is code * scale.  Activations have a scale per
+ * row and block (1 x 128), weights one per 128 rows and block (128 x 128).
+ * Scales are row-major [scale rows, mi_fp8_scale_cols(k)]: one column per 128
+ * of k, padded with zeros to a multiple of 4 (16-byte rows; mi_moe_permute_rows
+ * moves them like any other row).  Blocks at the end of k or of the rows may be
+ * partial; k is a multiple of 16.
+ */
+MI_API int64_t mi_fp8_scale_cols(int64_t k); /* 4 * ceil(k / 512) */
+
+/*
+ * The producer of those operands:
+ *     scale = max(amax(block) / 448, 2^-126),  code = e4m3_rne(y * (1 / scale))
+ * in fp32, with y = x, or with swiglu y = silu(gate) * up of rows [gate | up].
+ * An all-zero block has scale 2^-126 and zero codes.  A block holding a NaN or
+ * an infinity has that as its scale and dequantises to NaN throughout.
+ *   x       dtype [batch, rows, k] (swiglu: [batch, rows, 2k]), MI_BF16, MI_F16 or MI_F32
+ *   codes   uint8 [batch, rows, k], written
+ *   scales  block_rows 1: fp32 [batch, rows, cols]; block_rows 128: fp32 [batch,
+ *           ceil(rows / 128), cols]; cols = mi_fp8_scale_cols(k); every entry written
+ * Requirements: block_rows 1 or 128 (swiglu: 1), k % 16 == 0, all 16-byte
+ * aligned; the outputs may not overlap x.  batch == 0 or rows == 0 is a no-op.
+ */
+MI_API mi_status mi_fp8_quantize(const void* x, int64_t batch, int64_t rows, int64_t k,
+                              mi_dtype dtype, int64_t block_rows, int swiglu, uint8_t* codes,
+                              float* scales, void* stream);
+
+/*
+ * Residual addition and RMS norm with 8-bit output, for every token:
+ *     h = x + residual        fp32; residual_out = h rounded once to dtype
+ *     y = h / sqrt(mean(h^2) + eps) * weight        fp32, from the unrounded h
+ *     codes, scales = the 1 x 128 quantisation of y (as mi_fp8_quantize)
+ *     norm_out = y rounded once to dtype
+ *   x, residual   dtype [num_tokens, hidden_size]; residual NULL: h = x, and
+ *                 residual_out has to be NULL too
+ *   weight        [hidden_size] of weight_dtype: dtype or MI_F32
+ *   residual_out  dtype [num_tokens, hidden_size]; may be residual or x itself
+ *   norm_out      the same shape, or NULL (a router that reads the normed rows)
+ *   codes, scales uint8 [num_tokens, hidden_size], fp32 [num_tokens, cols]
+ * Requirements: hidden_size % 16 == 0, eps >= 0, all 16-byte aligned; no other
+ * overlap of outputs with inputs.  num_tokens == 0 is a no-op.
+ */
+MI_API mi_status mi_add_rmsnorm_fp8(const void* x, const void* residual, const void* weight,
+                                 mi_dtype dtype, mi_dtype weight_dtype, int64_t num_tokens,
+                                 int64_t hidden_size, float eps, void* residual_out,
+                                 void* norm_out, uint8_t* codes, float* scales, void* stream);
+
+/*
+ * GEMM of 8-bit block-scaled operands:
+ *     out[i, j] = sum_B a_scale[i, B] * b_scale[j / 128, B] * sum_{c in B} a[i, c] * b[j, c]
+ * over the blocks B of 128 columns; products and sums in fp32, one rounding.
+ * A NaN code or scale makes the outputs NaN that its row and column reach.
+ *   a, a_scale   uint8 [m, k], fp32 [m, cols]            (1 x 128 scales)
+ *   b, b_scale   uint8 [n, k], fp32 [ceil(n / 128), cols] (128 x 128 scales)
+ *   out          out_dtype [m, n] (MI_BF16, MI_F16 or MI_F32)
+ * Requirements: n % 16 == 0, k % 16 == 0, all 16-byte aligned.  k >= 2^22 or
+ * n >= 2^20 returns MI_EUNSUPPORTED.  m == 0 is a no-op.
+ */
+MI_API mi_status mi_mm_fp8_block(const uint8_t* a, const float* a_scale, int64_t m, int64_t k,
+                              const uint8_t* b, const float* b_scale, int64_t n, void* out,
+                              mi_dtype out_dtype, void* stream);
+
+/*
+ * The ragged form: the same product for the rows [m_indptr[e], m_indptr[e+1])
+ * of every expert e with b[e] (m_indptr as for mi_grouped_mm_bf16: device,
+ * int32 [batch + 1], non-decreasing, read on the device only).  Rows outside the
+ * groups are not written.
+ *   a, a_scale   uint8 [m_rows, k], fp32 [m_rows, cols]
+ *   b, b_scale   uint8 [batch, n, k], fp32 [batch, ceil(n / 128), cols]
+ *   out          out_dtype [m_rows, n]
+ * Requirements: as above, and 1 <= batch <= 1024.
+ */
+MI_API mi_status mi_grouped_mm_fp8_block(const uint8_t* a, const float* a_scale, int64_t m_rows,
+                                      int64_t k, const uint8_t* b, const float* b_scale,
+                                      int64_t batch, int64_t n, const int32_t* m_indptr,
+                                      void* out, mi_dtype out_dtype, void* stream);
+
+/*
+ * The way back from permuted rows to token rows:
+ *     out[t] = sum_j weights[t, j] * rows[perm[t * top_k + j]]
+ * in fp32 over the slots in order, rounded once; every element of out is written.
+ * A slot whose entry is outside [0, num_rows) contributes nothing (its weight is
+ * not looked at).  weights == NULL: all ones, which is the gradient of
+ * mi_moe_permute_rows with respect to its token rows.
+ *   rows     rows_dtype [num_rows, hidden_size];  perm int32 [num_tokens * top_k]
+ *   weights  fp32 [num_tokens, top_k] or NULL
+ *   out      out_dtype [num_tokens, hidden_size]; may not overlap rows
+ * Requirements: hidden_size % 8 == 0, rows and out 16-byte aligned, top_k >= 1,
+ * num_tokens * top_k < 2^31.  num_tokens == 0 is a no-op.
+ */
+MI_API mi_status mi_moe_combine_rows(const void* rows, mi_dtype rows_dtype, int64_t num_rows,
+                                  int64_t hidden_size, const int32_t* perm,
+                                  const float* weights, int64_t num_tokens, int64_t top_k,
+                                  void* out, mi_dtype out_dtype, void* stream);
+
+/*
+ * Its gradients, given grad_out of out (grad_dtype [num_tokens, hidden_size]):
+ *     grad_rows[perm[t * top_k + j]] = weights[t, j] * grad_out[t]   rounded once
+ *     grad_weights[t, j] = sum_c rows[perm[t * top_k + j], c] * grad_out[t, c]
+ * and 0 for the weight of a slot whose entry is outside [0, num_rows).
+ *   inverse       int32 [num_rows], the permuted_idx_to_expanded_idx that goes with
+ *                 perm: rows whose entry is negative get zeros, so every row is
+ *                 written.  NULL: rows no slot points at are untouched
+ *   grad_rows     rows_dtype [num_rows, hidden_size];  may not overlap the inputs
+ *   grad_weights  fp32 [num_tokens, top_k], or NULL (rows is then not read and may be)
+ * Requirements: as above, num_rows < 2^31.  Two slots with the same row (an
+ * invalid permutation) leave one of the two gradients there.
+ */
+MI_API mi_status mi_moe_combine_rows_backward(
+    const void* grad_out, mi_dtype grad_dtype, const void* rows, mi_dtype rows_dtype,
+    int64_t num_rows, int64_t hidden_size, const int32_t* perm, const int32_t* inverse,
+    const float* weights, int64_t num_tokens, int64_t top_k, void* grad_rows,
+    float* grad_weights, void* stream);
 
 #ifdef __cplusplus
 }

@@ -34,6 +34,13 @@ EXPORTS = [
     "mi_prepare_lora_fold",
     "mi_nvfp4_dequant_bf16",
     "mi_fp4_quantize",
+    "mi_fp8_scale_cols",
+    "mi_fp8_quantize",
+    "mi_add_rmsnorm_fp8",
+    "mi_mm_fp8_block",
+    "mi_grouped_mm_fp8_block",
+    "mi_moe_combine_rows",
+    "mi_moe_combine_rows_backward",
 ]
 
 _lib = None
@@ -110,6 +117,21 @@ def lib() -> ctypes.CDLL:
         L.mi_nvfp4_dequant_bf16.argtypes = [P, P, SZ, I64, I64, P, P]
         L.mi_fp4_quantize.restype = I32
         L.mi_fp4_quantize.argtypes = [P, I64, I64, I64, I32, P, P, P, SZ, P]
+        L.mi_fp8_scale_cols.restype = I64
+        L.mi_fp8_scale_cols.argtypes = [I64]
+        L.mi_fp8_quantize.restype = I32
+        L.mi_fp8_quantize.argtypes = [P, I64, I64, I64, I32, I64, I32, P, P, P]
+        L.mi_add_rmsnorm_fp8.restype = I32
+        L.mi_add_rmsnorm_fp8.argtypes = [P, P, P, I32, I32, I64, I64, F32, P, P, P, P, P]
+        L.mi_mm_fp8_block.restype = I32
+        L.mi_mm_fp8_block.argtypes = [P, P, I64, I64, P, P, I64, P, I32, P]
+        L.mi_grouped_mm_fp8_block.restype = I32
+        L.mi_grouped_mm_fp8_block.argtypes = [P, P, I64, I64, P, P, I64, I64, P, P, I32, P]
+        L.mi_moe_combine_rows.restype = I32
+        L.mi_moe_combine_rows.argtypes = [P, I32, I64, I64, P, P, I64, I64, P, I32, P]
+        L.mi_moe_combine_rows_backward.restype = I32
+        L.mi_moe_combine_rows_backward.argtypes = [P, I32, P, I32, I64, I64, P, P, P, I64, I64,
+                                                   P, P, P]
         _lib = L
     return _lib
 

@@ -38,6 +38,14 @@ __all__ = [
     "nvfp4_dequant",
     "fp4_quantize",
     "sf_bytes_needed",
+    "fp8_scale_cols",
+    "fp8_quantize",
+    "add_rmsnorm_fp8",
+    "mm_fp8_block",
+    "grouped_mm_fp8_block",
+    "moe_combine_rows",
+    "moe_combine_rows_backward",
+    "moe_permute_rows_backward",
 ]
 
 _DT = {torch.bfloat16: MI_BF16, torch.float16: MI_F16, torch.float32: MI_F32}
@@ -587,3 +595,296 @@ def fp4_quantize(x: torch.Tensor, global_scale: torch.Tensor, *, codes: torch.Te
                                      _ptr(global_scale.contiguous()), _ptr(codes), _ptr(sf),
                                      sf.numel(), _stream(x.device)))
     return codes, sf
+
+
+# ---------------------------------------------------------------------------
+# 8-bit block-scaled operands
+# ---------------------------------------------------------------------------
+
+_F8 = torch.float8_e4m3fn
+
+
+def _one_gpu(name, dev, *tensors):
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name}: all tensors must be on the same GPU")
+
+
+def _launch(dev, fn, *args):
+    """Enqueue on `dev`'s current stream, with `dev` current for the launch."""
+    if torch.cuda.current_device() == dev.index:
+        check(fn(*args, _stream(dev)))
+    else:
+        with torch.cuda.device(dev):
+            check(fn(*args, _stream(dev)))
+
+
+def fp8_scale_cols(k: int) -> int:
+    """Columns of the scale rows of ``k`` values: one per 128, padded to a multiple of 4."""
+    return 4 * (-(-k // 512))
+
+
+def _fp8_out(name, x, codes, scales, codes_shape, scale_shape):
+    if codes is None:
+        codes = torch.empty(codes_shape, dtype=_F8, device=x.device)
+    if scales is None:
+        scales = torch.empty(scale_shape, dtype=torch.float32, device=x.device)
+    _need(codes.dtype == _F8 and codes.shape == codes_shape and codes.is_contiguous(),
+          f"{name}: codes must be contiguous float8_e4m3fn of shape {tuple(codes_shape)}")
+    _need(scales.dtype == torch.float32 and scales.shape == scale_shape and
+          scales.is_contiguous(),
+          f"{name}: scales must be contiguous float32 of shape {tuple(scale_shape)}")
+    return codes, scales
+
+
+def fp8_quantize(x: torch.Tensor, *, block_rows: int = 1, swiglu: bool = False,
+                 codes: torch.Tensor | None = None, scales: torch.Tensor | None = None):
+    """``(codes, scales)`` of ``x`` (bf16 / fp16 / fp32, ``[rows, K]`` or ``[B, rows, K]``):
+    float8_e4m3fn codes of its shape and fp32 scales ``amax / 448`` of every
+    block, the operands of :func:`mm_fp8_block` and :func:`grouped_mm_fp8_block`.
+
+    ``block_rows=1``: a scale per row and 128 columns (activations), scales
+    ``[..., rows, fp8_scale_cols(K)]``; ``block_rows=128``: one per 128 x 128
+    block (weights), ``[..., ceil(rows / 128), fp8_scale_cols(K)]``.  With
+    ``swiglu`` (``block_rows=1``) the rows of ``x`` are ``[gate | up]`` of
+    ``2K`` columns and ``silu(gate) * up`` is quantised.  K is a multiple of 16.
+    """
+    _need(x.dtype in _DT and x.dim() in (2, 3), "fp8_quantize: x must be a bf16, fp16 or fp32 "
+          "[rows, K] or [B, rows, K] tensor")
+    _need(block_rows in (1, 128), "fp8_quantize: block_rows must be 1 or 128")
+    _need_cuda("fp8_quantize", x, codes, scales)
+    _one_gpu("fp8_quantize", x.device, codes, scales)
+    rows, k = x.shape[-2], x.shape[-1]
+    if swiglu:
+        _need(k % 2 == 0, "fp8_quantize: swiglu needs rows [gate | up]")
+        k //= 2
+    lead = x.shape[:-2]
+    codes, scales = _fp8_out("fp8_quantize", x, codes, scales, (*lead, rows, k),
+                             (*lead, -(-rows // block_rows), fp8_scale_cols(k)))
+    x = x.contiguous()
+    _launch(x.device, _lib.lib().mi_fp8_quantize, x.data_ptr(), lead[0] if lead else 1, rows, k,
+            _DT[x.dtype], block_rows, int(swiglu), codes.data_ptr(), scales.data_ptr())
+    return codes, scales
+
+
+def add_rmsnorm_fp8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
+                    *, eps: float = 1e-6, with_norm: bool = False,
+                    codes: torch.Tensor | None = None, scales: torch.Tensor | None = None,
+                    residual_out: torch.Tensor | None = None,
+                    norm_out: torch.Tensor | None = None):
+    """``h = x + residual``, ``y = h / sqrt(mean(h^2) + eps) * weight`` and the 1 x 128
+    quantisation of ``y``: ``(codes, scales, residual_out)``, with ``y`` itself in
+    ``x``'s type as a fourth where ``with_norm`` is set or ``norm_out`` is given.
+
+    ``x`` (and ``residual``) ``[T, H]`` bf16, fp16 or fp32; ``weight`` ``[H]`` of
+    that type or fp32.  ``residual_out`` is ``h`` rounded once (the norm uses the
+    unrounded sum); it may be ``residual`` or ``x`` itself, and is None without a
+    residual.
+    """
+    _need(x.dim() == 2 and x.dtype in _DT, "add_rmsnorm_fp8: x must be [T, H] bf16, fp16 or fp32")
+    T, H = x.shape
+    _need(weight.shape == (H,) and weight.dtype in (x.dtype, torch.float32),
+          "add_rmsnorm_fp8: weight must be [H] of x's type or float32")
+    _need(residual is None or (residual.shape == x.shape and residual.dtype == x.dtype),
+          "add_rmsnorm_fp8: residual must have x's shape and type")
+    _need(residual is not None or residual_out is None,
+          "add_rmsnorm_fp8: residual_out needs a residual")
+    _need_cuda("add_rmsnorm_fp8", x, weight, residual, codes, scales, residual_out, norm_out)
+    _one_gpu("add_rmsnorm_fp8", x.device, weight, residual, codes, scales, residual_out, norm_out)
+    codes, scales = _fp8_out("add_rmsnorm_fp8", x, codes, scales, (T, H), (T, fp8_scale_cols(H)))
+    x, weight = x.contiguous(), weight.contiguous()
+    if residual is not None:
+        residual = residual.contiguous()
+        if residual_out is None:
+            residual_out = torch.empty_like(x)
+    if norm_out is None and with_norm:
+        norm_out = torch.empty_like(x)
+    for name, t in (("residual_out", residual_out), ("norm_out", norm_out)):
+        _need(t is None or (t.shape == x.shape and t.dtype == x.dtype and t.is_contiguous()),
+              f"add_rmsnorm_fp8: {name} must be contiguous with x's shape and type")
+    _launch(x.device, _lib.lib().mi_add_rmsnorm_fp8, x.data_ptr(), _ptr(residual),
+            weight.data_ptr(), _DT[x.dtype], _DT[weight.dtype], T, H, float(eps),
+            _ptr(residual_out), _ptr(norm_out), codes.data_ptr(), scales.data_ptr())
+    return (codes, scales, residual_out) if norm_out is None else \
+        (codes, scales, residual_out, norm_out)
+
+
+def mm_fp8_block(a: torch.Tensor, b: torch.Tensor, a_scale: torch.Tensor, b_scale: torch.Tensor,
+                 *, out: torch.Tensor | None = None,
+                 out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """``(a * a_scale) @ (b * b_scale)^T`` of e4m3 codes with a scale per block of 128.
+
+    ``a`` float8_e4m3fn ``[M, K]`` with fp32 ``a_scale`` ``[M, fp8_scale_cols(K)]``
+    (1 x 128 blocks), ``b`` ``[N, K]`` with ``b_scale`` ``[ceil(N / 128),
+    fp8_scale_cols(K)]`` (128 x 128 blocks); N and K multiples of 16, any M.
+    Sums in fp32, one rounding to ``out_dtype`` (bf16, fp16 or fp32).
+    """
+    _need(a.dtype == _F8 and b.dtype == _F8 and a.dim() == 2 and b.dim() == 2 and
+          a.shape[1] == b.shape[1],
+          "mm_fp8_block: a and b must be float8_e4m3fn [M, K] and [N, K]")
+    (M, K), N = a.shape, b.shape[0]
+    cols = fp8_scale_cols(K)
+    _need(a_scale.dtype == torch.float32 and a_scale.shape == (M, cols),
+          f"mm_fp8_block: a_scale must be float32 (M, {cols})")
+    _need(b_scale.dtype == torch.float32 and b_scale.shape == (-(-N // 128), cols),
+          f"mm_fp8_block: b_scale must be float32 (ceil(N / 128), {cols})")
+    _need(out_dtype in _DT, "mm_fp8_block: out_dtype must be bfloat16, float16 or float32")
+    _need_cuda("mm_fp8_block", a, b, a_scale, b_scale, out)
+    _one_gpu("mm_fp8_block", a.device, b, a_scale, b_scale, out)
+    a, b, a_scale, b_scale = (t.contiguous() for t in (a, b, a_scale, b_scale))
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=a.device)
+    _need(out.shape == (M, N) and out.dtype == out_dtype and out.is_contiguous(),
+          "mm_fp8_block: out must be a contiguous (M, N) tensor of out_dtype")
+    _launch(a.device, _lib.lib().mi_mm_fp8_block, a.data_ptr(), a_scale.data_ptr(), M, K,
+            b.data_ptr(), b_scale.data_ptr(), N, out.data_ptr(), _DT[out_dtype])
+    return out
+
+
+def grouped_mm_fp8_block(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor,
+                         b_scale: torch.Tensor, m_indptr: torch.Tensor,
+                         out: torch.Tensor | None = None,
+                         out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """:func:`mm_fp8_block` of every expert's rows ``m_indptr[e] : m_indptr[e+1]`` with ``b[e]``.
+
+    ``a`` ``(cum_m, K)`` and ``a_scale`` ``(cum_m, fp8_scale_cols(K))``, ``b``
+    ``(batch, N, K)`` and ``b_scale`` ``(batch, ceil(N / 128), fp8_scale_cols(K))``,
+    ``m_indptr`` int32 ``(batch+1,)`` read on the device.  Rows outside the
+    groups of a caller-provided ``out`` are untouched (a fresh ``out`` is
+    zero-filled there).
+    """
+    _need(a.dtype == _F8 and b.dtype == _F8 and a.dim() == 2 and b.dim() == 3 and
+          a.shape[1] == b.shape[2],
+          "grouped_mm_fp8_block: a and b must be float8_e4m3fn (cum_m, K) and (batch, N, K)")
+    (M, K), (E, N) = a.shape, b.shape[:2]
+    cols = fp8_scale_cols(K)
+    _need(a_scale.dtype == torch.float32 and a_scale.shape == (M, cols),
+          f"grouped_mm_fp8_block: a_scale must be float32 (cum_m, {cols})")
+    _need(b_scale.dtype == torch.float32 and b_scale.shape == (E, -(-N // 128), cols),
+          f"grouped_mm_fp8_block: b_scale must be float32 (batch, ceil(N / 128), {cols})")
+    _need(m_indptr.dtype == torch.int32 and m_indptr.shape == (E + 1,),
+          "grouped_mm_fp8_block: m_indptr must be int32 of shape (batch_size + 1,)")
+    _need(out_dtype in _DT, "grouped_mm_fp8_block: out_dtype must be bfloat16, float16 or float32")
+    _need_cuda("grouped_mm_fp8_block", a, a_scale, b, b_scale, m_indptr, out)
+    _one_gpu("grouped_mm_fp8_block", a.device, a_scale, b, b_scale, m_indptr, out)
+    a, a_scale, b, b_scale, m_indptr = (t.contiguous() for t in
+                                        (a, a_scale, b, b_scale, m_indptr))
+    if out is None:
+        out = torch.zeros((M, N), dtype=out_dtype, device=a.device)
+    _need(out.shape == (M, N) and out.dtype == out_dtype and out.is_contiguous(),
+          "grouped_mm_fp8_block: out must be a contiguous (cum_m, N) tensor of out_dtype")
+    _launch(a.device, _lib.lib().mi_grouped_mm_fp8_block, a.data_ptr(), a_scale.data_ptr(), M, K,
+            b.data_ptr(), b_scale.data_ptr(), E, N, m_indptr.data_ptr(), out.data_ptr(),
+            _DT[out_dtype])
+    return out
+
+
+# ---------------------------------------------------------------------------
+# permuted rows -> token rows, and the gradients
+# ---------------------------------------------------------------------------
+
+def _combine(name, rows, perm, weights, T, top_k, out_dtype, out):
+    _need(rows.dim() == 2 and rows.dtype in _DT,
+          f"{name}: the rows must be [num_rows, H] bf16, fp16 or fp32")
+    _need(perm.dtype == torch.int32 and perm.numel() == T * top_k,
+          f"{name}: expanded_idx_to_permuted_idx must be int32 [num_tokens*top_k]")
+    out_dtype = rows.dtype if out_dtype is None else out_dtype
+    _need(out_dtype in _DT, f"{name}: out_dtype must be bfloat16, float16 or float32")
+    _need_cuda(name, rows, perm, weights, out)
+    _one_gpu(name, rows.device, perm, weights, out)
+    rows, perm = rows.contiguous(), perm.contiguous()
+    weights = None if weights is None else weights.contiguous()
+    P, H = rows.shape
+    if out is None:
+        out = torch.empty((T, H), dtype=out_dtype, device=rows.device)
+    _need(out.shape == (T, H) and out.dtype == out_dtype and out.is_contiguous(),
+          f"{name}: out must be a contiguous [T, H] tensor of out_dtype")
+    _launch(rows.device, _lib.lib().mi_moe_combine_rows, rows.data_ptr(), _DT[rows.dtype], P, H,
+            perm.data_ptr(), _ptr(weights), T, top_k, out.data_ptr(), _DT[out_dtype])
+    return out
+
+
+def moe_combine_rows(rows: torch.Tensor, expanded_idx_to_permuted_idx: torch.Tensor,
+                     topk_weights: torch.Tensor, *, out_dtype: torch.dtype | None = None,
+                     out: torch.Tensor | None = None) -> torch.Tensor:
+    """``out[t] = sum_j topk_weights[t, j] * rows[perm[t*top_k + j]]``: ``rows``
+    (bf16, fp16 or fp32 ``[num_rows, H]``, permuted order) back in token order
+    ``[T, H]``.  Slots whose entry lies outside ``[0, num_rows)`` contribute
+    nothing.  fp32 sums in slot order, one rounding to ``out_dtype`` (the
+    rows' type by default).  ``topk_weights`` fp32 ``[T, top_k]``."""
+    _need(topk_weights.dim() == 2 and topk_weights.dtype == torch.float32 and
+          topk_weights.shape[1] >= 1, "moe_combine_rows: topk_weights must be float32 [T, top_k]")
+    T, top_k = topk_weights.shape
+    return _combine("moe_combine_rows", rows, expanded_idx_to_permuted_idx, topk_weights, T,
+                    top_k, out_dtype, out)
+
+
+def moe_permute_rows_backward(grad_rows: torch.Tensor, expanded_idx_to_permuted_idx: torch.Tensor,
+                              top_k: int, *, out_dtype: torch.dtype | None = None,
+                              out: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of :func:`moe_permute_rows` with respect to ``x``:
+    ``out[t] = sum_j grad_rows[perm[t*top_k + j]]`` over the token's slots
+    that have a row, fp32 sums, one rounding."""
+    top_k = int(top_k)
+    n = expanded_idx_to_permuted_idx.numel()
+    _need(top_k >= 1 and n % top_k == 0,
+          "moe_permute_rows_backward: expanded_idx_to_permuted_idx must hold num_tokens*top_k "
+          "entries")
+    return _combine("moe_permute_rows_backward", grad_rows, expanded_idx_to_permuted_idx, None,
+                    n // top_k, top_k, out_dtype, out)
+
+
+def moe_combine_rows_backward(grad_out: torch.Tensor, rows: torch.Tensor,
+                              expanded_idx_to_permuted_idx: torch.Tensor,
+                              topk_weights: torch.Tensor, *,
+                              permuted_idx_to_expanded_idx: torch.Tensor | None = None,
+                              with_weights: bool = True,
+                              grad_rows: torch.Tensor | None = None,
+                              grad_weights: torch.Tensor | None = None):
+    """``(grad_rows, grad_weights)`` of :func:`moe_combine_rows` for ``grad_out`` ``[T, H]``:
+    ``grad_rows[perm[t*top_k + j]] = topk_weights[t, j] * grad_out[t]`` in the rows'
+    type and ``grad_weights[t, j] = <rows[perm[t*top_k + j]], grad_out[t]>`` in
+    fp32 (0 for a slot without a row; None with ``with_weights=False``, which
+    does not read the rows).
+
+    With ``permuted_idx_to_expanded_idx`` (the inverse that
+    :func:`moe_route_permutation` returns, one entry per row) the call writes
+    every row, zeros where no slot points.  Without it rows no slot points at
+    are zero in a fresh ``grad_rows`` and untouched in a caller's.  Each row may
+    be pointed at once.
+    """
+    name = "moe_combine_rows_backward"
+    _need(rows.dim() == 2 and rows.dtype in _DT,
+          f"{name}: rows must be [num_rows, H] bf16, fp16 or fp32")
+    _need(topk_weights.dim() == 2 and topk_weights.dtype == torch.float32 and
+          topk_weights.shape[1] >= 1, f"{name}: topk_weights must be float32 [T, top_k]")
+    T, top_k = topk_weights.shape
+    P, H = rows.shape
+    _need(grad_out.shape == (T, H) and grad_out.dtype in _DT,
+          f"{name}: grad_out must be [T, H] bf16, fp16 or fp32")
+    perm, inverse = expanded_idx_to_permuted_idx, permuted_idx_to_expanded_idx
+    _need(perm.dtype == torch.int32 and perm.numel() == T * top_k,
+          f"{name}: expanded_idx_to_permuted_idx must be int32 [num_tokens*top_k]")
+    _need(inverse is None or (inverse.dtype == torch.int32 and inverse.numel() == P),
+          f"{name}: permuted_idx_to_expanded_idx must be int32 [num_rows]")
+    _need(with_weights or grad_weights is None, f"{name}: grad_weights needs with_weights")
+    _need_cuda(name, grad_out, rows, perm, topk_weights, inverse, grad_rows, grad_weights)
+    _one_gpu(name, rows.device, grad_out, perm, topk_weights, inverse, grad_rows, grad_weights)
+    grad_out, rows, perm, topk_weights = (t.contiguous() for t in
+                                          (grad_out, rows, perm, topk_weights))
+    inverse = None if inverse is None else inverse.contiguous()
+    if grad_rows is None:
+        grad_rows = (torch.zeros_like if inverse is None else torch.empty_like)(rows)
+    if grad_weights is None and with_weights:
+        grad_weights = torch.empty_like(topk_weights)
+    _need(grad_rows.shape == rows.shape and grad_rows.dtype == rows.dtype and
+          grad_rows.is_contiguous(), f"{name}: grad_rows must be contiguous like rows")
+    _need(grad_weights is None or (grad_weights.shape == topk_weights.shape and
+                                   grad_weights.dtype == torch.float32 and
+                                   grad_weights.is_contiguous()),
+          f"{name}: grad_weights must be contiguous float32 [T, top_k]")
+    _launch(rows.device, _lib.lib().mi_moe_combine_rows_backward, grad_out.data_ptr(),
+            _DT[grad_out.dtype], rows.data_ptr(), _DT[rows.dtype], P, H, perm.data_ptr(),
+            _ptr(inverse), topk_weights.data_ptr(), T, top_k, grad_rows.data_ptr(),
+            _ptr(grad_weights))
+    return grad_rows, grad_weights

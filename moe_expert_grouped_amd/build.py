@@ -19,7 +19,7 @@ LIB = os.path.join(PKG, "libmi_moe.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["errors.cpp", "grouped_mm.hip", "lora_delta.hip", "nvfp4_lora.hip", "permute.hip",
-           "fp4_quantize.hip"]
+           "fp4_quantize.hip", "fp8_quantize.hip", "fp8_gemm.hip", "combine.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",
