@@ -39,9 +39,11 @@ constexpr uint32_t F8_OUT = 0x80000000u;
 
 __device__ __forceinline__ lds_void_ptr f8_lds(void* p) { return (lds_void_ptr)(p); }
 
-// Chunk c (16 bytes) of LDS row R sits at slot c ^ f8_swz(R): the 16 rows of a
-// fragment read then cover all 64 banks.  Depends on R % 32 only.
-__device__ __forceinline__ int f8_swz(int row) { return (row & 7) ^ ((row >> 3) & 3); }
+// Chunk c (16 bytes) of LDS row R sits at slot c ^ f8_swz(R): the even and the odd
+// ones of 16 rows take 8 different slots each, so the 16 rows of a fragment read
+// cover all 64 banks.  Depends on R % 16 only: every 16-row block is read at the
+// same offsets.
+__device__ __forceinline__ int f8_swz(int row) { return (row & 7) ^ ((row >> 3) & 1); }
 
 struct F8Args {
   const uint8_t* a;        // [m_rows, k]
@@ -162,18 +164,24 @@ __device__ __forceinline__ f32x4 f8_block(const F8Frag<true>& b, const F8Frag<tr
 // `rows` (1..BM) of the tile belong to the group.
 //
 // Staging: 8 rows of 128 bytes per DMA instruction straight into LDS, two
-// stages; the loads of step kt+1 are issued at the start of step kt and waited
-// for at its barrier.  Rows past the group or past n, and 16-byte chunks past
-// k, load as zeros.  a's scales of four steps (16 bytes a row) go into one LDS
-// buffer: it is refilled during step 4g+3, whose scales were read a step
-// before.  b's scales of 64 steps sit in one register, a lane each.
+// stages.  Rows past the group or past n, and 16-byte chunks past k, load as
+// zeros.  a's scales of four steps (16 bytes a row) go into one of two small
+// LDS buffers, b's of 64 steps sit in one register, a lane each.
+//
+// A step is FM regions of one 16-row block of a each.  A region reads the
+// fragment of the region after the next and issues its FN MFMAs; beside each the
+// result of the last but one is added to the sums, so nothing is waited for
+// where it is made.  The step's one barrier stands before its last two regions,
+// whose operands are in registers by then: behind it the stage is free for the
+// loads of step kt+2, and the next stage, loaded a step ago, is complete, so the
+// last regions read the next step's first fragments while their MFMAs run.
 template <int WM, int WN, int FM, int FN, typename OutT>
-__device__ __forceinline__ void f8_tile(const F8Args& p, uint8_t* s0, uint8_t* s1, float* ssa,
-                                        int e, int m0, int rows, int n0) {
+__device__ __forceinline__ void f8_tile(const F8Args& p, uint8_t* s0, uint8_t* s1, float* ssa0,
+                                        float* ssa1, int e, int m0, int rows, int n0) {
   constexpr int NW = WM * WN, BM = 16 * FM * WM, BN = 16 * FN * WN;
   constexpr int NIA = BM / 8 / NW, NIB = BN / 8 / NW;  // DMA instructions per wavefront
   static_assert(NW % 4 == 0 && NIA * 8 * NW == BM && NIB * 8 * NW == BN, "tile");
-  static_assert(BM % 64 == 0 && BM / 64 <= NW && 128 % (16 * FN) == 0, "tile");
+  static_assert(BM % 64 == 0 && BM / 64 <= NW && 128 % (16 * FN) == 0 && FM >= 2 && FN >= 2, "tile");
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
@@ -192,7 +200,7 @@ __device__ __forceinline__ void f8_tile(const F8Args& p, uint8_t* s0, uint8_t* s
 
   // DMA instruction i fills LDS rows 8 (NW i + wave) ..: lane l takes row l / 8
   // of them and chunk (l % 8) ^ f8_swz(row)
-  const int lr = lane >> 3, chunk = (lane & 7) ^ lr ^ (wave & 3);
+  const int lr = lane >> 3, chunk = (lane & 7) ^ lr ^ (wave & 1);
   uint32_t va[NIA], vb[NIB];
 #pragma unroll
   for (int i = 0; i < NIA; ++i) {
@@ -205,10 +213,12 @@ __device__ __forceinline__ void f8_tile(const F8Args& p, uint8_t* s0, uint8_t* s
     vb[i] = row < cols ? static_cast<uint32_t>(row) * k + chunk * 16 : F8_OUT;
   }
   const uint32_t tail = (KT - 1) * F8_BK + chunk * 16 < k ? 0u : F8_OUT;
+  // A step past the last loads zeros (its lane offsets are out of range): the
+  // steps stay free of branches, which keep the compiler from moving a region's
+  // additions into the next step.
   auto dma = [&](uint8_t* st, int kt) {
-    if (kt >= KT) return;
-    const uint32_t so = static_cast<uint32_t>(kt) * F8_BK;
-    const uint32_t drop = kt == KT - 1 ? tail : 0u;
+    const uint32_t so = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(min(kt, KT - 1)) * F8_BK);
+    const uint32_t drop = kt < KT - 1 ? 0u : kt == KT - 1 ? tail : F8_OUT;
 #pragma unroll
     for (int i = 0; i < NIA; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, f8_lds(st + (NW * i + wave) * 1024), 16,
@@ -218,25 +228,27 @@ __device__ __forceinline__ void f8_tile(const F8Args& p, uint8_t* s0, uint8_t* s
       __builtin_amdgcn_raw_ptr_buffer_load_lds(br, f8_lds(st + (BM + 8 * (NW * i + wave)) * 128),
                                                16, vb[i] | drop, so, 0, 0);
   };
-  const int srow = wave * 64 + lane;
+  // 64 rows' scales per wavefront; wavefronts past the tile's rows load the same again
+  const int swave = wave % (BM / 64), srow = swave * 64 + lane;
   const uint32_t vsa = srow < rows ? static_cast<uint32_t>(srow) * p.sc * 4 : F8_OUT;
-  auto dma_scales = [&](int kt) {  // kt a multiple of 4
-    if (kt < KT && wave < BM / 64)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(sar, f8_lds(ssa + wave * 256), 16, vsa, kt * 4, 0,
-                                               0);
+  auto dma_scales = [&](float* buf, int kt) {  // kt a multiple of 4
+    const uint32_t so = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(min(kt, p.sc - 4)) * 4);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(sar, f8_lds(buf + swave * 256), 16, vsa, so, 0, 0);
   };
 
-  // fragments: lane (r, g) holds chunks g and g + 4 of row r of a 16-row block;
-  // a and b use the same chunks, so the order of k inside the MFMA is theirs
+  // fragments: lane (r, g) holds chunks c and c + 4 of row r of a 16-row block,
+  // c = 0, 2, 1, 3 for g = 0 .. 3; a and b use the same chunks, so the order of k
+  // inside the MFMA is theirs.  The LDS serves lanes l and l + 32 together: their
+  // chunks have to differ in the lowest bit, which 0, 1, 2, 3 does not give (every
+  // read then took twice its 4 cycles: 323 against 260 us at m 4096, n = k = 8192)
   const int r = lane & 15, g = lane >> 4;
-  uint32_t fo[2][2];  // [block parity][chunk]
+  uint32_t fo[2];
 #pragma unroll
-  for (int o = 0; o < 2; ++o)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) fo[o][h] = r * 128 + (((g + 4 * h) ^ f8_swz(16 * o + r)) << 4);
+  for (int h = 0; h < 2; ++h)
+    fo[h] = r * 128 + (((((g & 1) << 1) | (g >> 1)) + 4 * h) ^ f8_swz(r)) * 16;
   auto frag = [&](const uint8_t* st, int blk) {
-    const u32x4 x = *reinterpret_cast<const u32x4*>(st + blk * 2048 + fo[blk & 1][0]);
-    const u32x4 y = *reinterpret_cast<const u32x4*>(st + blk * 2048 + fo[blk & 1][1]);
+    const u32x4 x = *reinterpret_cast<const u32x4*>(st + blk * 2048 + fo[0]);
+    const u32x4 y = *reinterpret_cast<const u32x4*>(st + blk * 2048 + fo[1]);
     return i32x8{(int)x[0], (int)x[1], (int)x[2], (int)x[3],
                  (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
   };
@@ -247,52 +259,90 @@ __device__ __forceinline__ void f8_tile(const F8Args& p, uint8_t* s0, uint8_t* s
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  const int srd = (wm * FM * 16 + r) * 4;  // this lane's row of the scale buffer
-  float sbv = 0.f;
-  float sk[FM];  // the scales of step 4g+3, read a step before
-  auto step = [&](auto S, const uint8_t* st, uint8_t* nx, int kt) {
+  using Frag = F8Frag<sizeof(OutT) == 4>;
+  const int ablk = wm * FM, bblk = BM / 16 + wn * FN;
+  const int srd = (wm * FM * 16 + r) * 4;  // this lane's row of a scale buffer
+  float sbv = 0.f;                         // b's scales of 64 steps
+  i32x8 fb[FN];                            // b's fragments of the step
+  i32x8 fa0, fa1;                          // a's of the next two regions,
+  float sa0, sa1;                          // and their scales
+  float f = 0.f;                           // the factor of the last region
+  f32x4 d0 = {0.f, 0.f, 0.f, 0.f}, d1 = d0;  // the last two results, not yet added
+
+  auto step = [&](auto S, uint8_t* st, uint8_t* nx, int kt) {
     constexpr int s = decltype(S)::value;
-    dma(nx, kt + 1);
-    if constexpr (s == 3) dma_scales(kt + 1);
+    float* const sc = s < 4 ? ssa0 : ssa1;
+    float* const sc_nx = s < 4 ? ssa1 : ssa0;
     const float sb = __builtin_bit_cast(
         float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sbv), kt & 63));
-    using Frag = F8Frag<sizeof(OutT) == 4>;
-    Frag fb[FN];
+    Frag fbx[FN];
 #pragma unroll
-    for (int j = 0; j < FN; ++j) fb[j] = Frag(frag(st, BM / 16 + wn * FN + j));
-    float f[FM];
-#pragma unroll
-    for (int i = 0; i < FM; ++i) f[i] = (s == 3 ? sk[i] : ssa[srd + 64 * i + s]) * sb;
-    if constexpr (s == 2) {
-#pragma unroll
-      for (int i = 0; i < FM; ++i) sk[i] = ssa[srd + 64 * i + 3];
-    }
+    for (int j = 0; j < FN; ++j) fbx[j] = Frag(fb[j]);
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-      const Frag fa(frag(st, wm * FM + i));
+      if (i == FM - 2) {
+        __syncthreads();
+        dma(st, kt + 2);
+        if constexpr ((s & 3) == 0) dma_scales(sc_nx, kt + 4);
+      }
+      const Frag fax(fa0);
+      const float f_prev = f;
+      f = sa0 * sb;
+      fa0 = fa1;
+      sa0 = sa1;
+      if (i < FM - 2) {
+        fa1 = frag(st, ablk + i + 2);
+        sa1 = sc[srd + 64 * (i + 2) + (s & 3)];
+      } else {
+        fa1 = frag(nx, ablk + i + 2 - FM);
+        sa1 = (s & 3) < 3 ? sc[srd + 64 * (i + 2 - FM) + (s & 3) + 1]
+                          : sc_nx[srd + 64 * (i + 2 - FM)];
+      }
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
-        const f32x4 d = f8_block(fb[j], fa);
+        const f32x4 d2 = f8_block(fbx[j], fax);
+        __builtin_amdgcn_sched_barrier(0);
+        if (i == FM - 1) fb[j] = frag(nx, bblk + j);
+        f32x4& o = acc[j >= 2 ? i : (i + FM - 1) % FM][(j + FN - 2) % FN];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) acc[i][j][q] = __builtin_fmaf(d[q], f[i], acc[i][j][q]);
+        for (int q = 0; q < 4; ++q) o[q] = __builtin_fmaf(d0[q], j >= 2 ? f : f_prev, o[q]);
+        asm volatile("" : "+v"(o));  // the sum is complete here, not later
+        d0 = d1;
+        d1 = d2;
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
-    __syncthreads();
   };
 
   dma(s0, 0);
-  dma_scales(0);
+  dma_scales(ssa0, 0);
   __syncthreads();
-  using std::integral_constant;
-  for (int kt = 0; kt < KT; kt += 4) {
+  dma(s1, 1);
+  fa0 = frag(s0, ablk);
+  fa1 = frag(s0, ablk + 1);
+  sa0 = ssa0[srd];
+  sa1 = ssa0[srd + 64];
+#pragma unroll
+  for (int j = 0; j < FN; ++j) fb[j] = frag(s0, bblk + j);
+  for (int kt = 0; kt < KT; kt += 8) {
     if ((kt & 63) == 0) sbv = sbp[min(kt + lane, p.sc - 1)];
-    step(integral_constant<int, 0>{}, s0, s1, kt);
-    if (kt + 1 >= KT) break;
-    step(integral_constant<int, 1>{}, s1, s0, kt + 1);
-    if (kt + 2 >= KT) break;
-    step(integral_constant<int, 2>{}, s0, s1, kt + 2);
-    if (kt + 3 >= KT) break;
-    step(integral_constant<int, 3>{}, s1, s0, kt + 3);
+#define F8_STEP(S_, ST_, NX_)                                       \
+  step(std::integral_constant<int, S_>{}, ST_, NX_, kt + S_);        \
+  if (kt + S_ + 1 >= KT) break;
+    F8_STEP(0, s0, s1)
+    F8_STEP(1, s1, s0)
+    F8_STEP(2, s0, s1)
+    F8_STEP(3, s1, s0)
+    F8_STEP(4, s0, s1)
+    F8_STEP(5, s1, s0)
+    F8_STEP(6, s0, s1)
+    F8_STEP(7, s1, s0)
+#undef F8_STEP
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    acc[FM - 1][FN - 2][q] = __builtin_fmaf(d0[q], f, acc[FM - 1][FN - 2][q]);
+    acc[FM - 1][FN - 1][q] = __builtin_fmaf(d1[q], f, acc[FM - 1][FN - 1][q]);
   }
 
   // acc[i][j][q]: row (wm FM + i) 16 + r, column (wn FN + j) 16 + 4 g + q
@@ -313,12 +363,16 @@ __device__ __forceinline__ void f8_tile(const F8Args& p, uint8_t* s0, uint8_t* s
   }
 }
 
+// two wavefronts per SIMD: 256 registers each, all of them usable by the VALU,
+// which adds the MFMAs' results
 template <int WM, int WN, int FM, int FN, typename OutT>
-__global__ __launch_bounds__(64 * WM * WN) void f8_mm_kernel(F8Args p) {
+__global__ __launch_bounds__(64 * WM * WN)
+    __attribute__((amdgpu_waves_per_eu(2, 2))) void f8_mm_kernel(F8Args p) {
   constexpr int BM = 16 * FM * WM, BN = 16 * FN * WN;
   __shared__ __attribute__((aligned(16))) uint8_t s0[(BM + BN) * F8_BK];
   __shared__ __attribute__((aligned(16))) uint8_t s1[(BM + BN) * F8_BK];
-  __shared__ __attribute__((aligned(16))) float ssa[BM * 4];
+  __shared__ __attribute__((aligned(16))) float ssa0[BM * 4];
+  __shared__ __attribute__((aligned(16))) float ssa1[BM * 4];
   const int nt = (p.n + BN - 1) / BN;
   const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
   int e = 0, m0, rows, mt, ni;
@@ -348,7 +402,7 @@ __global__ __launch_bounds__(64 * WM * WN) void f8_mm_kernel(F8Args p) {
     // number where m_indptr decreases
     rows = min(min(max(p.m_indptr[e + 1], s_row0[e]), p.m_rows) - m0, BM);
   }
-  f8_tile<WM, WN, FM, FN, OutT>(p, s0, s1, ssa, __builtin_amdgcn_readfirstlane(e),
+  f8_tile<WM, WN, FM, FN, OutT>(p, s0, s1, ssa0, ssa1, __builtin_amdgcn_readfirstlane(e),
                                 __builtin_amdgcn_readfirstlane(m0),
                                 __builtin_amdgcn_readfirstlane(rows),
                                 __builtin_amdgcn_readfirstlane(ni * BN));
@@ -371,7 +425,18 @@ mi_status f8_launch(const F8Args& p, hipStream_t stream, const char* what) {
 
 template <typename OutT>
 mi_status f8_dispatch(const F8Args& p, hipStream_t s, const char* what) {
-  return f8_launch<2, 2, 4, 4, OutT>(p, s, what);
+  // fp32 outputs: the fp16 fragments take twice the registers, 128 x 64 tiles
+  if constexpr (sizeof(OutT) == 4) {
+    return f8_launch<2, 2, 4, 2, OutT>(p, s, what);
+  } else {
+    // 256 x 256 tiles halve the bytes each MFMA needs (m 4096, n = k = 8192: 243
+    // against 288 us), but only where they fill the chip: m 1024 has 128 of them,
+    // 90 against 69 us.  Groups' rows are known on the device only: the average.
+    const long rows = p.m_rows / p.E;
+    const long tiles = (rows + 255) / 256 * ((p.n + 255) / 256) * p.E;
+    if (rows >= 192 && tiles >= 192) return f8_launch<2, 4, 8, 4, OutT>(p, s, what);
+    return f8_launch<2, 2, 4, 4, OutT>(p, s, what);
+  }
 }
 
 mi_status f8_run(const F8Args& p, int64_t m_rows, int64_t k, int64_t n, int64_t batch,
