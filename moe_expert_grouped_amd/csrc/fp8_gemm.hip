@@ -57,59 +57,89 @@ struct F8Args {
   int nb;                  // scale rows of one b: ceil(n / 128)
 };
 
-// Wavefront 0 walks m_indptr: first row (s_row0, clamped) and first tile
-// (s_t0) of every expert; entry E holds the ends.
-template <int BM>
-__device__ __forceinline__ void f8_walk(const int32_t* __restrict__ m_indptr, int m_rows, int E,
-                                        int* s_t0, int* s_row0) {
-  const int lane = threadIdx.x & 63;
-  const int per = (E + 63) / 64;
-  const int e0 = lane * per;
-  int c = 0;
-  for (int e = e0; e < min(e0 + per, E); ++e) {
-    const int s = min(max(m_indptr[e], 0), m_rows);
-    const int t = min(max(m_indptr[e + 1], s), m_rows);
-    s_row0[e] = s;
-    c += (t - s + BM - 1) / BM;
-    s_t0[e] = c;  // tiles of this lane's experts up to e; the lanes before are added below
-  }
-  int incl = c;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int v = __shfl_up(incl, off, 64);
-    if (lane >= off) incl += v;
-  }
-  int prev = incl - c;
-  for (int e = e0; e < min(e0 + per, E); ++e) {
-    const int upto = s_t0[e] + incl - c;
-    s_t0[e] = prev;
-    prev = upto;
-  }
-  if (lane == 63) {
-    s_t0[E] = incl;
-    s_row0[E] = min(max(m_indptr[E], 0), m_rows);
-  }
-}
-
-// the last e with pre[e] <= mt
-__device__ __forceinline__ int f8_owner(const int* pre, int E, int mt) {
-  int lo = 0, hi = E;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (pre[mid] <= mt) lo = mid; else hi = mid;
-  }
-  return lo;
+// inclusive sum over the wavefront's lanes
+__device__ __forceinline__ uint32_t f8_scan(uint32_t v) {
+#define F8_DPP(CTRL_, ROWS_) \
+  v += __builtin_amdgcn_update_dpp(0, v, CTRL_, ROWS_, 0xf, true);
+  F8_DPP(0x111, 0xf)  // row_shr 1, 2, 4, 8: within 16 lanes
+  F8_DPP(0x112, 0xf)
+  F8_DPP(0x114, 0xf)
+  F8_DPP(0x118, 0xf)
+  F8_DPP(0x142, 0xa)  // row_bcast 15: rows 0, 2 into 1, 3
+  F8_DPP(0x143, 0xc)  // row_bcast 31: the lower half into the upper
+#undef F8_DPP
+  return v;
 }
 
 // m-tile and n-panel of the L-th tile: F8_GROUP_M m-tiles sweep the n-panels together
-__device__ __forceinline__ void f8_order(long L, int count, int nt, int& mt, int& ni) {
-  const long span = static_cast<long>(F8_GROUP_M) * nt;
-  const int grp = static_cast<int>(L / span);
-  const int first = grp * F8_GROUP_M;
-  const int gsize = min(count - first, F8_GROUP_M);
-  const int in_grp = static_cast<int>(L - static_cast<long>(grp) * span);
+__device__ __forceinline__ void f8_order(uint32_t L, int count, int nt, int& mt, int& ni) {
+  const uint32_t span = F8_GROUP_M * nt;
+  const uint32_t grp = L / span;
+  const uint32_t first = grp * F8_GROUP_M;
+  const uint32_t gsize = min(count - first, static_cast<uint32_t>(F8_GROUP_M));
+  const uint32_t in_grp = L - grp * span;
   mt = first + in_grp % gsize;
   ni = in_grp / gsize;
+}
+
+struct F8Tile {
+  int e, m0, rows, n0;  // rows == 0: this workgroup has no tile
+};
+
+// The tile of BM rows and BN columns of this workgroup.  The grid is an upper
+// bound on the tiles; they are dealt in 8 contiguous runs, one per XCD (workgroup
+// ids go to the XCDs in turn).  Every wavefront reads m_indptr itself: a lane
+// has ceil(E / 64) experts, and where that is more than one, a second round
+// resolves the lane's.
+template <int BM, int BN>
+__device__ __forceinline__ F8Tile f8_find(const F8Args& p) {
+  const int lane = threadIdx.x & 63;
+  const int per = (p.E + 63) / 64;
+  const uint32_t nt = (p.n + BN - 1) / BN;
+  const uint32_t xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
+  auto bounds = [&](int e, int& s, int& t) {  // rows of expert e, clamped
+    if (p.m_indptr == nullptr) {
+      s = 0;
+      t = p.m_rows;
+    } else {
+      s = min(max(p.m_indptr[e], 0), p.m_rows);
+      t = min(max(p.m_indptr[e + 1], s), p.m_rows);
+    }
+  };
+  auto tiles = [](int s, int t) { return static_cast<uint32_t>(t - s + BM - 1) / BM; };
+  F8Tile f{0, 0, 0, 0};
+  uint32_t cnt = 0;
+  int s = 0, t = 0;
+  for (int e = lane * per; e < min((lane + 1) * per, p.E); ++e) {
+    bounds(e, s, t);
+    cnt += tiles(s, t);
+  }
+  uint32_t upto = f8_scan(cnt), before = upto - cnt;  // this lane's place in the list of tiles
+  const uint32_t count = __builtin_amdgcn_readlane(upto, 63);
+  const uint32_t total = count * nt, run = (total + 7) / 8, L = xcd * run + slot;
+  if (slot >= run || L >= total) return f;
+  int mt, ni;
+  f8_order(L, count, nt, mt, ni);
+  int owner = __builtin_popcountll(__ballot(upto <= static_cast<uint32_t>(mt)));
+  f.e = owner * per;
+  if (per > 1) {
+    const uint32_t base = __builtin_amdgcn_readlane(before, owner);
+    const int e = f.e + lane;
+    s = t = 0;
+    if (lane < per && e < p.E) bounds(e, s, t);
+    cnt = tiles(s, t);
+    upto = base + f8_scan(cnt);
+    before = upto - cnt;
+    owner = __builtin_popcountll(__ballot(upto <= static_cast<uint32_t>(mt)));
+    f.e += owner;
+  }
+  const int s_own = __builtin_amdgcn_readlane(s, owner), t_own = __builtin_amdgcn_readlane(t, owner);
+  f.m0 = s_own + (mt - static_cast<int>(__builtin_amdgcn_readlane(before, owner))) * BM;
+  f.n0 = ni * BN;
+  // in [s_own, t_own) where m_indptr is what it has to be; the counts of groups
+  // that overlap may pass 32 bits
+  f.rows = f.m0 >= s_own && f.m0 < t_own ? min(t_own - f.m0, BM) : 0;
+  return f;
 }
 
 // four consecutive outputs of one row, rounded once to nearest even; an offset
@@ -160,10 +190,28 @@ __device__ __forceinline__ f32x4 f8_block(const F8Frag<true>& b, const F8Frag<tr
   return d;
 }
 
+// at most N of this wavefront's loads are outstanding, its LDS reads have
+// returned, and every wavefront is here
+template <int N>
+__device__ __forceinline__ void f8_wait_barrier() {
+  // no access may move across, in the compiler either
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));  // vmcnt(N) lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
+}
+
+// the LDS rows of one step: the tile's rows of a, and of b
+struct F8Stage {
+  uint8_t *a, *b;
+};
+
 // One tile of BM = 16 FM WM rows and BN = 16 FN WN columns; WM * WN wavefronts.
 // `rows` (1..BM) of the tile belong to the group.
 //
-// Staging: 8 rows of 128 bytes per DMA instruction straight into LDS, two
+// Staging: 8 rows of 128 bytes per DMA instruction straight into LDS, NST
 // stages.  Rows past the group or past n, and 16-byte chunks past k, load as
 // zeros.  a's scales of four steps (16 bytes a row) go into one of two small
 // LDS buffers, b's of 64 steps sit in one register, a lane each.
@@ -173,13 +221,19 @@ __device__ __forceinline__ f32x4 f8_block(const F8Frag<true>& b, const F8Frag<tr
 // result of the last but one is added to the sums, so nothing is waited for
 // where it is made.  The step's one barrier stands before its last two regions,
 // whose operands are in registers by then: behind it the stage is free for the
-// loads of step kt+2, and the next stage, loaded a step ago, is complete, so the
-// last regions read the next step's first fragments while their MFMAs run.
-template <int WM, int WN, int FM, int FN, typename OutT>
-__device__ __forceinline__ void f8_tile(const F8Args& p, uint8_t* s0, uint8_t* s1, float* ssa0,
-                                        float* ssa1, int e, int m0, int rows, int n0) {
+// loads of step kt+NST, and the next stage is complete (the wait leaves the loads
+// of the later ones in flight), so the last regions read the next step's first
+// fragments while their MFMAs run.
+template <int WM, int WN, int FM, int FN, int NST, typename OutT>
+__device__ __forceinline__ void f8_tile(const F8Args& p, F8Stage s0, F8Stage s1, F8Stage s2,
+                                        F8Stage s3, float* ssa0, float* ssa1, const F8Tile& t) {
+  const int e = t.e, m0 = t.m0, rows = t.rows, n0 = t.n0;
   constexpr int NW = WM * WN, BM = 16 * FM * WM, BN = 16 * FN * WN;
   constexpr int NIA = BM / 8 / NW, NIB = BN / 8 / NW;  // DMA instructions per wavefront
+  // the loads of the stages after the next may be in flight at a step's barrier
+  // (the scales' among them, which are read two steps after their load at least)
+  constexpr int FLY = (NST - 2) * (NIA + NIB);
+  static_assert((NST == 2 || NST == 4) && FLY < 64, "stages");
   static_assert(NW % 4 == 0 && NIA * 8 * NW == BM && NIB * 8 * NW == BN, "tile");
   static_assert(BM % 64 == 0 && BM / 64 <= NW && 128 % (16 * FN) == 0 && FM >= 2 && FN >= 2, "tile");
   const int tid = threadIdx.x, lane = tid & 63;
@@ -216,17 +270,17 @@ __device__ __forceinline__ void f8_tile(const F8Args& p, uint8_t* s0, uint8_t* s
   // A step past the last loads zeros (its lane offsets are out of range): the
   // steps stay free of branches, which keep the compiler from moving a region's
   // additions into the next step.
-  auto dma = [&](uint8_t* st, int kt) {
+  auto dma = [&](const F8Stage& st, int kt) {
     const uint32_t so = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(min(kt, KT - 1)) * F8_BK);
     const uint32_t drop = kt < KT - 1 ? 0u : kt == KT - 1 ? tail : F8_OUT;
 #pragma unroll
     for (int i = 0; i < NIA; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, f8_lds(st + (NW * i + wave) * 1024), 16,
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, f8_lds(st.a + (NW * i + wave) * 1024), 16,
                                                va[i] | drop, so, 0, 0);
 #pragma unroll
     for (int i = 0; i < NIB; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(br, f8_lds(st + (BM + 8 * (NW * i + wave)) * 128),
-                                               16, vb[i] | drop, so, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(br, f8_lds(st.b + (NW * i + wave) * 1024), 16,
+                                               vb[i] | drop, so, 0, 0);
   };
   // 64 rows' scales per wavefront; wavefronts past the tile's rows load the same again
   const int swave = wave % (BM / 64), srow = swave * 64 + lane;
@@ -260,7 +314,7 @@ __device__ __forceinline__ void f8_tile(const F8Args& p, uint8_t* s0, uint8_t* s
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   using Frag = F8Frag<sizeof(OutT) == 4>;
-  const int ablk = wm * FM, bblk = BM / 16 + wn * FN;
+  const int ablk = wm * FM, bblk = wn * FN;
   const int srd = (wm * FM * 16 + r) * 4;  // this lane's row of a scale buffer
   float sbv = 0.f;                         // b's scales of 64 steps
   i32x8 fb[FN];                            // b's fragments of the step
@@ -269,7 +323,7 @@ __device__ __forceinline__ void f8_tile(const F8Args& p, uint8_t* s0, uint8_t* s
   float f = 0.f;                           // the factor of the last region
   f32x4 d0 = {0.f, 0.f, 0.f, 0.f}, d1 = d0;  // the last two results, not yet added
 
-  auto step = [&](auto S, uint8_t* st, uint8_t* nx, int kt) {
+  auto step = [&](auto S, const F8Stage& st, const F8Stage& nx, int kt) {
     constexpr int s = decltype(S)::value;
     float* const sc = s < 4 ? ssa0 : ssa1;
     float* const sc_nx = s < 4 ? ssa1 : ssa0;
@@ -281,8 +335,8 @@ __device__ __forceinline__ void f8_tile(const F8Args& p, uint8_t* s0, uint8_t* s
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
       if (i == FM - 2) {
-        __syncthreads();
-        dma(st, kt + 2);
+        f8_wait_barrier<FLY>();
+        dma(st, kt + NST);
         if constexpr ((s & 3) == 0) dma_scales(sc_nx, kt + 4);
       }
       const Frag fax(fa0);
@@ -291,10 +345,10 @@ __device__ __forceinline__ void f8_tile(const F8Args& p, uint8_t* s0, uint8_t* s
       fa0 = fa1;
       sa0 = sa1;
       if (i < FM - 2) {
-        fa1 = frag(st, ablk + i + 2);
+        fa1 = frag(st.a, ablk + i + 2);
         sa1 = sc[srd + 64 * (i + 2) + (s & 3)];
       } else {
-        fa1 = frag(nx, ablk + i + 2 - FM);
+        fa1 = frag(nx.a, ablk + i + 2 - FM);
         sa1 = (s & 3) < 3 ? sc[srd + 64 * (i + 2 - FM) + (s & 3) + 1]
                           : sc_nx[srd + 64 * (i + 2 - FM)];
       }
@@ -302,7 +356,7 @@ __device__ __forceinline__ void f8_tile(const F8Args& p, uint8_t* s0, uint8_t* s
       for (int j = 0; j < FN; ++j) {
         const f32x4 d2 = f8_block(fbx[j], fax);
         __builtin_amdgcn_sched_barrier(0);
-        if (i == FM - 1) fb[j] = frag(nx, bblk + j);
+        if (i == FM - 1) fb[j] = frag(nx.b, bblk + j);
         f32x4& o = acc[j >= 2 ? i : (i + FM - 1) % FM][(j + FN - 2) % FN];
 #pragma unroll
         for (int q = 0; q < 4; ++q) o[q] = __builtin_fmaf(d0[q], j >= 2 ? f : f_prev, o[q]);
@@ -316,126 +370,332 @@ __device__ __forceinline__ void f8_tile(const F8Args& p, uint8_t* s0, uint8_t* s
 
   dma(s0, 0);
   dma_scales(ssa0, 0);
-  __syncthreads();
-  dma(s1, 1);
-  fa0 = frag(s0, ablk);
-  fa1 = frag(s0, ablk + 1);
+  if constexpr (NST == 4) {
+    dma(s1, 1);
+    dma(s2, 2);
+  }
+  f8_wait_barrier<FLY>();
+  dma(NST == 4 ? s3 : s1, NST - 1);
+  fa0 = frag(s0.a, ablk);
+  fa1 = frag(s0.a, ablk + 1);
   sa0 = ssa0[srd];
   sa1 = ssa0[srd + 64];
 #pragma unroll
-  for (int j = 0; j < FN; ++j) fb[j] = frag(s0, bblk + j);
+  for (int j = 0; j < FN; ++j) fb[j] = frag(s0.b, bblk + j);
   for (int kt = 0; kt < KT; kt += 8) {
     if ((kt & 63) == 0) sbv = sbp[min(kt + lane, p.sc - 1)];
 #define F8_STEP(S_, ST_, NX_)                                       \
   step(std::integral_constant<int, S_>{}, ST_, NX_, kt + S_);        \
   if (kt + S_ + 1 >= KT) break;
     F8_STEP(0, s0, s1)
-    F8_STEP(1, s1, s0)
-    F8_STEP(2, s0, s1)
-    F8_STEP(3, s1, s0)
+    F8_STEP(1, s1, NST == 4 ? s2 : s0)
+    F8_STEP(2, NST == 4 ? s2 : s0, NST == 4 ? s3 : s1)
+    F8_STEP(3, NST == 4 ? s3 : s1, s0)
     F8_STEP(4, s0, s1)
-    F8_STEP(5, s1, s0)
-    F8_STEP(6, s0, s1)
-    F8_STEP(7, s1, s0)
+    F8_STEP(5, s1, NST == 4 ? s2 : s0)
+    F8_STEP(6, NST == 4 ? s2 : s0, NST == 4 ? s3 : s1)
+    F8_STEP(7, NST == 4 ? s3 : s1, s0)
 #undef F8_STEP
   }
+  // the loads of the steps past the last write (zeros) to LDS: not after this
+  // workgroup's end
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     acc[FM - 1][FN - 2][q] = __builtin_fmaf(d0[q], f, acc[FM - 1][FN - 2][q]);
     acc[FM - 1][FN - 1][q] = __builtin_fmaf(d1[q], f, acc[FM - 1][FN - 1][q]);
   }
 
-  // acc[i][j][q]: row (wm FM + i) 16 + r, column (wn FN + j) 16 + 4 g + q
-  constexpr int ES = sizeof(OutT);
+  // acc[i][j][q]: row (wm FM + i) 16 + r, column (wn FN + j) 16 + 4 g + q.  The
+  // wavefront's outputs go through its own part of the stages (free after the
+  // barrier) so that it stores whole runs of RB bytes of a row, 16 bytes a lane,
+  // instead of 8 bytes from each of 64 places.  16-byte chunk c of a row sits at
+  // slot c ^ (row % CPR).  The stores are streaming (non-temporal): they cover
+  // whole 64-byte pieces at least and the outputs do not push operands out of L2
+  // (skewed experts: 817 us with 8-byte stores, 741 staged, 736 streaming).
+  constexpr int ES = sizeof(OutT), RB = 16 * FN * ES, CPR = RB / 16, REG = 16 * FM * RB;
+  static_assert(NW / 2 * REG <= (BM + BN) * F8_BK && 64 % CPR == 0, "epilogue");
+  f8_wait_barrier<0>();
+  uint8_t* const reg = (wave < NW / 2 ? s0.a : s1.a) + wave % (NW / 2) * REG;
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      const int row = 16 * i + r;
+      if constexpr (ES == 4) {
+        *reinterpret_cast<f32x4*>(reg + row * RB + ((4 * j + g) ^ (r % CPR)) * 16) = acc[i][j];
+      } else {
+        typedef OutT t4 __attribute__((ext_vector_type(4)));
+        *reinterpret_cast<t4*>(reg + row * RB + ((2 * j + (g >> 1)) ^ (r % CPR)) * 16 +
+                               (g & 1) * 8) = __builtin_convertvector(acc[i][j], t4);
+      }
+    }
   const __amdgpu_buffer_rsrc_t orsrc =
       buf_rsrc(static_cast<OutT*>(p.out) + static_cast<long>(m0) * n,
                static_cast<uint32_t>(rows) * n * ES);
+  constexpr int RPI = 64 / CPR;  // rows per store
+  const int pr = lane / CPR, pc = lane % CPR;
+  const int col = wn * 16 * FN + pc * (16 / ES);
 #pragma unroll
-  for (int i = 0; i < FM; ++i) {
-    const int row = (wm * FM + i) * 16 + r;
-#pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      const int col = (wn * FN + j) * 16 + 4 * g;
-      f8_store4<OutT>(orsrc, row < rows && col < cols
-                                 ? (static_cast<uint32_t>(row) * n + n0 + col) * ES : F8_OUT,
-                      acc[i][j]);
-    }
+  for (int r0 = 0; r0 < 16 * FM; r0 += RPI) {
+    const int lrow = r0 + pr, row = wm * FM * 16 + lrow;
+    const u32x4 v = *reinterpret_cast<const u32x4*>(reg + lrow * RB + (pc ^ (lrow % CPR)) * 16);
+    __builtin_amdgcn_raw_buffer_store_b128(
+        v, orsrc, row < rows && col < cols ? (static_cast<uint32_t>(row) * n + n0 + col) * ES : F8_OUT,
+        0, 2);
   }
 }
 
-// two wavefronts per SIMD: 256 registers each, all of them usable by the VALU,
-// which adds the MFMAs' results
-template <int WM, int WN, int FM, int FN, typename OutT>
+// Tiles of one shape.  Two wavefronts per SIMD: 256 registers each, all of them
+// usable by the VALU, which adds the MFMAs' results.
+template <int WM, int WN, int FM, int FN, int NST, typename OutT>
 __global__ __launch_bounds__(64 * WM * WN)
     __attribute__((amdgpu_waves_per_eu(2, 2))) void f8_mm_kernel(F8Args p) {
-  constexpr int BM = 16 * FM * WM, BN = 16 * FN * WN;
-  __shared__ __attribute__((aligned(16))) uint8_t s0[(BM + BN) * F8_BK];
-  __shared__ __attribute__((aligned(16))) uint8_t s1[(BM + BN) * F8_BK];
+  constexpr int BM = 16 * FM * WM, BN = 16 * FN * WN, STAGE = (BM + BN) * F8_BK;
+  // each stage its own array: the compiler then knows which loads a read waits for
+  __shared__ __attribute__((aligned(16))) uint8_t s0[STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t s1[STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t s2[NST == 4 ? STAGE : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t s3[NST == 4 ? STAGE : 16];
   __shared__ __attribute__((aligned(16))) float ssa0[BM * 4];
   __shared__ __attribute__((aligned(16))) float ssa1[BM * 4];
-  const int nt = (p.n + BN - 1) / BN;
-  const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
-  int e = 0, m0, rows, mt, ni;
-  if (p.m_indptr == nullptr) {
-    const int count = (p.m_rows + BM - 1) / BM;
-    const long total = static_cast<long>(count) * nt, run = (total + 7) / 8;
-    const long L = xcd * run + slot;
-    if (slot >= run || L >= total) return;
-    f8_order(L, count, nt, mt, ni);
-    m0 = mt * BM;
-    rows = min(p.m_rows - m0, BM);
-  } else {
-    // the walk's tables live in stage 1, which step 0 overwrites after a barrier
-    static_assert((BM + BN) * F8_BK >= 2 * (F8_MAX_EXPERTS + 1) * 4, "tables");
-    int* const s_t0 = reinterpret_cast<int*>(s1);
-    int* const s_row0 = s_t0 + (F8_MAX_EXPERTS + 1);
-    if ((threadIdx.x >> 6) == 0) f8_walk<BM>(p.m_indptr, p.m_rows, p.E, s_t0, s_row0);
-    __syncthreads();
-    const int count = s_t0[p.E];
-    const long total = static_cast<long>(count) * nt, run = (total + 7) / 8;
-    const long L = xcd * run + slot;
-    if (slot >= run || L >= total) return;
-    f8_order(L, count, nt, mt, ni);
-    e = f8_owner(s_t0, p.E, mt);
-    m0 = s_row0[e] + (mt - s_t0[e]) * BM;
-    // the group's own end, read again: the next group's first row is another
-    // number where m_indptr decreases
-    rows = min(min(max(p.m_indptr[e + 1], s_row0[e]), p.m_rows) - m0, BM);
+  const F8Tile t = f8_find<BM, BN>(p);
+  if (t.rows == 0) return;
+  constexpr int B = BM * F8_BK;  // b's rows follow a's
+  const F8Stage st0{s0, s0 + B}, st1{s1, s1 + B}, st2{s2, NST == 4 ? s2 + B : s2},
+      st3{s3, NST == 4 ? s3 + B : s3};
+  if constexpr (FM >= 4) {
+    if (t.rows <= BM / 2) {  // a group's last tile: half the work
+      f8_tile<WM, WN, FM / 2, FN, NST, OutT>(p, st0, st1, st2, st3, ssa0, ssa1, t);
+      return;
+    }
   }
-  f8_tile<WM, WN, FM, FN, OutT>(p, s0, s1, ssa0, ssa1, __builtin_amdgcn_readfirstlane(e),
-                                __builtin_amdgcn_readfirstlane(m0),
-                                __builtin_amdgcn_readfirstlane(rows),
-                                __builtin_amdgcn_readfirstlane(ni * BN));
+  f8_tile<WM, WN, FM, FN, NST, OutT>(p, st0, st1, st2, st3, ssa0, ssa1, t);
 }
 
-template <int WM, int WN, int FM, int FN, typename OutT>
-mi_status f8_launch(const F8Args& p, hipStream_t stream, const char* what) {
-  constexpr int BM = 16 * FM * WM, BN = 16 * FN * WN;
-  // an upper bound on the tiles: a group's last tile may be partial, and there
-  // are no more such groups than rows
-  long tiles = (static_cast<long>(p.m_rows) + BM - 1) / BM;
+// 256 x 256 tiles; a group's last tile, where it has at most 128 or 64 rows, does a
+// half or a quarter of the work.  It keeps its place among the group's tiles,
+// which share b's panels in L2.
+template <typename OutT>
+__global__ __launch_bounds__(512)
+    __attribute__((amdgpu_waves_per_eu(2, 2))) void f8_mm_large_kernel(F8Args p) {
+  __shared__ __attribute__((aligned(16))) uint8_t s0[512 * F8_BK];
+  __shared__ __attribute__((aligned(16))) uint8_t s1[512 * F8_BK];
+  __shared__ __attribute__((aligned(16))) float ssa0[256 * 4];
+  __shared__ __attribute__((aligned(16))) float ssa1[256 * 4];
+  const F8Tile t = f8_find<256, 256>(p);
+  if (t.rows == 0) return;
+  constexpr int B = 256 * F8_BK;
+  const F8Stage st0{s0, s0 + B}, st1{s1, s1 + B};
+  if (t.rows > 128)
+    f8_tile<2, 4, 8, 4, 2, OutT>(p, st0, st1, st0, st1, ssa0, ssa1, t);
+  else if (t.rows > 64)
+    f8_tile<2, 4, 4, 4, 2, OutT>(p, st0, st1, st0, st1, ssa0, ssa1, t);
+  else
+    f8_tile<1, 8, 4, 2, 2, OutT>(p, st0, st1, st0, st1, ssa0, ssa1, t);
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: the call streams b from memory, so every wavefront loads it
+// straight into MFMA operands (no LDS, no barrier) with P steps in flight.  A
+// workgroup has 16 FM rows and 16 FN columns; its NW wavefronts take the
+// steps (128 columns of k) in turn, NW consecutive lines of each row of b at a
+// time, and their sums are added in wavefront order in LDS at the end.
+// ---------------------------------------------------------------------------
+template <int FM, int FN, int NW, int P, typename OutT>
+__global__ __launch_bounds__(64 * NW) void f8_mm_few_kernel(F8Args p) {
+  constexpr int BM = 16 * FM, BN = 16 * FN;
+  static_assert(128 % BN == 0, "one b scale per step");
+  __shared__ __attribute__((aligned(16))) f32x4 red[NW * FM * FN * 64];
+  const F8Tile t = f8_find<BM, BN>(p);
+  if (t.rows == 0) return;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int k = p.k, n = p.n, KT = (k + F8_BK - 1) / F8_BK;
+  const int cols = min(n - t.n0, BN);
+  const int r = lane & 15, g = lane >> 4;
+  const __amdgpu_buffer_rsrc_t ar = buf_rsrc(p.a + static_cast<long>(t.m0) * k,
+                                             static_cast<uint32_t>(t.rows) * k);
+  const __amdgpu_buffer_rsrc_t br = buf_rsrc(p.b + (static_cast<long>(t.e) * n + t.n0) * k,
+                                             static_cast<uint32_t>(cols) * k);
+  const __amdgpu_buffer_rsrc_t sar = buf_rsrc(p.sa + static_cast<long>(t.m0) * p.sc,
+                                              static_cast<uint32_t>(t.rows) * p.sc * 4);
+  const float* sbp = p.sb + (static_cast<long>(t.e) * p.nb + t.n0 / 128) * p.sc;
+
+  // lane (r, g): chunks g and g + 4 of row r
+  uint32_t va[FM], vs[FM], vb[FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const bool in = 16 * i + r < t.rows;
+    va[i] = in ? static_cast<uint32_t>(16 * i + r) * k + g * 16 : F8_OUT;
+    vs[i] = in ? static_cast<uint32_t>(16 * i + r) * p.sc * 4 : F8_OUT;
+  }
+#pragma unroll
+  for (int j = 0; j < FN; ++j)
+    vb[j] = 16 * j + r < cols ? static_cast<uint32_t>(16 * j + r) * k + g * 16 : F8_OUT;
+  const int last = (KT - 1) * F8_BK + g * 16;
+  const uint32_t tail0 = last < k ? 0u : F8_OUT, tail1 = last + 64 < k ? 0u : F8_OUT;
+
+  struct Slot {
+    u32x4 a[FM][2], b[FN][2];
+    float s[FM];
+  } slot[P];
+  // step kt >= KT loads zeros, its scales among them
+  auto load = [&](Slot& q, int kt) {
+    const uint32_t so = __builtin_amdgcn_readfirstlane(min(kt, KT - 1) * F8_BK);
+    const uint32_t all = kt < KT ? 0u : F8_OUT;
+    const uint32_t d0 = kt == KT - 1 ? tail0 : all, d1 = kt == KT - 1 ? tail1 : all;
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      q.b[j][0] = buf_ld128(br, vb[j] | d0, so);
+      q.b[j][1] = buf_ld128(br, (vb[j] + 64) | d1, so);
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      q.a[i][0] = buf_ld128(ar, va[i] | d0, so);
+      q.a[i][1] = buf_ld128(ar, (va[i] + 64) | d1, so);
+      q.s[i] = __uint_as_float(buf_ld32(sar, vs[i] | all, so / (F8_BK / 4)));
+    }
+  };
+  f32x4 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  using Frag = F8Frag<sizeof(OutT) == 4>;
+  auto frag = [](const u32x4& x, const u32x4& y) {
+    return Frag(i32x8{(int)x[0], (int)x[1], (int)x[2], (int)x[3],
+                      (int)y[0], (int)y[1], (int)y[2], (int)y[3]});
+  };
+  float sbv = 0.f;  // b's scales of this wavefront's next 64 steps, a lane each
+  auto add = [&](const Slot& q, int it) {
+    const float sb = __builtin_bit_cast(
+        float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sbv), it & 63));
+    Frag fb[FN];
+#pragma unroll
+    for (int j = 0; j < FN; ++j) fb[j] = frag(q.b[j][0], q.b[j][1]);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const Frag fa = frag(q.a[i][0], q.a[i][1]);
+      const float f = q.s[i] * sb;
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const f32x4 d = f8_block(fb[j], fa);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[i][j][c] = __builtin_fmaf(d[c], f, acc[i][j][c]);
+      }
+    }
+  };
+#pragma unroll
+  for (int u = 0; u < P; ++u) {
+    load(slot[u], wave + NW * u);
+    __builtin_amdgcn_sched_barrier(0);  // slots in order: the loop's waits stay exact
+  }
+  const int IT = (KT + NW - 1) / NW;
+  static_assert(64 % P == 0, "the scale register is refilled between rounds");
+  for (int it = 0; it < IT; it += P) {
+    if ((it & 63) == 0) {
+      const int kt = wave + NW * (it + lane);
+      sbv = kt < KT ? sbp[kt] : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < P; ++u) {
+      add(slot[u], it + u);
+      load(slot[u], wave + NW * (it + u + P));
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) red[((wave * FM + i) * FN + j) * 64 + lane] = acc[i][j];
+  __syncthreads();
+  constexpr int ES = sizeof(OutT);
+  const __amdgpu_buffer_rsrc_t orsrc =
+      buf_rsrc(static_cast<OutT*>(p.out) + static_cast<long>(t.m0) * n,
+               static_cast<uint32_t>(t.rows) * n * ES);
+  for (int q = tid; q < FM * FN * 64; q += 64 * NW) {
+    f32x4 v = red[q];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) v += red[w * FM * FN * 64 + q];
+    // quad q: block (i, j) = q / 64, row 16 i + q % 16, columns 16 j + 4 ((q % 64) / 16) ..
+    const int i = q / (64 * FN), j = (q / 64) % FN;
+    const int row = 16 * i + (q & 15), col = 16 * j + 4 * ((q & 63) >> 4);
+    f8_store4<OutT>(orsrc, row < t.rows && col < cols
+                               ? (static_cast<uint32_t>(row) * n + t.n0 + col) * ES : F8_OUT, v);
+  }
+}
+
+// An upper bound on the tiles: a group's last one may be partial, and there are
+// no more such groups than rows.
+mi_status f8_grid(const F8Args& p, int bm, int bn, const char* what, dim3* grid) {
+  long tiles = (static_cast<long>(p.m_rows) + bm - 1) / bm;
   if (p.m_indptr != nullptr) tiles += p.E < p.m_rows ? p.E : p.m_rows;
-  tiles *= (p.n + BN - 1) / BN;
-  const long G = (tiles + 7) / 8 * 8;
-  MI_REQUIRE(G < (1L << 31), "%s: problem too large", what);
-  hipLaunchKernelGGL((f8_mm_kernel<WM, WN, FM, FN, OutT>), dim3(static_cast<unsigned>(G)),
-                     dim3(64 * WM * WN), 0, stream, p);
-  return launch_status(what);
+  tiles *= (p.n + bn - 1) / bn;
+  const long g = (tiles + 7) / 8 * 8;
+  MI_REQUIRE(g < (1L << 31), "%s: problem too large", what);
+  *grid = dim3(static_cast<unsigned>(g));
+  return MI_OK;
+}
+
+#define F8_LAUNCH(KERNEL_, BM_, BN_, THREADS_)                         \
+  do {                                                                 \
+    dim3 grid;                                                         \
+    const mi_status st = f8_grid(p, BM_, BN_, what, &grid);            \
+    if (st != MI_OK) return st;                                        \
+    hipLaunchKernelGGL((KERNEL_), grid, dim3(THREADS_), 0, stream, p); \
+    return launch_status(what);                                        \
+  } while (0)
+
+template <int WM, int WN, int FM, int FN, int NST, typename OutT>
+mi_status f8_launch(const F8Args& p, hipStream_t stream, const char* what) {
+  F8_LAUNCH((f8_mm_kernel<WM, WN, FM, FN, NST, OutT>), 16 * FM * WM, 16 * FN * WN, 64 * WM * WN);
 }
 
 template <typename OutT>
+mi_status f8_launch_large(const F8Args& p, hipStream_t stream, const char* what) {
+  F8_LAUNCH(f8_mm_large_kernel<OutT>, 256, 256, 512);
+}
+
+template <int FM, int FN, int NW, int P, typename OutT>
+mi_status f8_launch_few(const F8Args& p, hipStream_t stream, const char* what) {
+  F8_LAUNCH((f8_mm_few_kernel<FM, FN, NW, P, OutT>), 16 * FM, 16 * FN, 64 * NW);
+}
+#undef F8_LAUNCH
+
+template <typename OutT>
 mi_status f8_dispatch(const F8Args& p, hipStream_t s, const char* what) {
-  // fp32 outputs: the fp16 fragments take twice the registers, 128 x 64 tiles
-  if constexpr (sizeof(OutT) == 4) {
-    return f8_launch<2, 2, 4, 2, OutT>(p, s, what);
+  // By the sizes the host knows: of groups' rows only their average.  Times in us
+  // at n = k = 8192 unless said otherwise.
+  const long E = p.E, rows = (p.m_rows + E - 1) / E, n = p.n;
+  auto tiles = [&](long bm, long bn) { return (rows + bm - 1) / bm * ((n + bn - 1) / bn) * E; };
+  if (p.m_indptr == nullptr) {
+    // few rows: as long as its tiles run in one round, or where no other tile
+    // would read b less often (m 16: 15.5 against 17.7 for 64 x 64 tiles; m 24, two
+    // rounds: 27.4 against 17.8).  16 columns per workgroup where 32 do not give
+    // every CU one (m 1, n = k = 4096: 5.5 against 7.1)
+    if (tiles(16, 16) <= 256) return f8_launch_few<1, 1, 4, 4, OutT>(p, s, what);
+    if (rows <= 16 || tiles(16, 32) <= 256) return f8_launch_few<1, 2, 4, 2, OutT>(p, s, what);
   } else {
-    // 256 x 256 tiles halve the bytes each MFMA needs (m 4096, n = k = 8192: 243
-    // against 288 us), but only where they fill the chip: m 1024 has 128 of them,
-    // 90 against 69 us.  Groups' rows are known on the device only: the average.
-    const long rows = p.m_rows / p.E;
-    const long tiles = (rows + 255) / 256 * ((p.n + 255) / 256) * p.E;
-    if (rows >= 192 && tiles >= 192) return f8_launch<2, 4, 8, 4, OutT>(p, s, what);
-    return f8_launch<2, 2, 4, 4, OutT>(p, s, what);
+    // groups of few rows: b is read once per 16 or 32 rows (64 experts, n 2048,
+    // k 4096: 8 rows each 99 against 101, 12 rows 132 against 110, 16 rows 117
+    // against 114 for 64 x 64 tiles).  With little work per tile the start of its
+    // workgroup counts and larger tiles are as good (k 1024)
+    if (rows <= 8) return f8_launch_few<1, 2, 4, 2, OutT>(p, s, what);
+    if (rows <= 12) return f8_launch_few<2, 4, 4, 2, OutT>(p, s, what);
+  }
+  // 64 x 64 tiles with four stages, two workgroups per CU, while they run in one
+  // round (m 256: 31 against 44; m 384: 48 against 45)
+  if (tiles(64, 64) <= 512 || (p.m_indptr != nullptr && rows <= 40))
+    return f8_launch<2, 2, 2, 2, 4, OutT>(p, s, what);
+  if constexpr (sizeof(OutT) == 2) {
+    // 256 x 256 tiles have the fewest bytes per MFMA, but have to fill the chip
+    // (m 4096: 236 against 295; m 1024, 128 such tiles: 86 against 67)
+    if (rows >= 112 && tiles(256, 256) >= 192) return f8_launch_large<OutT>(p, s, what);
+    return f8_launch<2, 2, 4, 4, 2, OutT>(p, s, what);
+  } else {
+    // fp32: the fp16 fragments take twice the registers
+    return f8_launch<2, 2, 4, 2, 2, OutT>(p, s, what);
   }
 }
 
