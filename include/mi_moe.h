@@ -513,8 +513,8 @@ MI_API mi_status mi_mm_fp8_block(const uint8_t* a, const float* a_scale, int64_t
 /*
  * The ragged form: the same product for the rows [m_indptr[e], m_indptr[e+1])
  * of every expert e with b[e] (m_indptr as for mi_grouped_mm_bf16: device,
- * int32 [batch + 1], non-decreasing, read on the device only).  Rows outside the
- * groups are not written.
+ * int32 [batch + 1], non-decreasing, read on the device only).  Rows before the
+ * first group and behind the last are not written, or with zero_outside zeroed.
  *   a, a_scale   uint8 [m_rows, k], fp32 [m_rows, cols]
  *   b, b_scale   uint8 [batch, n, k], fp32 [batch, ceil(n / 128), cols]
  *   out          out_dtype [m_rows, n]
@@ -523,7 +523,8 @@ MI_API mi_status mi_mm_fp8_block(const uint8_t* a, const float* a_scale, int64_t
 MI_API mi_status mi_grouped_mm_fp8_block(const uint8_t* a, const float* a_scale, int64_t m_rows,
                                       int64_t k, const uint8_t* b, const float* b_scale,
                                       int64_t batch, int64_t n, const int32_t* m_indptr,
-                                      void* out, mi_dtype out_dtype, void* stream);
+                                      int zero_outside, void* out, mi_dtype out_dtype,
+                                      void* stream);
 
 /*
  * The way back from permuted rows to token rows:

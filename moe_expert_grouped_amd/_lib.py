@@ -126,7 +126,7 @@ def lib() -> ctypes.CDLL:
         L.mi_mm_fp8_block.restype = I32
         L.mi_mm_fp8_block.argtypes = [P, P, I64, I64, P, P, I64, P, I32, P]
         L.mi_grouped_mm_fp8_block.restype = I32
-        L.mi_grouped_mm_fp8_block.argtypes = [P, P, I64, I64, P, P, I64, I64, P, P, I32, P]
+        L.mi_grouped_mm_fp8_block.argtypes = [P, P, I64, I64, P, P, I64, I64, P, I32, P, I32, P]
         L.mi_moe_combine_rows.restype = I32
         L.mi_moe_combine_rows.argtypes = [P, I32, I64, I64, P, P, I64, I64, P, I32, P]
         L.mi_moe_combine_rows_backward.restype = I32

@@ -55,6 +55,7 @@ struct F8Args {
   int m_rows, k, n, E;
   int sc;                  // scale columns: 4 * ceil(k / 512)
   int nb;                  // scale rows of one b: ceil(n / 128)
+  int zero_outside;        // out's rows outside the groups are zeroed
 };
 
 // inclusive sum over the wavefront's lanes
@@ -140,6 +141,22 @@ __device__ __forceinline__ F8Tile f8_find(const F8Args& p) {
   // that overlap may pass 32 bits
   f.rows = f.m0 >= s_own && f.m0 < t_own ? min(t_own - f.m0, BM) : 0;
   return f;
+}
+
+// Zeros to out's rows before the first group and behind the last one, this
+// workgroup's share of them.
+template <typename OutT>
+__device__ __forceinline__ void f8_zero_outside(const F8Args& p) {
+  if (!p.zero_outside) return;
+  const int first = min(max(p.m_indptr[0], 0), p.m_rows);
+  const int last = min(max(p.m_indptr[p.E], first), p.m_rows);
+  if (first == 0 && last == p.m_rows) return;
+  const int64_t per_row = static_cast<int64_t>(p.n) * sizeof(OutT) / 16;  // 16-byte pieces
+  const int64_t head = first * per_row, all = head + (p.m_rows - last) * per_row;
+  char* const out = static_cast<char*>(p.out);
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < all;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x)
+    gst<u32x4>(out + (i < head ? i : i - head + last * per_row) * 16, u32x4{0, 0, 0, 0});
 }
 
 // four consecutive outputs of one row, rounded once to nearest even; an offset
@@ -459,6 +476,7 @@ __global__ __launch_bounds__(64 * WM * WN)
   __shared__ __attribute__((aligned(16))) uint8_t s3[NST == 4 ? STAGE : 16];
   __shared__ __attribute__((aligned(16))) float ssa0[BM * 4];
   __shared__ __attribute__((aligned(16))) float ssa1[BM * 4];
+  f8_zero_outside<OutT>(p);
   const F8Tile t = f8_find<BM, BN>(p);
   if (t.rows == 0) return;
   constexpr int B = BM * F8_BK;  // b's rows follow a's
@@ -483,6 +501,7 @@ __global__ __launch_bounds__(512)
   __shared__ __attribute__((aligned(16))) uint8_t s1[512 * F8_BK];
   __shared__ __attribute__((aligned(16))) float ssa0[256 * 4];
   __shared__ __attribute__((aligned(16))) float ssa1[256 * 4];
+  f8_zero_outside<OutT>(p);
   const F8Tile t = f8_find<256, 256>(p);
   if (t.rows == 0) return;
   constexpr int B = 256 * F8_BK;
@@ -507,6 +526,7 @@ __global__ __launch_bounds__(64 * NW) void f8_mm_few_kernel(F8Args p) {
   constexpr int BM = 16 * FM, BN = 16 * FN;
   static_assert(128 % BN == 0, "one b scale per step");
   __shared__ __attribute__((aligned(16))) f32x4 red[NW * FM * FN * 64];
+  f8_zero_outside<OutT>(p);
   const F8Tile t = f8_find<BM, BN>(p);
   if (t.rows == 0) return;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -755,8 +775,8 @@ extern "C" mi_status mi_mm_fp8_block(const uint8_t* a, const float* a_scale, int
 extern "C" mi_status mi_grouped_mm_fp8_block(const uint8_t* a, const float* a_scale,
                                              int64_t m_rows, int64_t k, const uint8_t* b,
                                              const float* b_scale, int64_t batch, int64_t n,
-                                             const int32_t* m_indptr, void* out,
-                                             mi_dtype out_dtype, void* stream) {
+                                             const int32_t* m_indptr, int zero_outside,
+                                             void* out, mi_dtype out_dtype, void* stream) {
   using namespace mi;
   clear_error();
   MI_REQUIRE(m_indptr != nullptr, "grouped_mm_fp8_block: m_indptr is null");
@@ -766,6 +786,7 @@ extern "C" mi_status mi_grouped_mm_fp8_block(const uint8_t* a, const float* a_sc
   p.b = b;
   p.sb = b_scale;
   p.m_indptr = m_indptr;
+  p.zero_outside = zero_outside != 0;
   p.out = out;
   return f8_run(p, m_rows, k, n, batch, out_dtype, stream, "grouped_mm_fp8_block");
 }

@@ -427,3 +427,25 @@ def test_empty_calls(gpu):
     ind = torch.zeros(2, dtype=torch.int32, device=gpu)
     assert grouped_mm_fp8_block(c, s, b[None], sb[None], ind).shape == (0, 64)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("indptr,m", [([4, 4, 9], 40), ([0, 0, 0], 7), ([0, 33, 33], 33),
+                                      ([2, 200, 500], 700)], ids=str)
+def test_grouped_fresh_out_is_zero_outside_the_groups(gpu, indptr, m):
+    """A fresh out holds zeros before the first group and behind the last, also
+    where its memory held something else."""
+    g = synth.gen(m)
+    n, k = 272, 144
+    E = len(indptr) - 1
+    a, b = _codes(g, (m, k)).to(gpu).view(F8), _codes(g, (E, n, k)).to(gpu).view(F8)
+    sa, sb = _scale_rows(g, (m,), k).to(gpu), _scale_rows(g, (E, 3), k).to(gpu)
+    ind = torch.tensor(indptr, dtype=torch.int32, device=gpu)
+    for dtype in DTYPES:
+        print(f"grouped_mm_fp8_block fresh out {indptr} {dtype}", flush=True)
+        torch.full((m, n), float("nan"), dtype=dtype, device=gpu)  # freed: reused by out
+        got = grouped_mm_fp8_block(a, sa * 2.0 ** -8, b, sb * 2.0 ** -8, ind, out_dtype=dtype)
+        v = _np(got)
+        inside = np.zeros(m, bool)
+        inside[indptr[0]:indptr[-1]] = True
+        assert not v[~inside].any() and np.isfinite(v).all()
+        assert not inside.any() or (v[inside] != 0).any(axis=1).all()

@@ -106,7 +106,7 @@ def _mm(**kw):
 
 def _gmm(**kw):
     return _call("mi_grouped_mm_fp8_block", dict(a=FAKE, sa=FAKE, m=5, k=128, b=FAKE, sb=FAKE, e=4,
-                                                 n=64, ind=FAKE, out=FAKE, dt=_lib.MI_BF16,
+                                                 n=64, ind=FAKE, zero=0, out=FAKE, dt=_lib.MI_BF16,
                                                  stream=None), **kw)
 
 
@@ -216,7 +216,7 @@ def test_python_refusals_before_the_gpu():
         mi.mm_fp8_block(a.float(), b, sa, sb)
     with pytest.raises(ValueError, match="float8_e4m3fn"):
         mi.mm_fp8_block(a, b[:, :128], sa, sb)
-    with pytest.raises(ValueError, match=r"a_scale must be float32 \(M, 4\)"):
+    with pytest.raises(ValueError, match=r"a_scale must be float32 \(M, fp8_scale_cols"):
         mi.mm_fp8_block(a, b, sa[:, :2], sb)
     with pytest.raises(ValueError, match="b_scale must be"):
         mi.mm_fp8_block(a, b, sa, sb[:1])
