@@ -32,7 +32,6 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) void* lds_void_ptr;
 
 constexpr int F8_MAX_EXPERTS = 1024;
-constexpr int F8_GROUP_M = 8;
 constexpr int F8_BK = 128;             // one scale block: one 128-byte LDS row
 // a lane offset past every descriptor's range: its load gives zero, its store is dropped
 constexpr uint32_t F8_OUT = 0x80000000u;
@@ -72,12 +71,14 @@ __device__ __forceinline__ uint32_t f8_scan(uint32_t v) {
   return v;
 }
 
-// m-tile and n-panel of the L-th tile: F8_GROUP_M m-tiles sweep the n-panels together
-__device__ __forceinline__ void f8_order(uint32_t L, int count, int nt, int& mt, int& ni) {
-  const uint32_t span = F8_GROUP_M * nt;
+// m-tile and n-panel of the L-th tile: GM m-tiles sweep the n-panels together
+template <uint32_t GM>
+__device__ __forceinline__ void f8_order(uint32_t L, uint32_t count, uint32_t nt, int& mt,
+                                         int& ni) {
+  const uint32_t span = GM * nt;
   const uint32_t grp = L / span;
-  const uint32_t first = grp * F8_GROUP_M;
-  const uint32_t gsize = min(count - first, static_cast<uint32_t>(F8_GROUP_M));
+  const uint32_t first = grp * GM;
+  const uint32_t gsize = min(count - first, GM);
   const uint32_t in_grp = L - grp * span;
   mt = first + in_grp % gsize;
   ni = in_grp / gsize;
@@ -120,7 +121,9 @@ __device__ __forceinline__ F8Tile f8_find(const F8Args& p) {
   const uint32_t total = count * nt, run = (total + 7) / 8, L = xcd * run + slot;
   if (slot >= run || L >= total) return f;
   int mt, ni;
-  f8_order(L, count, nt, mt, ni);
+  // 256-row tiles: 4 together 227 us, 8 232, 16 238 at m 4096, n = k = 8192; 64-row
+  // tiles: 8 together 29.9, 16 31.0 at m 256
+  f8_order<BM >= 256 ? 4 : 8>(L, count, nt, mt, ni);
   int owner = __builtin_popcountll(__ballot(upto <= static_cast<uint32_t>(mt)));
   f.e = owner * per;
   if (per > 1) {
@@ -241,7 +244,7 @@ struct F8Stage {
 // loads of step kt+NST, and the next stage is complete (the wait leaves the loads
 // of the later ones in flight), so the last regions read the next step's first
 // fragments while their MFMAs run.
-template <int WM, int WN, int FM, int FN, int NST, typename OutT>
+template <int WM, int WN, int FM, int FN, int NST, bool STREAM, typename OutT>
 __device__ __forceinline__ void f8_tile(const F8Args& p, F8Stage s0, F8Stage s1, F8Stage s2,
                                         F8Stage s3, float* ssa0, float* ssa1, const F8Tile& t) {
   const int e = t.e, m0 = t.m0, rows = t.rows, n0 = t.n0;
@@ -284,26 +287,40 @@ __device__ __forceinline__ void f8_tile(const F8Args& p, F8Stage s0, F8Stage s1,
     vb[i] = row < cols ? static_cast<uint32_t>(row) * k + chunk * 16 : F8_OUT;
   }
   const uint32_t tail = (KT - 1) * F8_BK + chunk * 16 < k ? 0u : F8_OUT;
+  // STREAM: the steps go through the blocks of k from `rot` on, a multiple of 4
+  // (one load of a's scales), and round the end; every n-panel of b (all its
+  // m-tiles: they share the panel) and every group has its own start.  With one
+  // start for all, workgroups ask for the same bytes of rows that are a power of
+  // two apart, and those lie in a few memory channels.
+  const int rot = STREAM && k % 512 == 0 ? (n0 / BN + e) % (KT / 4) * 4 : 0;
+  auto block = [&](int kt) { return !STREAM || kt + rot < KT ? kt + rot : kt + rot - KT; };
   // A step past the last loads zeros (its lane offsets are out of range): the
   // steps stay free of branches, which keep the compiler from moving a region's
   // additions into the next step.
-  auto dma = [&](const F8Stage& st, int kt) {
-    const uint32_t so = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(min(kt, KT - 1)) * F8_BK);
-    const uint32_t drop = kt < KT - 1 ? 0u : kt == KT - 1 ? tail : F8_OUT;
+  // Pieces [first, first + count) of the NI loads of a stage.
+  constexpr int NI = NIA + NIB;
+  auto dma = [&](const F8Stage& st, int kt, int first, int count) {
+    const int kb = block(min(kt, KT - 1));  // KT - 1 itself has the tail: rot is 0 then
+    const uint32_t so = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(kb) * F8_BK);
+    const uint32_t drop = kt >= KT ? F8_OUT : kb == KT - 1 ? tail : 0u;
 #pragma unroll
-    for (int i = 0; i < NIA; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, f8_lds(st.a + (NW * i + wave) * 1024), 16,
-                                               va[i] | drop, so, 0, 0);
-#pragma unroll
-    for (int i = 0; i < NIB; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(br, f8_lds(st.b + (NW * i + wave) * 1024), 16,
-                                               vb[i] | drop, so, 0, 0);
+    for (int i = 0; i < NI; ++i) {
+      if (i < first || i >= first + count) continue;
+      if (i < NIA)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, f8_lds(st.a + (NW * i + wave) * 1024), 16,
+                                                 va[i < NIA ? i : 0] | drop, so, 0, 0);
+      else
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            br, f8_lds(st.b + (NW * (i - NIA) + wave) * 1024), 16,
+            vb[i < NIA ? 0 : i - NIA] | drop, so, 0, STREAM ? 2 : 0);
+    }
   };
   // 64 rows' scales per wavefront; wavefronts past the tile's rows load the same again
   const int swave = wave % (BM / 64), srow = swave * 64 + lane;
   const uint32_t vsa = srow < rows ? static_cast<uint32_t>(srow) * p.sc * 4 : F8_OUT;
   auto dma_scales = [&](float* buf, int kt) {  // kt a multiple of 4
-    const uint32_t so = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(min(kt, p.sc - 4)) * 4);
+    const uint32_t so =
+        __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(kt < KT ? block(kt) : 0) * 4);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(sar, f8_lds(buf + swave * 256), 16, vsa, so, 0, 0);
   };
 
@@ -340,12 +357,16 @@ __device__ __forceinline__ void f8_tile(const F8Args& p, F8Stage s0, F8Stage s1,
   float f = 0.f;                           // the factor of the last region
   f32x4 d0 = {0.f, 0.f, 0.f, 0.f}, d1 = d0;  // the last two results, not yet added
 
-  auto step = [&](auto S, const F8Stage& st, const F8Stage& nx, int kt) {
+  // A stage's loads go out PPR per region from the one behind the barrier on, over
+  // half of the regions: all at once they hold up the MFMAs behind them, later
+  // they would not arrive in time.
+  constexpr int PPR = (2 * NI + FM - 1) / FM;
+  auto step = [&](auto S, const F8Stage& pv, const F8Stage& st, const F8Stage& nx, int kt) {
     constexpr int s = decltype(S)::value;
     float* const sc = s < 4 ? ssa0 : ssa1;
     float* const sc_nx = s < 4 ? ssa1 : ssa0;
     const float sb = __builtin_bit_cast(
-        float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sbv), kt & 63));
+        float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sbv), block(kt) & 63));
     Frag fbx[FN];
 #pragma unroll
     for (int j = 0; j < FN; ++j) fbx[j] = Frag(fb[j]);
@@ -353,9 +374,11 @@ __device__ __forceinline__ void f8_tile(const F8Args& p, F8Stage s0, F8Stage s1,
     for (int i = 0; i < FM; ++i) {
       if (i == FM - 2) {
         f8_wait_barrier<FLY>();
-        dma(st, kt + NST);
         if constexpr ((s & 3) == 0) dma_scales(sc_nx, kt + 4);
       }
+      constexpr int R0 = FM - 2;  // the region behind the barrier
+      if (i >= R0) dma(st, kt + NST, (i - R0) * PPR, PPR);
+      else if ((i + 2) * PPR < NI) dma(pv, kt + NST - 1, (i + 2) * PPR, PPR);
       const Frag fax(fa0);
       const float f_prev = f;
       f = sa0 * sb;
@@ -385,33 +408,39 @@ __device__ __forceinline__ void f8_tile(const F8Args& p, F8Stage s0, F8Stage s1,
     }
   };
 
-  dma(s0, 0);
+  dma(s0, 0, 0, NI);
   dma_scales(ssa0, 0);
   if constexpr (NST == 4) {
-    dma(s1, 1);
-    dma(s2, 2);
+    dma(s1, 1, 0, NI);
+    dma(s2, 2, 0, NI);
   }
   f8_wait_barrier<FLY>();
-  dma(NST == 4 ? s3 : s1, NST - 1);
+  dma(NST == 4 ? s3 : s1, NST - 1, 0, 2 * PPR);  // the rest in step 0
   fa0 = frag(s0.a, ablk);
   fa1 = frag(s0.a, ablk + 1);
   sa0 = ssa0[srd];
   sa1 = ssa0[srd + 64];
 #pragma unroll
   for (int j = 0; j < FN; ++j) fb[j] = frag(s0.b, bblk + j);
+  // b's scales of the 64 blocks that block kb is one of
+  auto load_sb = [&](int kb) { sbv = sbp[min((kb & ~63) + lane, p.sc - 1)]; };
+  load_sb(block(0));
   for (int kt = 0; kt < KT; kt += 8) {
-    if ((kt & 63) == 0) sbv = sbp[min(kt + lane, p.sc - 1)];
-#define F8_STEP(S_, ST_, NX_)                                       \
-  step(std::integral_constant<int, S_>{}, ST_, NX_, kt + S_);        \
+    if (KT > 64 && kt > 0 && (block(kt) & 63) < 4) load_sb(block(kt));
+#define F8_STEP(S_, PV_, ST_, NX_)                                  \
+  step(std::integral_constant<int, S_>{}, PV_, ST_, NX_, kt + S_);   \
   if (kt + S_ + 1 >= KT) break;
-    F8_STEP(0, s0, s1)
-    F8_STEP(1, s1, NST == 4 ? s2 : s0)
-    F8_STEP(2, NST == 4 ? s2 : s0, NST == 4 ? s3 : s1)
-    F8_STEP(3, NST == 4 ? s3 : s1, s0)
-    F8_STEP(4, s0, s1)
-    F8_STEP(5, s1, NST == 4 ? s2 : s0)
-    F8_STEP(6, NST == 4 ? s2 : s0, NST == 4 ? s3 : s1)
-    F8_STEP(7, NST == 4 ? s3 : s1, s0)
+    const F8Stage& t2 = NST == 4 ? s2 : s0;
+    const F8Stage& t3 = NST == 4 ? s3 : s1;
+    F8_STEP(0, t3, s0, s1)
+    F8_STEP(1, s0, s1, t2)
+    F8_STEP(2, s1, t2, t3)
+    F8_STEP(3, t2, t3, s0)
+    if (KT > 64 && (block(kt + 4) & 63) < 4) load_sb(block(kt + 4));
+    F8_STEP(4, t3, s0, s1)
+    F8_STEP(5, s0, s1, t2)
+    F8_STEP(6, s1, t2, t3)
+    F8_STEP(7, t2, t3, s0)
 #undef F8_STEP
   }
   // the loads of the steps past the last write (zeros) to LDS: not after this
@@ -465,7 +494,7 @@ __device__ __forceinline__ void f8_tile(const F8Args& p, F8Stage s0, F8Stage s1,
 
 // Tiles of one shape.  Two wavefronts per SIMD: 256 registers each, all of them
 // usable by the VALU, which adds the MFMAs' results.
-template <int WM, int WN, int FM, int FN, int NST, typename OutT>
+template <int WM, int WN, int FM, int FN, int NST, bool STREAM, typename OutT>
 __global__ __launch_bounds__(64 * WM * WN)
     __attribute__((amdgpu_waves_per_eu(2, 2))) void f8_mm_kernel(F8Args p) {
   constexpr int BM = 16 * FM * WM, BN = 16 * FN * WN, STAGE = (BM + BN) * F8_BK;
@@ -484,17 +513,17 @@ __global__ __launch_bounds__(64 * WM * WN)
       st3{s3, NST == 4 ? s3 + B : s3};
   if constexpr (FM >= 4) {
     if (t.rows <= BM / 2) {  // a group's last tile: half the work
-      f8_tile<WM, WN, FM / 2, FN, NST, OutT>(p, st0, st1, st2, st3, ssa0, ssa1, t);
+      f8_tile<WM, WN, FM / 2, FN, NST, STREAM, OutT>(p, st0, st1, st2, st3, ssa0, ssa1, t);
       return;
     }
   }
-  f8_tile<WM, WN, FM, FN, NST, OutT>(p, st0, st1, st2, st3, ssa0, ssa1, t);
+  f8_tile<WM, WN, FM, FN, NST, STREAM, OutT>(p, st0, st1, st2, st3, ssa0, ssa1, t);
 }
 
 // 256 x 256 tiles; a group's last tile, where it has at most 128 or 64 rows, does a
 // half or a quarter of the work.  It keeps its place among the group's tiles,
 // which share b's panels in L2.
-template <typename OutT>
+template <bool STREAM, typename OutT>
 __global__ __launch_bounds__(512)
     __attribute__((amdgpu_waves_per_eu(2, 2))) void f8_mm_large_kernel(F8Args p) {
   __shared__ __attribute__((aligned(16))) uint8_t s0[512 * F8_BK];
@@ -507,11 +536,11 @@ __global__ __launch_bounds__(512)
   constexpr int B = 256 * F8_BK;
   const F8Stage st0{s0, s0 + B}, st1{s1, s1 + B};
   if (t.rows > 128)
-    f8_tile<2, 4, 8, 4, 2, OutT>(p, st0, st1, st0, st1, ssa0, ssa1, t);
+    f8_tile<2, 4, 8, 4, 2, STREAM, OutT>(p, st0, st1, st0, st1, ssa0, ssa1, t);
   else if (t.rows > 64)
-    f8_tile<2, 4, 4, 4, 2, OutT>(p, st0, st1, st0, st1, ssa0, ssa1, t);
+    f8_tile<2, 4, 4, 4, 2, STREAM, OutT>(p, st0, st1, st0, st1, ssa0, ssa1, t);
   else
-    f8_tile<1, 8, 4, 2, 2, OutT>(p, st0, st1, st0, st1, ssa0, ssa1, t);
+    f8_tile<1, 8, 4, 2, 2, STREAM, OutT>(p, st0, st1, st0, st1, ssa0, ssa1, t);
 }
 
 // ---------------------------------------------------------------------------
@@ -658,6 +687,19 @@ mi_status f8_grid(const F8Args& p, int bm, int bn, const char* what, dim3* grid)
   return MI_OK;
 }
 
+// Whether a product of groups streams b: its panels are read about once (groups
+// of up to a tile's rows on average), and the next call would hardly find them in
+// the 256 MB memory-side cache.  Then b is loaded with the non-temporal policy
+// and every panel has its own first step.  64 experts, n 2048, k 4096, 16 rows
+// each: 130 us, non-temporal 119, with own first steps 81; k 2048: 51.8 and 48.4;
+// skewed 128 experts of 15 MB: 744 and 727 (non-temporal).  Panels read twice or
+// found in the cache lose (128-row tiles of 256 rows each 468 and 489, 16 experts
+// of 1 MB 9.5 and 11.5).
+bool f8_stream_b(const F8Args& p, int bm) {
+  return p.m_indptr != nullptr && p.m_rows / p.E <= bm &&
+         static_cast<int64_t>(p.E) * p.n * p.k >= (128LL << 20);
+}
+
 #define F8_LAUNCH(KERNEL_, BM_, BN_, THREADS_)                         \
   do {                                                                 \
     dim3 grid;                                                         \
@@ -669,12 +711,16 @@ mi_status f8_grid(const F8Args& p, int bm, int bn, const char* what, dim3* grid)
 
 template <int WM, int WN, int FM, int FN, int NST, typename OutT>
 mi_status f8_launch(const F8Args& p, hipStream_t stream, const char* what) {
-  F8_LAUNCH((f8_mm_kernel<WM, WN, FM, FN, NST, OutT>), 16 * FM * WM, 16 * FN * WN, 64 * WM * WN);
+  if (f8_stream_b(p, 16 * FM * WM))
+    F8_LAUNCH((f8_mm_kernel<WM, WN, FM, FN, NST, true, OutT>), 16 * FM * WM, 16 * FN * WN,
+              64 * WM * WN);
+  F8_LAUNCH((f8_mm_kernel<WM, WN, FM, FN, NST, false, OutT>), 16 * FM * WM, 16 * FN * WN, 64 * WM * WN);
 }
 
 template <typename OutT>
 mi_status f8_launch_large(const F8Args& p, hipStream_t stream, const char* what) {
-  F8_LAUNCH(f8_mm_large_kernel<OutT>, 256, 256, 512);
+  if (f8_stream_b(p, 256)) F8_LAUNCH((f8_mm_large_kernel<true, OutT>), 256, 256, 512);
+  F8_LAUNCH((f8_mm_large_kernel<false, OutT>), 256, 256, 512);
 }
 
 template <int FM, int FN, int NW, int P, typename OutT>
@@ -685,33 +731,38 @@ mi_status f8_launch_few(const F8Args& p, hipStream_t stream, const char* what) {
 
 template <typename OutT>
 mi_status f8_dispatch(const F8Args& p, hipStream_t s, const char* what) {
-  // By the sizes the host knows: of groups' rows only their average.  Times in us
-  // at n = k = 8192 unless said otherwise.
+  // By the sizes the host knows: of groups' rows only their average.  Times in us,
+  // of dense products at n = k = 8192 unless said otherwise.
+  const bool grouped = p.m_indptr != nullptr;
   const long E = p.E, rows = (p.m_rows + E - 1) / E, n = p.n;
-  auto tiles = [&](long bm, long bn) { return (rows + bm - 1) / bm * ((n + bn - 1) / bn) * E; };
-  if (p.m_indptr == nullptr) {
-    // few rows: as long as its tiles run in one round, or where no other tile
-    // would read b less often (m 16: 15.5 against 17.7 for 64 x 64 tiles; m 24, two
-    // rounds: 27.4 against 17.8).  16 columns per workgroup where 32 do not give
-    // every CU one (m 1, n = k = 4096: 5.5 against 7.1)
-    if (tiles(16, 16) <= 256) return f8_launch_few<1, 1, 4, 4, OutT>(p, s, what);
-    if (rows <= 16 || tiles(16, 32) <= 256) return f8_launch_few<1, 2, 4, 2, OutT>(p, s, what);
-  } else {
-    // groups of few rows: b is read once per 16 or 32 rows (64 experts, n 2048,
-    // k 4096: 8 rows each 99 against 101, 12 rows 132 against 110, 16 rows 117
-    // against 114 for 64 x 64 tiles).  With little work per tile the start of its
-    // workgroup counts and larger tiles are as good (k 1024)
-    if (rows <= 8) return f8_launch_few<1, 2, 4, 2, OutT>(p, s, what);
-    if (rows <= 12) return f8_launch_few<2, 4, 4, 2, OutT>(p, s, what);
-  }
-  // 64 x 64 tiles with four stages, two workgroups per CU, while they run in one
-  // round (m 256: 31 against 44; m 384: 48 against 45)
-  if (tiles(64, 64) <= 512 || (p.m_indptr != nullptr && rows <= 40))
+  auto tiles = [&](long bm, long bn) { return (rows + bm - 1) / bm * ((n + bn - 1) / bn); };
+  const long active = E < p.m_rows ? E : p.m_rows;  // groups that have rows, at most
+  // Few rows.  Dense: as long as the tiles run in one round, or where no other tile
+  // would read b less often (m 16: 15.6 against 17.5 for 64 x 64 tiles; m 24, two
+  // rounds: 27.5 against 17.5); 16 columns per workgroup where 32 do not give every
+  // CU one (m 1, n = k = 4096: 5.8 against 7.4).  Groups: while only a few have rows
+  // (64 experts, n 2048, k 4096: 8 rows 12.8 against 16.2, 16 rows 25 against 21).
+  if (!grouped && tiles(16, 16) <= 256) return f8_launch_few<1, 1, 4, 4, OutT>(p, s, what);
+  if (grouped ? rows <= 16 && active * ((n + 31) / 32) <= 512
+              : rows <= 16 || tiles(16, 32) <= 256)
+    return f8_launch_few<1, 2, 4, 2, OutT>(p, s, what);
+  // 64 x 64 tiles with four stages.  Dense: while they run in one round of two
+  // workgroups per CU (m 256: 32 against 42 for 128 x 128; m 384: 48 against 43).
+  // Groups of up to 48 rows: while the 128 x 128 tiles would not fill such a round (8
+  // experts, n = k = 4096, 16 rows: 25 against 32; 64 experts, n 2048: 89 against 81),
+  // with a long k two (64 experts, n 1536, k 7168, 4 rows: 109 against 123).
+  const long panels = active * ((n + 127) / 128);
+  if (grouped ? rows <= 48 && (panels < 512 || (panels <= 1024 && p.k > 4096))
+              : tiles(64, 64) <= 512)
     return f8_launch<2, 2, 2, 2, 4, OutT>(p, s, what);
   if constexpr (sizeof(OutT) == 2) {
     // 256 x 256 tiles have the fewest bytes per MFMA, but have to fill the chip
-    // (m 4096: 236 against 295; m 1024, 128 such tiles: 86 against 67)
-    if (rows >= 112 && tiles(256, 256) >= 192) return f8_launch_large<OutT>(p, s, what);
+    // (m 4096: 227 against 290; m 1024, 128 such tiles: 81 against 69; 8 groups of
+    // 192 rows, n = k = 4096: 56 against 48, of 256 rows 58 against 75).  A group has
+    // half a tile more than its rows fill; below 104 rows the 128-row tiles are as
+    // good (64 experts, n 2048, k 4096, 96 rows: 105 and 108)
+    const long large = grouped ? E * (2 * rows + 256) / 512 * ((n + 255) / 256) : tiles(256, 256);
+    if (rows >= 104 && large >= 192) return f8_launch_large<OutT>(p, s, what);
     return f8_launch<2, 2, 4, 4, 2, OutT>(p, s, what);
   } else {
     // fp32: the fp16 fragments take twice the registers
