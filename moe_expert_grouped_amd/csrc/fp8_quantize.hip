@@ -137,7 +137,11 @@ __global__ __launch_bounds__(256) void f8_blocks_kernel(const T* __restrict__ x,
                                                         uint8_t* __restrict__ codes,
                                                         float* __restrict__ scales) {
   __shared__ uint32_t s_max[4];
-  const int64_t blk = blockIdx.x;
+  // workgroup ids go to the 8 XCDs in turn: each XCD gets a contiguous run of
+  // blocks, so that its L2 joins the lines two neighbours write parts of
+  const int64_t total = static_cast<int64_t>(gridDim.x) / 8 * 8, per_xcd = total / 8;
+  const int64_t id = blockIdx.x;
+  const int64_t blk = id < total ? (id & 7) * per_xcd + (id >> 3) : id;
   const int cb = static_cast<int>(blk % kb);
   const int64_t rest = blk / kb;
   const int rb = static_cast<int>(rest % nb);
