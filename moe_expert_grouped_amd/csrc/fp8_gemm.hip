@@ -80,8 +80,10 @@ __device__ __forceinline__ void f8_order(uint32_t L, uint32_t count, uint32_t nt
   const uint32_t first = grp * GM;
   const uint32_t gsize = min(count - first, GM);
   const uint32_t in_grp = L - grp * span;
-  mt = first + in_grp % gsize;
+  // The m-tiles turn by one every 8 panels: consecutive tiles of one place then
+  // are not all of the same height (skewed experts 790 -> 780 us with 128-row tiles)
   ni = in_grp / gsize;
+  mt = first + (in_grp % gsize + ni / 8) % gsize;
 }
 
 struct F8Tile {
@@ -408,6 +410,10 @@ __device__ __forceinline__ void f8_tile(const F8Args& p, F8Stage s0, F8Stage s1,
     }
   };
 
+  // b's scales of the 64 blocks that block kb is one of; before the stages, as a
+  // wait for them would be a wait for everything before them
+  auto load_sb = [&](int kb) { sbv = sbp[min((kb & ~63) + lane, p.sc - 1)]; };
+  load_sb(block(0));
   dma(s0, 0, 0, NI);
   dma_scales(ssa0, 0);
   if constexpr (NST == 4) {
@@ -422,9 +428,6 @@ __device__ __forceinline__ void f8_tile(const F8Args& p, F8Stage s0, F8Stage s1,
   sa1 = ssa0[srd + 64];
 #pragma unroll
   for (int j = 0; j < FN; ++j) fb[j] = frag(s0.b, bblk + j);
-  // b's scales of the 64 blocks that block kb is one of
-  auto load_sb = [&](int kb) { sbv = sbp[min((kb & ~63) + lane, p.sc - 1)]; };
-  load_sb(block(0));
   for (int kt = 0; kt < KT; kt += 8) {
     if (KT > 64 && kt > 0 && (block(kt) & 63) < 4) load_sb(block(kt));
 #define F8_STEP(S_, PV_, ST_, NX_)                                  \
@@ -757,17 +760,16 @@ mi_status f8_dispatch(const F8Args& p, hipStream_t s, const char* what) {
     return f8_launch<2, 2, 2, 2, 4, OutT>(p, s, what);
   if constexpr (sizeof(OutT) == 2) {
     // 256 x 256 tiles have the fewest bytes per MFMA, but have to fill the chip
-    // (m 4096: 227 against 290; m 1024, 128 such tiles: 81 against 69; 8 groups of
+    // (m 4096: 222 against 286; m 1024, 128 such tiles: 81 against 66; 8 groups of
     // 192 rows, n = k = 4096: 56 against 48, of 256 rows 58 against 75).  A group has
     // half a tile more than its rows fill; below 104 rows the 128-row tiles are as
     // good (64 experts, n 2048, k 4096, 96 rows: 105 and 108)
     const long large = grouped ? E * (2 * rows + 256) / 512 * ((n + 255) / 256) : tiles(256, 256);
     if (rows >= 104 && large >= 192) return f8_launch_large<OutT>(p, s, what);
-    return f8_launch<2, 2, 4, 4, 2, OutT>(p, s, what);
-  } else {
-    // fp32: the fp16 fragments take twice the registers
-    return f8_launch<2, 2, 4, 2, 2, OutT>(p, s, what);
   }
+  // fp32 outputs stay here: fp16 fragments of a 256-row tile would not fit the
+  // registers (m 4096: 450; with 128 x 64 tiles 569)
+  return f8_launch<2, 2, 4, 4, 2, OutT>(p, s, what);
 }
 
 mi_status f8_run(const F8Args& p, int64_t m_rows, int64_t k, int64_t n, int64_t batch,
