@@ -91,11 +91,14 @@ struct F8Tile {
 };
 
 // The tile of BM rows and BN columns of this workgroup.  The grid is an upper
-// bound on the tiles; they are dealt in 8 contiguous runs, one per XCD (workgroup
-// ids go to the XCDs in turn).  Every wavefront reads m_indptr itself: a lane
-// has ceil(E / 64) experts, and where that is more than one, a second round
-// resolves the lane's.
-template <int BM, int BN>
+// bound on the tiles; workgroup ids go to the 8 XCDs in turn.  The list of tiles
+// is dealt to the XCDs in chunks of up to CM tiles, what an XCD runs at once, all
+// of one size: an XCD's L2 serves neighbours, and with chunks from the whole list
+// every XCD has its share of the short tiles (one contiguous run each was up to a
+// quarter longer on one XCD than on average, skewed experts).
+// Every wavefront reads m_indptr itself: a lane has ceil(E / 64) experts, and
+// where that is more than one, a second round resolves the lane's.
+template <int BM, int BN, uint32_t CM>
 __device__ __forceinline__ F8Tile f8_find(const F8Args& p) {
   const int lane = threadIdx.x & 63;
   const int per = (p.E + 63) / 64;
@@ -120,8 +123,11 @@ __device__ __forceinline__ F8Tile f8_find(const F8Args& p) {
   }
   uint32_t upto = f8_scan(cnt), before = upto - cnt;  // this lane's place in the list of tiles
   const uint32_t count = __builtin_amdgcn_readlane(upto, 63);
-  const uint32_t total = count * nt, run = (total + 7) / 8, L = xcd * run + slot;
-  if (slot >= run || L >= total) return f;
+  const uint32_t total = count * nt;
+  const uint32_t rounds = max((total + 8 * CM - 1) / (8 * CM), 1u);
+  const uint32_t chunk = max((total + 8 * rounds - 1) / (8 * rounds), 1u);
+  const uint32_t round = slot / chunk, L = (round * 8 + xcd) * chunk + slot % chunk;
+  if (round >= rounds || L >= total) return f;
   int mt, ni;
   // 256-row tiles: 4 together 227 us, 8 232, 16 238 at m 4096, n = k = 8192; 64-row
   // tiles: 8 together 29.9, 16 31.0 at m 256
@@ -509,7 +515,7 @@ __global__ __launch_bounds__(64 * WM * WN)
   __shared__ __attribute__((aligned(16))) float ssa0[BM * 4];
   __shared__ __attribute__((aligned(16))) float ssa1[BM * 4];
   f8_zero_outside<OutT>(p);
-  const F8Tile t = f8_find<BM, BN>(p);
+  const F8Tile t = f8_find<BM, BN, 64>(p);  // two workgroups per CU
   if (t.rows == 0) return;
   constexpr int B = BM * F8_BK;  // b's rows follow a's
   const F8Stage st0{s0, s0 + B}, st1{s1, s1 + B}, st2{s2, NST == 4 ? s2 + B : s2},
@@ -534,7 +540,7 @@ __global__ __launch_bounds__(512)
   __shared__ __attribute__((aligned(16))) float ssa0[256 * 4];
   __shared__ __attribute__((aligned(16))) float ssa1[256 * 4];
   f8_zero_outside<OutT>(p);
-  const F8Tile t = f8_find<256, 256>(p);
+  const F8Tile t = f8_find<256, 256, 32>(p);
   if (t.rows == 0) return;
   constexpr int B = 256 * F8_BK;
   const F8Stage st0{s0, s0 + B}, st1{s1, s1 + B};
@@ -559,7 +565,7 @@ __global__ __launch_bounds__(64 * NW) void f8_mm_few_kernel(F8Args p) {
   static_assert(128 % BN == 0, "one b scale per step");
   __shared__ __attribute__((aligned(16))) f32x4 red[NW * FM * FN * 64];
   f8_zero_outside<OutT>(p);
-  const F8Tile t = f8_find<BM, BN>(p);
+  const F8Tile t = f8_find<BM, BN, 1u << 26>(p);
   if (t.rows == 0) return;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -679,12 +685,12 @@ __global__ __launch_bounds__(64 * NW) void f8_mm_few_kernel(F8Args p) {
 }
 
 // An upper bound on the tiles: a group's last one may be partial, and there are
-// no more such groups than rows.
-mi_status f8_grid(const F8Args& p, int bm, int bn, const char* what, dim3* grid) {
+// no more such groups than rows.  Then 8 for every round of chunks of cm tiles.
+mi_status f8_grid(const F8Args& p, int bm, int bn, long cm, const char* what, dim3* grid) {
   long tiles = (static_cast<long>(p.m_rows) + bm - 1) / bm;
   if (p.m_indptr != nullptr) tiles += p.E < p.m_rows ? p.E : p.m_rows;
   tiles *= (p.n + bn - 1) / bn;
-  const long g = (tiles + 7) / 8 * 8;
+  const long g = (tiles + 7) / 8 * 8 + 8 * ((tiles + 8 * cm - 1) / (8 * cm));
   MI_REQUIRE(g < (1L << 31), "%s: problem too large", what);
   *grid = dim3(static_cast<unsigned>(g));
   return MI_OK;
@@ -703,10 +709,10 @@ bool f8_stream_b(const F8Args& p, int bm) {
          static_cast<int64_t>(p.E) * p.n * p.k >= (128LL << 20);
 }
 
-#define F8_LAUNCH(KERNEL_, BM_, BN_, THREADS_)                         \
+#define F8_LAUNCH(KERNEL_, BM_, BN_, CM_, THREADS_)                      \
   do {                                                                 \
     dim3 grid;                                                         \
-    const mi_status st = f8_grid(p, BM_, BN_, what, &grid);            \
+    const mi_status st = f8_grid(p, BM_, BN_, CM_, what, &grid);       \
     if (st != MI_OK) return st;                                        \
     hipLaunchKernelGGL((KERNEL_), grid, dim3(THREADS_), 0, stream, p); \
     return launch_status(what);                                        \
@@ -715,20 +721,21 @@ bool f8_stream_b(const F8Args& p, int bm) {
 template <int WM, int WN, int FM, int FN, int NST, typename OutT>
 mi_status f8_launch(const F8Args& p, hipStream_t stream, const char* what) {
   if (f8_stream_b(p, 16 * FM * WM))
-    F8_LAUNCH((f8_mm_kernel<WM, WN, FM, FN, NST, true, OutT>), 16 * FM * WM, 16 * FN * WN,
+    F8_LAUNCH((f8_mm_kernel<WM, WN, FM, FN, NST, true, OutT>), 16 * FM * WM, 16 * FN * WN, 64,
               64 * WM * WN);
-  F8_LAUNCH((f8_mm_kernel<WM, WN, FM, FN, NST, false, OutT>), 16 * FM * WM, 16 * FN * WN, 64 * WM * WN);
+  F8_LAUNCH((f8_mm_kernel<WM, WN, FM, FN, NST, false, OutT>), 16 * FM * WM, 16 * FN * WN, 64,
+            64 * WM * WN);
 }
 
 template <typename OutT>
 mi_status f8_launch_large(const F8Args& p, hipStream_t stream, const char* what) {
-  if (f8_stream_b(p, 256)) F8_LAUNCH((f8_mm_large_kernel<true, OutT>), 256, 256, 512);
-  F8_LAUNCH((f8_mm_large_kernel<false, OutT>), 256, 256, 512);
+  if (f8_stream_b(p, 256)) F8_LAUNCH((f8_mm_large_kernel<true, OutT>), 256, 256, 32, 512);
+  F8_LAUNCH((f8_mm_large_kernel<false, OutT>), 256, 256, 32, 512);
 }
 
 template <int FM, int FN, int NW, int P, typename OutT>
 mi_status f8_launch_few(const F8Args& p, hipStream_t stream, const char* what) {
-  F8_LAUNCH((f8_mm_few_kernel<FM, FN, NW, P, OutT>), 16 * FM, 16 * FN, 64 * NW);
+  F8_LAUNCH((f8_mm_few_kernel<FM, FN, NW, P, OutT>), 16 * FM, 16 * FN, 1L << 26, 64 * NW);
 }
 #undef F8_LAUNCH
 
