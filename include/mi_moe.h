@@ -469,7 +469,7 @@ MI_API int64_t mi_fp8_scale_cols(int64_t k); /* 4 * ceil(k / 512) */
  *   scales  block_rows 1: fp32 [batch, rows, cols]; block_rows 128: fp32 [batch,
  *           ceil(rows / 128), cols]; cols = mi_fp8_scale_cols(k); every entry written
  * Requirements: block_rows 1 or 128 (swiglu: 1), k % 16 == 0, all 16-byte
- * aligned; the outputs may not overlap x.  batch == 0 or rows == 0 is a no-op.
+ * aligned; the outputs may not overlap x or each other.  batch == 0 or rows == 0 is a no-op.
  */
 MI_API mi_status mi_fp8_quantize(const void* x, int64_t batch, int64_t rows, int64_t k,
                               mi_dtype dtype, int64_t block_rows, int swiglu, uint8_t* codes,
@@ -488,7 +488,7 @@ MI_API mi_status mi_fp8_quantize(const void* x, int64_t batch, int64_t rows, int
  *   norm_out      the same shape, or NULL (a router that reads the normed rows)
  *   codes, scales uint8 [num_tokens, hidden_size], fp32 [num_tokens, cols]
  * Requirements: hidden_size % 16 == 0, eps >= 0, all 16-byte aligned; no other
- * overlap of outputs with inputs.  num_tokens == 0 is a no-op.
+ * overlap of an output with another tensor.  num_tokens == 0 is a no-op.
  */
 MI_API mi_status mi_add_rmsnorm_fp8(const void* x, const void* residual, const void* weight,
                                  mi_dtype dtype, mi_dtype weight_dtype, int64_t num_tokens,
@@ -503,8 +503,10 @@ MI_API mi_status mi_add_rmsnorm_fp8(const void* x, const void* residual, const v
  *   a, a_scale   uint8 [m, k], fp32 [m, cols]            (1 x 128 scales)
  *   b, b_scale   uint8 [n, k], fp32 [ceil(n / 128), cols] (128 x 128 scales)
  *   out          out_dtype [m, n] (MI_BF16, MI_F16 or MI_F32)
- * Requirements: n % 16 == 0, k % 16 == 0, all 16-byte aligned.  k >= 2^22 or
- * n >= 2^20 returns MI_EUNSUPPORTED.  m == 0 is a no-op.
+ * The factor a_scale * b_scale is one fp32 product: where it leaves fp32's normal
+ * range (below 2^-126) the result has its precision.
+ * Requirements: n % 16 == 0, k % 16 == 0, all 16-byte aligned, out apart from the
+ * inputs.  k >= 2^22 or n >= 2^20 returns MI_EUNSUPPORTED.  m == 0 is a no-op.
  */
 MI_API mi_status mi_mm_fp8_block(const uint8_t* a, const float* a_scale, int64_t m, int64_t k,
                               const uint8_t* b, const float* b_scale, int64_t n, void* out,
@@ -535,9 +537,9 @@ MI_API mi_status mi_grouped_mm_fp8_block(const uint8_t* a, const float* a_scale,
  * mi_moe_permute_rows with respect to its token rows.
  *   rows     rows_dtype [num_rows, hidden_size];  perm int32 [num_tokens * top_k]
  *   weights  fp32 [num_tokens, top_k] or NULL
- *   out      out_dtype [num_tokens, hidden_size]; may not overlap rows
+ *   out      out_dtype [num_tokens, hidden_size]; may not overlap an input
  * Requirements: hidden_size % 8 == 0, rows and out 16-byte aligned, top_k >= 1,
- * num_tokens * top_k < 2^31.  num_tokens == 0 is a no-op.
+ * num_tokens * top_k < 2^31, num_rows < 2^31.  num_tokens == 0 is a no-op.
  */
 MI_API mi_status mi_moe_combine_rows(const void* rows, mi_dtype rows_dtype, int64_t num_rows,
                                   int64_t hidden_size, const int32_t* perm,
@@ -552,9 +554,9 @@ MI_API mi_status mi_moe_combine_rows(const void* rows, mi_dtype rows_dtype, int6
  *   inverse       int32 [num_rows], the permuted_idx_to_expanded_idx that goes with
  *                 perm: rows whose entry is negative get zeros, so every row is
  *                 written.  NULL: rows no slot points at are untouched
- *   grad_rows     rows_dtype [num_rows, hidden_size];  may not overlap the inputs
+ *   grad_rows     rows_dtype [num_rows, hidden_size]
  *   grad_weights  fp32 [num_tokens, top_k], or NULL (rows is then not read and may be)
- * Requirements: as above, num_rows < 2^31.  Two slots with the same row (an
+ * Requirements: as above; the outputs may not overlap an input or each other.  Two slots with the same row (an
  * invalid permutation) leave one of the two gradients there.
  */
 MI_API mi_status mi_moe_combine_rows_backward(

@@ -165,6 +165,7 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(
   }
 }
 
+int64_t size_of(mi_dtype d) { return d == MI_F32 ? 4 : 2; }
 bool known(mi_dtype d) { return d == MI_BF16 || d == MI_F16 || d == MI_F32; }
 // grid of 4-wavefront workgroups over `units`; the wavefronts stride over the rest
 dim3 grid_of(int64_t units) {
@@ -192,13 +193,18 @@ extern "C" mi_status mi_moe_combine_rows(const void* rows, mi_dtype rows_dtype, 
   MI_REQUIRE(hidden_size > 0 && hidden_size % 8 == 0 && hidden_size < (1LL << 30),
              "moe_combine_rows: hidden_size %% 8 == 0 required (got %lld)",
              (long long)hidden_size);
-  MI_REQUIRE(num_tokens >= 0 && top_k >= 1 && num_tokens <= (1LL << 31) / top_k - 1,
+  MI_REQUIRE(num_tokens >= 0 && top_k >= 1 && num_tokens <= ((1LL << 31) - 1) / top_k,
              "moe_combine_rows: num_tokens * top_k must be in [0, 2^31)");
   MI_REQUIRE(num_rows >= 0, "moe_combine_rows: num_rows must be >= 0");
   if (num_tokens == 0) return MI_OK;
   MI_REQUIRE(perm != nullptr && out != nullptr && (rows != nullptr || num_rows == 0),
              "moe_combine_rows: null pointer");
   MI_REQUIRE(aligned16(rows) && aligned16(out), "moe_combine_rows: rows and out must be 16-byte aligned");
+  MI_REQUIRE(num_rows < (1LL << 31), "moe_combine_rows: num_rows out of range");
+  const int64_t slots = num_tokens * top_k, ob = num_tokens * hidden_size * size_of(out_dtype);
+  MI_REQUIRE(!overlap(out, ob, rows, num_rows * hidden_size * size_of(rows_dtype)) &&
+                 !overlap(out, ob, perm, slots * 4) && !overlap(out, ob, weights, slots * 4),
+             "moe_combine_rows: out may not overlap an input");
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int h = static_cast<int>(hidden_size);
   const int upr = (h + (rows_dtype == MI_F32 ? 255 : 511)) / (rows_dtype == MI_F32 ? 256 : 512);
@@ -223,7 +229,7 @@ extern "C" mi_status mi_moe_combine_rows_backward(
   MI_REQUIRE(hidden_size > 0 && hidden_size % 8 == 0 && hidden_size < (1LL << 30),
              "moe_combine_rows_backward: hidden_size %% 8 == 0 required (got %lld)",
              (long long)hidden_size);
-  MI_REQUIRE(num_tokens >= 0 && top_k >= 1 && num_tokens <= (1LL << 31) / top_k - 1,
+  MI_REQUIRE(num_tokens >= 0 && top_k >= 1 && num_tokens <= ((1LL << 31) - 1) / top_k,
              "moe_combine_rows_backward: num_tokens * top_k must be in [0, 2^31)");
   MI_REQUIRE(num_rows >= 0 && num_rows < (1LL << 31),
              "moe_combine_rows_backward: num_rows out of range");
@@ -235,8 +241,19 @@ extern "C" mi_status mi_moe_combine_rows_backward(
              "moe_combine_rows_backward: grad_weights needs rows");
   MI_REQUIRE(aligned16(grad_out) && aligned16(rows) && aligned16(grad_rows),
              "moe_combine_rows_backward: grad_out, rows and grad_rows must be 16-byte aligned");
-  hipStream_t s = static_cast<hipStream_t>(stream);
   const int64_t slots = num_tokens * top_k;
+  const int64_t rb = num_rows * hidden_size * size_of(rows_dtype);
+  const int64_t gb = num_tokens * hidden_size * size_of(grad_dtype);
+  auto apart = [&](const void* o, int64_t n) {  // from every input
+    return !overlap(o, n, grad_out, gb) && !overlap(o, n, rows, rb) &&
+           !overlap(o, n, perm, slots * 4) && !overlap(o, n, inverse, num_rows * 4) &&
+           !overlap(o, n, weights, slots * 4);
+  };
+  MI_REQUIRE(apart(grad_rows, rb) && apart(grad_weights, slots * 4) &&
+                 !overlap(grad_rows, rb, grad_weights, slots * 4),
+             "moe_combine_rows_backward: grad_rows and grad_weights may not overlap an input or "
+             "each other");
+  hipStream_t s = static_cast<hipStream_t>(stream);
   const int64_t units = inverse != nullptr && num_rows > slots ? num_rows : slots;
   MI_BY_TYPE(rows_dtype, T, MI_BY_TYPE(grad_dtype, G, {
     hipLaunchKernelGGL((combine_backward_kernel<T, G>), grid_of(units), dim3(256), 0, s,

@@ -38,6 +38,12 @@ mi_status launch_status(const char* what);
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+// whether an bytes at a and bn bytes at b share any; a null pointer has none
+inline bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+  return p != 0 && q != 0 && p < q + bn && q < p + an;
+}
+
 // ---------------------------------------------------------------------------
 // device types
 // ---------------------------------------------------------------------------

@@ -686,12 +686,13 @@ __global__ __launch_bounds__(64 * NW) void f8_mm_few_kernel(F8Args p) {
 
 // An upper bound on the tiles: a group's last one may be partial, and there are
 // no more such groups than rows.  Then 8 for every round of chunks of cm tiles.
-mi_status f8_grid(const F8Args& p, int bm, int bn, long cm, const char* what, dim3* grid) {
+mi_status f8_grid(const F8Args& p, int bm, int bn, long cm, int threads, const char* what,
+                  dim3* grid) {
   long tiles = (static_cast<long>(p.m_rows) + bm - 1) / bm;
   if (p.m_indptr != nullptr) tiles += p.E < p.m_rows ? p.E : p.m_rows;
   tiles *= (p.n + bn - 1) / bn;
   const long g = (tiles + 7) / 8 * 8 + 8 * ((tiles + 8 * cm - 1) / (8 * cm));
-  MI_REQUIRE(g < (1L << 31), "%s: problem too large", what);
+  MI_REQUIRE(g * threads < (1L << 32), "%s: more tiles than one launch takes", what);
   *grid = dim3(static_cast<unsigned>(g));
   return MI_OK;
 }
@@ -712,7 +713,7 @@ bool f8_stream_b(const F8Args& p, int bm) {
 #define F8_LAUNCH(KERNEL_, BM_, BN_, CM_, THREADS_)                      \
   do {                                                                 \
     dim3 grid;                                                         \
-    const mi_status st = f8_grid(p, BM_, BN_, CM_, what, &grid);       \
+    const mi_status st = f8_grid(p, BM_, BN_, CM_, THREADS_, what, &grid); \
     if (st != MI_OK) return st;                                        \
     hipLaunchKernelGGL((KERNEL_), grid, dim3(THREADS_), 0, stream, p); \
     return launch_status(what);                                        \
@@ -802,6 +803,12 @@ mi_status f8_run(const F8Args& p, int64_t m_rows, int64_t k, int64_t n, int64_t 
   MI_REQUIRE(aligned16(p.a) && aligned16(p.b) && aligned16(p.sa) && aligned16(p.sb) &&
                  aligned16(p.out),
              "%s: a, b, their scales and out must be 16-byte aligned", what);
+  const int64_t sc = mi_fp8_scale_cols(k) * 4, ob = m_rows * n * (out_dtype == MI_F32 ? 4 : 2);
+  MI_REQUIRE(!overlap(p.out, ob, p.a, m_rows * k) && !overlap(p.out, ob, p.sa, m_rows * sc) &&
+                 !overlap(p.out, ob, p.b, batch * n * k) &&
+                 !overlap(p.out, ob, p.sb, batch * ((n + 127) / 128) * sc) &&
+                 !overlap(p.out, ob, p.m_indptr, (batch + 1) * 4),
+             "%s: out may not overlap an input", what);
   F8Args q = p;
   q.m_rows = static_cast<int>(m_rows);
   q.k = static_cast<int>(k);

@@ -132,15 +132,16 @@ __global__ __launch_bounds__(256) void f8_rows_kernel(const T* __restrict__ x, i
 // One 128 x 128 block per workgroup: thread (tid / 16, tid % 16) has 8 columns
 // of 8 rows, 16 rows apart, in registers between the reduction and the codes.
 template <typename T>
-__global__ __launch_bounds__(256) void f8_blocks_kernel(const T* __restrict__ x, int rows, int k,
-                                                        int sc, int nb, int kb,
+__global__ __launch_bounds__(256) void f8_blocks_kernel(const T* __restrict__ x, int64_t blocks,
+                                                        int rows, int k, int sc, int nb, int kb,
                                                         uint8_t* __restrict__ codes,
                                                         float* __restrict__ scales) {
   __shared__ uint32_t s_max[4];
   // workgroup ids go to the 8 XCDs in turn: each XCD gets a contiguous run of
   // blocks, so that its L2 joins the lines two neighbours write parts of
-  const int64_t total = static_cast<int64_t>(gridDim.x) / 8 * 8, per_xcd = total / 8;
-  const int64_t id = blockIdx.x;
+  const int64_t total = blocks / 8 * 8, per_xcd = total / 8;
+  const int64_t id = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
+  if (id >= blocks) return;
   const int64_t blk = id < total ? (id & 7) * per_xcd + (id >> 3) : id;
   const int cb = static_cast<int>(blk % kb);
   const int64_t rest = blk / kb;
@@ -192,13 +193,14 @@ __global__ __launch_bounds__(256) void f8_blocks_kernel(const T* __restrict__ x,
 template <typename T, int NC>
 __global__ __launch_bounds__(256) void rmsnorm_f8_kernel(const T* x, const T* r,
                                                          const void* __restrict__ w, bool w_f32,
-                                                         int h, int upr, float eps, T* res_out,
+                                                         int t, int h, int upr, float eps, T* res_out,
                                                          T* norm_out, uint8_t* __restrict__ codes,
                                                          float* __restrict__ scales) {
   __shared__ float s_sum[4];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t row = blockIdx.x;
+  const int64_t row = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
+  if (row >= t) return;
   x += row * h;
   if (r != nullptr) r += row * h;
   auto load_h = [&](int col, float* y) {
@@ -215,7 +217,7 @@ __global__ __launch_bounds__(256) void rmsnorm_f8_kernel(const T* x, const T* r,
   float keep[NC > 0 ? NC : 1][8];
   float ss = 0.f;
   const int nc = NC > 0 ? NC : (upr + 3) / 4;
-#pragma unroll
+#pragma unroll NC > 0 ? NC : 1
   for (int c = 0; c < nc; ++c) {
     float* y = keep[NC > 0 ? c : 0];
     load_h((c * 4 + wave) * 512 + lane * 8, y);
@@ -230,7 +232,7 @@ __global__ __launch_bounds__(256) void rmsnorm_f8_kernel(const T* x, const T* r,
   const float rstd = __fdiv_rn(1.f, __fsqrt_rn(ss / static_cast<float>(h) + eps));
   codes += row * h;
   scales += row * (4 * upr);
-#pragma unroll
+#pragma unroll NC > 0 ? NC : 1
   for (int c = 0; c < nc; ++c) {
     const int unit = c * 4 + wave, col = unit * 512 + lane * 8;
     if (unit >= upr) break;
@@ -258,6 +260,13 @@ __global__ __launch_bounds__(256) void rmsnorm_f8_kernel(const T* x, const T* r,
   }
 }
 
+// A workgroup each: a launch has fewer than 2^32 threads per dimension
+dim3 f8q_grid(int64_t n) {
+  constexpr int64_t X = 1 << 20;
+  return n <= X ? dim3(static_cast<unsigned>(n))
+                : dim3(static_cast<unsigned>(X), static_cast<unsigned>((n + X - 1) / X));
+}
+
 int64_t f8_units(int64_t k) { return (k + 511) / 512; }
 
 template <typename T>
@@ -278,9 +287,8 @@ mi_status launch_quantize(const void* x, int64_t batch, int64_t rows, int64_t k,
                          codes, scales);
   } else {
     const int64_t nb = (rows + 127) / 128, kb = (k + 127) / 128;
-    MI_REQUIRE(batch * nb * kb < (1LL << 31), "fp8_quantize: too many blocks");
-    hipLaunchKernelGGL((f8_blocks_kernel<T>), dim3(static_cast<unsigned>(batch * nb * kb)),
-                       dim3(256), 0, s, xp, static_cast<int>(rows), ki, 4 * upr,
+    hipLaunchKernelGGL((f8_blocks_kernel<T>), f8q_grid(batch * nb * kb), dim3(256), 0, s, xp,
+                       batch * nb * kb, static_cast<int>(rows), ki, 4 * upr,
                        static_cast<int>(nb), static_cast<int>(kb), codes, scales);
   }
   return launch_status("fp8_quantize");
@@ -292,9 +300,9 @@ mi_status launch_norm(const void* x, const void* r, const void* w, bool w_f32, i
                       float* scales, hipStream_t s) {
   const int upr = static_cast<int>(f8_units(h));
 #define MI_NORM_LAUNCH(NC_)                                                                     \
-  hipLaunchKernelGGL((rmsnorm_f8_kernel<T, NC_>), dim3(static_cast<unsigned>(t)), dim3(256), 0, \
-                     s, static_cast<const T*>(x), static_cast<const T*>(r), w, w_f32,           \
-                     static_cast<int>(h), upr, eps, static_cast<T*>(res_out),                   \
+  hipLaunchKernelGGL((rmsnorm_f8_kernel<T, NC_>), f8q_grid(t), dim3(256), 0, s,                 \
+                     static_cast<const T*>(x), static_cast<const T*>(r), w, w_f32,              \
+                     static_cast<int>(t), static_cast<int>(h), upr, eps, static_cast<T*>(res_out), \
                      static_cast<T*>(norm_out), codes, scales)
   if (upr <= 4) MI_NORM_LAUNCH(1);
   else if (upr <= 8) MI_NORM_LAUNCH(2);
@@ -302,11 +310,6 @@ mi_status launch_norm(const void* x, const void* r, const void* w, bool w_f32, i
   else MI_NORM_LAUNCH(0);
 #undef MI_NORM_LAUNCH
   return launch_status("add_rmsnorm_fp8");
-}
-
-bool overlap(const void* a, const void* b, int64_t bytes) {
-  const char *p = static_cast<const char*>(a), *q = static_cast<const char*>(b);
-  return p != nullptr && q != nullptr && p < q + bytes && q < p + bytes;
 }
 
 }  // namespace
@@ -333,6 +336,14 @@ extern "C" mi_status mi_fp8_quantize(const void* x, int64_t batch, int64_t rows,
   MI_REQUIRE(x != nullptr && codes != nullptr && scales != nullptr, "fp8_quantize: null pointer");
   MI_REQUIRE(aligned16(x) && aligned16(codes) && aligned16(scales),
              "fp8_quantize: x, codes and scales must be 16-byte aligned");
+  MI_REQUIRE(block_rows == 1 || batch * ((rows + 127) / 128) * ((k + 127) / 128) < (1LL << 31),
+             "fp8_quantize: too many blocks");
+  const int64_t values = batch * rows * k;
+  const int64_t xb = values * (dtype == MI_F32 ? 4 : 2) * (swiglu ? 2 : 1);
+  const int64_t sb = batch * ((rows + block_rows - 1) / block_rows) * mi_fp8_scale_cols(k) * 4;
+  MI_REQUIRE(!overlap(codes, values, x, xb) && !overlap(scales, sb, x, xb) &&
+                 !overlap(codes, values, scales, sb),
+             "fp8_quantize: codes and scales may not overlap x or each other");
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int br = static_cast<int>(block_rows);
   if (dtype == MI_BF16)
@@ -368,14 +379,25 @@ extern "C" mi_status mi_add_rmsnorm_fp8(const void* x, const void* residual, con
                  aligned16(norm_out) && aligned16(codes) && aligned16(scales),
              "add_rmsnorm_fp8: every tensor must be 16-byte aligned");
   // a stream written where another row is still to be read would race
-  const int64_t bytes = num_tokens * hidden_size * (dtype == MI_F32 ? 4 : 2);
-  MI_REQUIRE(residual_out == residual || !overlap(residual_out, residual, bytes),
+  const int64_t n = num_tokens * hidden_size, bytes = n * (dtype == MI_F32 ? 4 : 2);
+  MI_REQUIRE(residual_out == residual || !overlap(residual_out, bytes, residual, bytes),
              "add_rmsnorm_fp8: residual_out may be residual itself, not overlap it otherwise");
-  MI_REQUIRE(residual_out == x || !overlap(residual_out, x, bytes),
+  MI_REQUIRE(residual_out == x || !overlap(residual_out, bytes, x, bytes),
              "add_rmsnorm_fp8: residual_out may be x itself, not overlap it otherwise");
-  MI_REQUIRE(!overlap(norm_out, x, bytes) && !overlap(norm_out, residual, bytes) &&
-                 !overlap(norm_out, residual_out, bytes),
+  MI_REQUIRE(!overlap(norm_out, bytes, x, bytes) && !overlap(norm_out, bytes, residual, bytes) &&
+                 !overlap(norm_out, bytes, residual_out, bytes),
              "add_rmsnorm_fp8: norm_out may not overlap x, residual or residual_out");
+  const int64_t sb = num_tokens * mi_fp8_scale_cols(hidden_size) * 4;
+  const int64_t wb = hidden_size * (weight_dtype == MI_F32 ? 4 : 2);
+  MI_REQUIRE(!overlap(residual_out, bytes, weight, wb) && !overlap(norm_out, bytes, weight, wb) &&
+                 !overlap(codes, n, weight, wb) && !overlap(scales, sb, weight, wb),
+             "add_rmsnorm_fp8: no output may overlap weight");
+  for (const void* const other : {x, residual, static_cast<const void*>(residual_out),
+                                  static_cast<const void*>(norm_out)})
+    MI_REQUIRE(!overlap(codes, n, other, bytes) && !overlap(scales, sb, other, bytes),
+               "add_rmsnorm_fp8: codes and scales may not overlap another tensor");
+  MI_REQUIRE(!overlap(codes, n, scales, sb),
+             "add_rmsnorm_fp8: codes and scales may not overlap another tensor");
   hipStream_t s = static_cast<hipStream_t>(stream);
   const bool wf = weight_dtype == MI_F32;
   if (dtype == MI_BF16)

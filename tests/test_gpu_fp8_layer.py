@@ -240,3 +240,25 @@ def test_offsets_past_32_bits(gpu):
                                                  tw[t:t + 1].cpu())
         assert (np.abs(_np(gr[s]) - rr) <= (HALF[torch.bfloat16] + U) * np.abs(rr)).all(), t
         assert (np.abs(_np(gw[t:t + 1]) - rw) <= (k / 64 + 8) * U * mag + U * np.abs(rw)).all(), t
+
+
+def test_more_rows_than_one_launch_dimension(gpu):
+    """2^24 and a few rows, more than a launch has workgroups of 256 threads in one
+    dimension: the first and the last rows are those of a small call."""
+    t, h = 2 ** 24 + 5, 16
+    g = synth.gen(72, gpu)
+    x = torch.randn(t, h, generator=g, device=gpu, dtype=torch.bfloat16)
+    w = torch.randn(h, generator=g, device=gpu, dtype=torch.bfloat16)
+    parts = (slice(0, 300), slice(2 ** 20 - 40, 2 ** 20 + 40), slice(t - 300, t))
+    print("add_rmsnorm_fp8", flush=True)
+    codes, sc, ro = add_rmsnorm_fp8(x, w, x)
+    for r in parts:
+        c1, s1, r1 = add_rmsnorm_fp8(x[r], w, x[r])
+        assert torch.equal(codes[r].view(torch.uint8), c1.view(torch.uint8))
+        assert torch.equal(sc[r], s1) and torch.equal(ro[r], r1)
+    print("fp8_quantize, blocks", flush=True)
+    codes, sc = fp8_quantize(x[:, None], block_rows=128)
+    for r in parts:
+        c1, s1 = fp8_quantize(x[r][:, None], block_rows=128)
+        assert torch.equal(codes[r].view(torch.uint8), c1.view(torch.uint8))
+        assert torch.equal(sc[r], s1)

@@ -207,6 +207,49 @@ def test_combine_refusals():
     assert b(t=0, go=None) == _lib.MI_OK
 
 
+def test_outputs_apart_from_the_inputs():
+    """Every output against every tensor it may not share memory with: at its
+    start, at its last bytes, and (no refusal for that reason) right behind it."""
+    far = lambda i: FAKE + (i << 24)
+
+    def each(fn, base, outs, size, allowed=()):
+        for out in outs:
+            for other in size:
+                if other == out or (out, other) in allowed or (other, out) in allowed:
+                    continue
+                for at in (0, (size[other] - 1) // 16 * 16):
+                    assert "overlap" in _err(_call(fn, base, **{out: base[other] + at})), (out, other)
+                before = base[other] - -(-size[out] // 16) * 16 + 16
+                assert "overlap" in _err(_call(fn, base, **{out: before})), (out, other)
+
+    mm = dict(a=far(1), sa=far(2), m=5, k=128, b=far(3), sb=far(4), n=64, out=far(5),
+              dt=_lib.MI_BF16, stream=None)
+    sizes = dict(a=5 * 128, sa=5 * 16, b=64 * 128, sb=16, out=5 * 64 * 2)
+    each("mi_mm_fp8_block", mm, ["out"], sizes)
+    gmm = dict(a=far(1), sa=far(2), m=5, k=128, b=far(3), sb=far(4), e=4, n=64, ind=far(6), zero=0,
+               out=far(5), dt=_lib.MI_F32, stream=None)
+    each("mi_grouped_mm_fp8_block", gmm, ["out"],
+         dict(a=5 * 128, sa=5 * 16, b=4 * 64 * 128, sb=4 * 16, ind=20, out=5 * 64 * 4))
+    for glu in (0, 1):
+        q = dict(x=far(1), batch=1, rows=4, k=128, dt=_lib.MI_BF16, br=1, glu=glu, codes=far(2),
+                 scales=far(3), stream=None)
+        each("mi_fp8_quantize", q, ["codes", "scales"],
+             dict(x=4 * 128 * 2 * (1 + glu), codes=4 * 128, scales=4 * 16))
+    norm = dict(x=far(1), r=far(2), w=far(3), dt=_lib.MI_BF16, wdt=_lib.MI_F32, t=4, h=256,
+                eps=1e-6, ro=far(4), no=far(5), codes=far(6), scales=far(7), stream=None)
+    sizes = dict(x=2048, r=2048, w=1024, ro=2048, no=2048, codes=1024, scales=64)
+    each("mi_add_rmsnorm_fp8", norm, ["ro", "no", "codes", "scales"], sizes,
+         allowed=[("ro", "x"), ("ro", "r")])
+    comb = dict(rows=far(1), dt=_lib.MI_F16, p=8, h=64, perm=far(2), w=far(3), t=4, k=2, out=far(4),
+                odt=_lib.MI_F32, stream=None)
+    each("mi_moe_combine_rows", comb, ["out"], dict(rows=1024, perm=32, w=32, out=1024))
+    back = dict(go=far(1), gdt=_lib.MI_F32, rows=far(2), dt=_lib.MI_BF16, p=8, h=64, perm=far(3),
+                inv=far(4), w=far(5), t=4, k=2, gr=far(6), gw=far(7), stream=None)
+    each("mi_moe_combine_rows_backward", back, ["gr", "gw"],
+         dict(go=1024, rows=1024, perm=32, inv=32, w=32, gr=1024, gw=32))
+    assert "num_rows out of range" in _err(_call("mi_moe_combine_rows", comb, p=1 << 31))
+
+
 def test_python_refusals_before_the_gpu():
     """Shapes and types are checked first; then CPU tensors are refused."""
     f8 = torch.float8_e4m3fn
