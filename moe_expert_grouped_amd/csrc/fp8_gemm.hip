@@ -132,9 +132,10 @@ __device__ __forceinline__ F8Tile f8_find(const F8Args& p) {
   const uint32_t round = slot / chunk, L = (round * 8 + xcd) * chunk + slot % chunk;
   if (round >= rounds || L >= total) return f;
   int mt, ni;
-  // 256-row tiles: 4 together 227 us, 8 232, 16 238 at m 4096, n = k = 8192; 64-row
-  // tiles: 8 together 29.9, 16 31.0 at m 256
-  f8_order<BM >= 256 ? 4 : 8>(L, count, nt, mt, ni);
+  // 256-row tiles, 4, 6 and 8 together: m 4096, n = k = 8192 217, 213 and 219 us; 64
+  // experts, n = k = 2048, 512 rows each 169, 163 and 168; 64-row tiles: 8 together
+  // 29.9, 16 31.0 at m 256
+  f8_order<BM >= 256 ? 6 : 8>(L, count, nt, mt, ni);
   int owner = __builtin_popcountll(__ballot(upto <= static_cast<uint32_t>(mt)));
   f.e = owner * per;
   if (per > 1) {
@@ -214,11 +215,12 @@ __device__ __forceinline__ f32x4 f8_block(const F8Frag<false>& b, const F8Frag<f
   const f32x4 z = {0.f, 0.f, 0.f, 0.f};
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b.v, a.v, z, 0, 0, 0, 0, 0, 0);
 }
-__device__ __forceinline__ f32x4 f8_block(const F8Frag<true>& b, const F8Frag<true>& a) {
-  f32x4 d = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int c = 0; c < 4; ++c) d = __builtin_amdgcn_mfma_f32_16x16x32_f16(b.v[c], a.v[c], d, 0, 0, 0);
-  return d;
+// a quarter of it on top of d: the four of a block depend on each other, so those
+// of several blocks are issued in turn (64 experts, n = k = 4096, 256 rows each:
+// 637 -> 614 us; m 333, n 1744, k 2064: 10.2 -> 9.9)
+__device__ __forceinline__ f32x4 f8_quarter(const F8Frag<true>& b, const F8Frag<true>& a, int c,
+                                            f32x4 d) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(b.v[c], a.v[c], d, 0, 0, 0);
 }
 
 // at most N of this wavefront's loads are outstanding, its LDS reads have
@@ -249,8 +251,8 @@ struct F8Stage {
 //
 // A step is FM regions of one 16-row block of a each.  A region reads the
 // fragment of the region after the next and issues its FN MFMAs; beside each the
-// result of the last but one is added to the sums, so nothing is waited for
-// where it is made.  The step's one barrier stands before its last two regions,
+// result of the last but one is added to the sums (with fp32 outputs the last
+// region's), so nothing is waited for where it is made.  The step's one barrier stands before its last two regions,
 // whose operands are in registers by then: behind it the stage is free for the
 // loads of step kt+NST, and the next stage is complete (the wait leaves the loads
 // of the later ones in flight), so the last regions read the next step's first
@@ -358,7 +360,8 @@ __device__ __forceinline__ void f8_tile(const F8Args& p, F8Stage s0, F8Stage s1,
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  using Frag = F8Frag<sizeof(OutT) == 4>;
+  constexpr bool EXACT = sizeof(OutT) == 4;
+  using Frag = F8Frag<EXACT>;
   const int ablk = wm * FM, bblk = wn * FN;
   const int srd = (wm * FM * 16 + r) * 4;  // this lane's row of a scale buffer
   float sbv = 0.f;                         // b's scales of 64 steps
@@ -366,7 +369,15 @@ __device__ __forceinline__ void f8_tile(const F8Args& p, F8Stage s0, F8Stage s1,
   i32x8 fa0, fa1;                          // a's of the next two regions,
   float sa0, sa1;                          // and their scales
   float f = 0.f;                           // the factor of the last region
-  f32x4 d0 = {0.f, 0.f, 0.f, 0.f}, d1 = d0;  // the last two results, not yet added
+  // results not yet added: the last two, of fp32 outputs the last region's
+  constexpr int ND = EXACT ? FN : 2;
+  f32x4 d[ND];
+#pragma unroll
+  for (int j = 0; j < ND; ++j) d[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto add = [](f32x4& o, f32x4 v, float by) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) o[q] = __builtin_fmaf(v[q], by, o[q]);
+  };
 
   // A stage's loads go out PPR per region from the one behind the barrier on, over
   // half of the regions: all at once they hold up the MFMAs behind them, later
@@ -403,18 +414,36 @@ __device__ __forceinline__ void f8_tile(const F8Args& p, F8Stage s0, F8Stage s1,
         sa1 = (s & 3) < 3 ? sc[srd + 64 * (i + 2 - FM) + (s & 3) + 1]
                           : sc_nx[srd + 64 * (i + 2 - FM)];
       }
+      // the sum is complete at its asm, not later
+      if constexpr (EXACT) {
+        f32x4 dn[FN];
 #pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        const f32x4 d2 = f8_block(fbx[j], fax);
-        __builtin_amdgcn_sched_barrier(0);
-        if (i == FM - 1) fb[j] = frag(nx.b, bblk + j);
-        f32x4& o = acc[j >= 2 ? i : (i + FM - 1) % FM][(j + FN - 2) % FN];
+        for (int c = 0; c < 4; ++c)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) o[q] = __builtin_fmaf(d0[q], j >= 2 ? f : f_prev, o[q]);
-        asm volatile("" : "+v"(o));  // the sum is complete here, not later
-        d0 = d1;
-        d1 = d2;
+          for (int j = 0; j < FN; ++j)
+            dn[j] = f8_quarter(fbx[j], fax, c, c ? dn[j] : f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          if (i == FM - 1) fb[j] = frag(nx.b, bblk + j);
+          f32x4& o = acc[(i + FM - 1) % FM][j];
+          add(o, d[j], f_prev);
+          asm volatile("" : "+v"(o));
+          d[j] = dn[j];
+        }
         __builtin_amdgcn_sched_barrier(0);
+      } else {
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          const f32x4 d2 = f8_block(fbx[j], fax);
+          __builtin_amdgcn_sched_barrier(0);
+          if (i == FM - 1) fb[j] = frag(nx.b, bblk + j);
+          f32x4& o = acc[j >= 2 ? i : (i + FM - 1) % FM][(j + FN - 2) % FN];
+          add(o, d[0], j >= 2 ? f : f_prev);
+          asm volatile("" : "+v"(o));
+          d[0] = d[1];
+          d[1] = d2;
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
     }
   };
@@ -459,10 +488,7 @@ __device__ __forceinline__ void f8_tile(const F8Args& p, F8Stage s0, F8Stage s1,
   // workgroup's end
   __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    acc[FM - 1][FN - 2][q] = __builtin_fmaf(d0[q], f, acc[FM - 1][FN - 2][q]);
-    acc[FM - 1][FN - 1][q] = __builtin_fmaf(d1[q], f, acc[FM - 1][FN - 1][q]);
-  }
+  for (int j = 0; j < ND; ++j) add(acc[FM - 1][FN - ND + j], d[j], f);
 
   // acc[i][j][q]: row (wm FM + i) 16 + r, column (wn FN + j) 16 + 4 g + q.  The
   // wavefront's outputs go through its own part of the stages (free after the
@@ -639,12 +665,21 @@ __global__ __launch_bounds__(64 * NW) void f8_mm_few_kernel(F8Args p) {
     for (int i = 0; i < FM; ++i) {
       const Frag fa = frag(q.a[i][0], q.a[i][1]);
       const float f = q.s[i] * sb;
+      f32x4 d[FN];
+      if constexpr (sizeof(OutT) == 4) {
 #pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        const f32x4 d = f8_block(fb[j], fa);
+        for (int c = 0; c < 4; ++c)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) acc[i][j][c] = __builtin_fmaf(d[c], f, acc[i][j][c]);
+          for (int j = 0; j < FN; ++j)
+            d[j] = f8_quarter(fb[j], fa, c, c ? d[j] : f32x4{0.f, 0.f, 0.f, 0.f});
+      } else {
+#pragma unroll
+        for (int j = 0; j < FN; ++j) d[j] = f8_block(fb[j], fa);
       }
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[i][j][c] = __builtin_fmaf(d[j][c], f, acc[i][j][c]);
     }
   };
 #pragma unroll

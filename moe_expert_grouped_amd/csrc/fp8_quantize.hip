@@ -100,6 +100,10 @@ __device__ __forceinline__ void quantise_unit(const float* y, int col, int k, ui
   if ((col & 127) == 0) gst<float>(scales_row + (col >> 7), col < k ? s : 0.f);
 }
 
+// 1 x 128 blocks: a wavefront per unit.  Bound by memory: x is read once with
+// 16-byte loads (fp32: two), and a block's amax takes 4 exchanges among its 16
+// lanes, no LDS and no barrier.  65536 x 2048 of bf16 [gate | up]: 675 MB in
+// 131 us, 5.15 TB/s, the rate of a large copy (5.1).
 template <typename T, bool GLU>
 __global__ __launch_bounds__(256) void f8_rows_kernel(const T* __restrict__ x, int64_t units,
                                                       int k, int upr, uint8_t* __restrict__ codes,
@@ -130,7 +134,9 @@ __global__ __launch_bounds__(256) void f8_rows_kernel(const T* __restrict__ x, i
 }
 
 // One 128 x 128 block per workgroup: thread (tid / 16, tid % 16) has 8 columns
-// of 8 rows, 16 rows apart, in registers between the reduction and the codes.
+// of 8 rows, 16 rows apart, in registers between the reduction and the codes, so
+// x is read once.  Bound by memory: 8 x 2000 x 4112 of fp32, 329 MB in 64.5 us,
+// 5.1 TB/s, the rate of a large copy.
 template <typename T>
 __global__ __launch_bounds__(256) void f8_blocks_kernel(const T* __restrict__ x, int64_t blocks,
                                                         int rows, int k, int sc, int nb, int kb,
@@ -190,6 +196,12 @@ __global__ __launch_bounds__(256) void f8_blocks_kernel(const T* __restrict__ x,
 // the row's NC units per wavefront are kept in registers between the sum of
 // squares and the output; NC == 0: any length, x and r are read again (before
 // this thread overwrites its own part of the stream, which may be r itself).
+// One workgroup per row also where rows are few: the row's sum is then one barrier
+// away (one token of 4096: 3.2 us, the latency of a launch and two dependent passes
+// over the registers).  Many rows are bound by memory: 8192 x 7168 of bf16 with
+// both streams and y itself, 530 MB in 104 us, 5.1 TB/s, the rate of a large copy.
+// A row of up to 8192 values stays in registers; longer ones are read twice, the
+// second time mostly from L2.
 template <typename T, int NC>
 __global__ __launch_bounds__(256) void rmsnorm_f8_kernel(const T* x, const T* r,
                                                          const void* __restrict__ w, bool w_f32,
