@@ -236,37 +236,42 @@ __device__ __forceinline__ void f8_wait_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// the LDS rows of one step: the tile's rows of a, and of b
+// the LDS rows of one step: the tile's rows 0 .. 127 and 128 .. of a, and of b.
+// A pointer to one array, or to its half, is known at compile time wherever LDS is
+// read (the compiler then knows which of the loads in flight a read waits for; one
+// chosen at run time would wait for all).
 struct F8Stage {
-  uint8_t *a, *b;
+  uint8_t *a0, *a1, *b0, *b1;
 };
 
 // One tile of BM = 16 FM WM rows and BN = 16 FN WN columns; WM * WN wavefronts.
 // `rows` (1..BM) of the tile belong to the group.
 //
 // Staging: 8 rows of 128 bytes per DMA instruction straight into LDS, NST
-// stages.  Rows past the group or past n, and 16-byte chunks past k, load as
-// zeros.  a's scales of four steps (16 bytes a row) go into one of two small
-// LDS buffers, b's of 64 steps sit in one register, a lane each.
+// stages (two to four).  Rows past the group or past n, and 16-byte chunks past k,
+// load as zeros.  a's scales of four steps (16 bytes a row) go into one of two (with
+// three stages three) small LDS buffers, b's of 64 steps sit in one register, a lane
+// each.
 //
 // A step is FM regions of one 16-row block of a each.  A region reads the
 // fragment of the region after the next and issues its FN MFMAs; beside each the
 // result of the last but one is added to the sums (with fp32 outputs the last
-// region's), so nothing is waited for where it is made.  The step's one barrier stands before its last two regions,
-// whose operands are in registers by then: behind it the stage is free for the
-// loads of step kt+NST, and the next stage is complete (the wait leaves the loads
-// of the later ones in flight), so the last regions read the next step's first
-// fragments while their MFMAs run.
+// region's), so nothing is waited for where it is made.  The step's one barrier
+// stands before its last two regions, whose operands are in registers by then:
+// behind it the stage is free for the loads of step kt+NST, and the next stage is
+// complete (the wait leaves the loads of the later ones in flight), so the last
+// regions read the next step's first fragments while their MFMAs run.
 template <int WM, int WN, int FM, int FN, int NST, bool STREAM, typename OutT>
 __device__ __forceinline__ void f8_tile(const F8Args& p, F8Stage s0, F8Stage s1, F8Stage s2,
-                                        F8Stage s3, float* ssa0, float* ssa1, const F8Tile& t) {
+                                        F8Stage s3, float* ssa0, float* ssa1, float* ssa2,
+                                        uint8_t* reg, const F8Tile& t) {
   const int e = t.e, m0 = t.m0, rows = t.rows, n0 = t.n0;
   constexpr int NW = WM * WN, BM = 16 * FM * WM, BN = 16 * FN * WN;
   constexpr int NIA = BM / 8 / NW, NIB = BN / 8 / NW;  // DMA instructions per wavefront
   // the loads of the stages after the next may be in flight at a step's barrier
   // (the scales' among them, which are read two steps after their load at least)
   constexpr int FLY = (NST - 2) * (NIA + NIB);
-  static_assert((NST == 2 || NST == 4) && FLY < 64, "stages");
+  static_assert(NST >= 2 && NST <= 4 && FLY < 64, "stages");
   static_assert(NW % 4 == 0 && NIA * 8 * NW == BM && NIB * 8 * NW == BN, "tile");
   static_assert(BM % 64 == 0 && BM / 64 <= NW && 128 % (16 * FN) == 0 && FM >= 2 && FN >= 2, "tile");
   const int tid = threadIdx.x, lane = tid & 63;
@@ -281,9 +286,14 @@ __device__ __forceinline__ void f8_tile(const F8Args& p, F8Stage s0, F8Stage s1,
                                              static_cast<uint32_t>(cols) * k);
   const __amdgpu_buffer_rsrc_t sar = buf_rsrc(p.sa + static_cast<long>(m0) * p.sc,
                                               static_cast<uint32_t>(rows) * p.sc * 4);
-  // this wavefront's columns lie in one 128-column block of b
-  const int sbrow = min((n0 + wn * 16 * FN) / 128, p.nb - 1);
+  // Where a stage is in pieces every wavefront has rows in both: SPLIT_A half of its
+  // rows of a in 0 .. 127 and half in 128 .., SPLIT the same of its rows of b.  Else
+  // they are consecutive, and those of b are in one 128-column block.
+  constexpr bool SPLIT = NST == 3, SPLIT_A = BM == 256;
+  static_assert(!SPLIT || BN == 256, "split");
+  const int sbrow = SPLIT ? n0 / 128 : min((n0 + wn * 16 * FN) / 128, p.nb - 1);
   const float* sbp = p.sb + (static_cast<long>(e) * p.nb + sbrow) * p.sc;
+  const float* sbp1 = sbp + (SPLIT && sbrow + 1 < p.nb ? p.sc : 0);
 
   // DMA instruction i fills LDS rows 8 (NW i + wave) ..: lane l takes row l / 8
   // of them and chunk (l % 8) ^ f8_swz(row)
@@ -320,12 +330,15 @@ __device__ __forceinline__ void f8_tile(const F8Args& p, F8Stage s0, F8Stage s1,
     for (int i = 0; i < NI; ++i) {
       if (i < first || i >= first + count) continue;
       if (i < NIA)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, f8_lds(st.a + (NW * i + wave) * 1024), 16,
-                                                 va[i < NIA ? i : 0] | drop, so, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            ar, f8_lds(NW * i < 16 ? st.a0 + (NW * i + wave) * 1024
+                                   : st.a1 + (NW * i - 16 + wave) * 1024),
+            16, va[i < NIA ? i : 0] | drop, so, 0, 0);
       else
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            br, f8_lds(st.b + (NW * (i - NIA) + wave) * 1024), 16,
-            vb[i < NIA ? 0 : i - NIA] | drop, so, 0, STREAM ? 2 : 0);
+            br, f8_lds(NW * (i - NIA) < 16 ? st.b0 + (NW * (i - NIA) + wave) * 1024
+                                           : st.b1 + (NW * (i - NIA) - 16 + wave) * 1024),
+            16, vb[i < NIA ? 0 : i - NIA] | drop, so, 0, STREAM ? 2 : 0);
     }
   };
   // 64 rows' scales per wavefront; wavefronts past the tile's rows load the same again
@@ -362,13 +375,22 @@ __device__ __forceinline__ void f8_tile(const F8Args& p, F8Stage s0, F8Stage s1,
 
   constexpr bool EXACT = sizeof(OutT) == 4;
   using Frag = F8Frag<EXACT>;
-  const int ablk = wm * FM, bblk = wn * FN;
-  const int srd = (wm * FM * 16 + r) * 4;  // this lane's row of a scale buffer
-  float sbv = 0.f;                         // b's scales of 64 steps
+  auto frag_a = [&](const F8Stage& st, int i) {
+    return SPLIT_A ? frag(i < FM / 2 ? st.a0 : st.a1, wm * (FM / 2) + i % (FM / 2))
+                   : frag(st.a0, wm * FM + i);
+  };
+  // block j of this wavefront's columns
+  auto frag_b = [&](const F8Stage& st, int j) {
+    return SPLIT ? frag(j < FN / 2 ? st.b0 : st.b1, wn * (FN / 2) + j % (FN / 2))
+                 : frag(st.b0, wn * FN + j);
+  };
+  const int srd = (wm * (SPLIT_A ? 64 : FM * 16) + r) * 4;  // this lane's row of a scale buffer
+  auto soff = [](int i) { return SPLIT_A && i >= FM / 2 ? 512 + 64 * (i - FM / 2) : 64 * i; };
+  float sbv = 0.f, sbv1 = 0.f;             // b's scales of 64 steps
   i32x8 fb[FN];                            // b's fragments of the step
   i32x8 fa0, fa1;                          // a's of the next two regions,
   float sa0, sa1;                          // and their scales
-  float f = 0.f;                           // the factor of the last region
+  float f = 0.f, f1 = 0.f;                 // the factors of the last region, by block of b
   // results not yet added: the last two, of fp32 outputs the last region's
   constexpr int ND = EXACT ? FN : 2;
   f32x4 d[ND];
@@ -385,10 +407,15 @@ __device__ __forceinline__ void f8_tile(const F8Args& p, F8Stage s0, F8Stage s1,
   constexpr int PPR = (2 * NI + FM - 1) / FM;
   auto step = [&](auto S, const F8Stage& pv, const F8Stage& st, const F8Stage& nx, int kt) {
     constexpr int s = decltype(S)::value;
-    float* const sc = s < 4 ? ssa0 : ssa1;
-    float* const sc_nx = s < 4 ? ssa1 : ssa0;
+    // with three stages the unrolled steps are 12 and the scale buffers three
+    float* const sc = s < 4 ? ssa0 : s < 8 ? ssa1 : ssa2;
+    float* const sc_nx = s < 4 ? ssa1 : s < 8 && NST == 3 ? ssa2 : ssa0;
     const float sb = __builtin_bit_cast(
         float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sbv), block(kt) & 63));
+    const float sb1 =
+        !SPLIT ? sb
+               : __builtin_bit_cast(float, __builtin_amdgcn_readlane(
+                                               __builtin_bit_cast(int, sbv1), block(kt) & 63));
     Frag fbx[FN];
 #pragma unroll
     for (int j = 0; j < FN; ++j) fbx[j] = Frag(fb[j]);
@@ -402,15 +429,16 @@ __device__ __forceinline__ void f8_tile(const F8Args& p, F8Stage s0, F8Stage s1,
       if (i >= R0) dma(st, kt + NST, (i - R0) * PPR, PPR);
       else if ((i + 2) * PPR < NI) dma(pv, kt + NST - 1, (i + 2) * PPR, PPR);
       const Frag fax(fa0);
-      const float f_prev = f;
+      const float f_prev = f, f1_prev = f1;
       f = sa0 * sb;
+      f1 = SPLIT ? sa0 * sb1 : f;
       fa0 = fa1;
       sa0 = sa1;
       if (i < FM - 2) {
-        fa1 = frag(st.a, ablk + i + 2);
-        sa1 = sc[srd + 64 * (i + 2) + (s & 3)];
+        fa1 = frag_a(st, i + 2);
+        sa1 = sc[srd + soff(i + 2) + (s & 3)];
       } else {
-        fa1 = frag(nx.a, ablk + i + 2 - FM);
+        fa1 = frag_a(nx, i + 2 - FM);
         sa1 = (s & 3) < 3 ? sc[srd + 64 * (i + 2 - FM) + (s & 3) + 1]
                           : sc_nx[srd + 64 * (i + 2 - FM)];
       }
@@ -424,9 +452,9 @@ __device__ __forceinline__ void f8_tile(const F8Args& p, F8Stage s0, F8Stage s1,
             dn[j] = f8_quarter(fbx[j], fax, c, c ? dn[j] : f32x4{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
-          if (i == FM - 1) fb[j] = frag(nx.b, bblk + j);
+          if (i == FM - 1) fb[j] = frag_b(nx, j);
           f32x4& o = acc[(i + FM - 1) % FM][j];
-          add(o, d[j], f_prev);
+          add(o, d[j], SPLIT && j >= FN / 2 ? f1_prev : f_prev);
           asm volatile("" : "+v"(o));
           d[j] = dn[j];
         }
@@ -436,9 +464,10 @@ __device__ __forceinline__ void f8_tile(const F8Args& p, F8Stage s0, F8Stage s1,
         for (int j = 0; j < FN; ++j) {
           const f32x4 d2 = f8_block(fbx[j], fax);
           __builtin_amdgcn_sched_barrier(0);
-          if (i == FM - 1) fb[j] = frag(nx.b, bblk + j);
+          if (i == FM - 1) fb[j] = frag_b(nx, j);
           f32x4& o = acc[j >= 2 ? i : (i + FM - 1) % FM][(j + FN - 2) % FN];
-          add(o, d[0], j >= 2 ? f : f_prev);
+          const bool second = SPLIT && (j + FN - 2) % FN >= FN / 2;
+          add(o, d[0], j >= 2 ? (second ? f1 : f) : (second ? f1_prev : f_prev));
           asm volatile("" : "+v"(o));
           d[0] = d[1];
           d[1] = d2;
@@ -450,57 +479,66 @@ __device__ __forceinline__ void f8_tile(const F8Args& p, F8Stage s0, F8Stage s1,
 
   // b's scales of the 64 blocks that block kb is one of; before the stages, as a
   // wait for them would be a wait for everything before them
-  auto load_sb = [&](int kb) { sbv = sbp[min((kb & ~63) + lane, p.sc - 1)]; };
+  auto load_sb = [&](int kb) {
+    const int c = min((kb & ~63) + lane, p.sc - 1);
+    sbv = sbp[c];
+    if constexpr (SPLIT) sbv1 = sbp1[c];
+  };
   load_sb(block(0));
   dma(s0, 0, 0, NI);
   dma_scales(ssa0, 0);
-  if constexpr (NST == 4) {
-    dma(s1, 1, 0, NI);
-    dma(s2, 2, 0, NI);
-  }
+  if constexpr (NST >= 3) dma(s1, 1, 0, NI);
+  if constexpr (NST == 4) dma(s2, 2, 0, NI);
   f8_wait_barrier<FLY>();
-  dma(NST == 4 ? s3 : s1, NST - 1, 0, 2 * PPR);  // the rest in step 0
-  fa0 = frag(s0.a, ablk);
-  fa1 = frag(s0.a, ablk + 1);
+  dma(NST == 4 ? s3 : NST == 3 ? s2 : s1, NST - 1, 0, 2 * PPR);  // the rest in step 0
+  fa0 = frag_a(s0, 0);
+  fa1 = frag_a(s0, 1);
   sa0 = ssa0[srd];
   sa1 = ssa0[srd + 64];
 #pragma unroll
-  for (int j = 0; j < FN; ++j) fb[j] = frag(s0.b, bblk + j);
-  for (int kt = 0; kt < KT; kt += 8) {
-    if (KT > 64 && kt > 0 && (block(kt) & 63) < 4) load_sb(block(kt));
-#define F8_STEP(S_, PV_, ST_, NX_)                                  \
-  step(std::integral_constant<int, S_>{}, PV_, ST_, NX_, kt + S_);   \
+  for (int j = 0; j < FN; ++j) fb[j] = frag_b(s0, j);
+  const F8Stage* const sts[4] = {&s0, &s1, &s2, &s3};
+  constexpr int UNROLL = NST == 3 ? 12 : 8;
+  for (int kt = 0; kt < KT; kt += UNROLL) {
+#define F8_STEP(S_)                                                                       \
+  if (S_ % 4 == 0 && KT > 64 && kt + S_ > 0 && (block(kt + S_) & 63) < 4)                 \
+    load_sb(block(kt + S_));                                                              \
+  step(std::integral_constant<int, S_>{}, *sts[(S_ + NST - 1) % NST], *sts[S_ % NST],     \
+       *sts[(S_ + 1) % NST], kt + S_);                                                    \
   if (kt + S_ + 1 >= KT) break;
-    const F8Stage& t2 = NST == 4 ? s2 : s0;
-    const F8Stage& t3 = NST == 4 ? s3 : s1;
-    F8_STEP(0, t3, s0, s1)
-    F8_STEP(1, s0, s1, t2)
-    F8_STEP(2, s1, t2, t3)
-    F8_STEP(3, t2, t3, s0)
-    if (KT > 64 && (block(kt + 4) & 63) < 4) load_sb(block(kt + 4));
-    F8_STEP(4, t3, s0, s1)
-    F8_STEP(5, s0, s1, t2)
-    F8_STEP(6, s1, t2, t3)
-    F8_STEP(7, t2, t3, s0)
+    F8_STEP(0)
+    F8_STEP(1)
+    F8_STEP(2)
+    F8_STEP(3)
+    F8_STEP(4)
+    F8_STEP(5)
+    F8_STEP(6)
+    F8_STEP(7)
+    if constexpr (UNROLL == 12) {
+      F8_STEP(8)
+      F8_STEP(9)
+      F8_STEP(10)
+      F8_STEP(11)
+    }
 #undef F8_STEP
   }
   // the loads of the steps past the last write (zeros) to LDS: not after this
   // workgroup's end
   __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
 #pragma unroll
-  for (int j = 0; j < ND; ++j) add(acc[FM - 1][FN - ND + j], d[j], f);
+  for (int j = 0; j < ND; ++j)
+    add(acc[FM - 1][FN - ND + j], d[j], SPLIT && FN - ND + j >= FN / 2 ? f1 : f);
 
-  // acc[i][j][q]: row (wm FM + i) 16 + r, column (wn FN + j) 16 + 4 g + q.  The
-  // wavefront's outputs go through its own part of the stages (free after the
-  // barrier) so that it stores whole runs of RB bytes of a row, 16 bytes a lane,
-  // instead of 8 bytes from each of 64 places.  16-byte chunk c of a row sits at
+  // acc[i][j][q]: row 16 i + r, column 16 j + 4 g + q of the wavefront's.  Its
+  // outputs go through its own part of the stages (`reg`, free after the barrier)
+  // so that it stores whole runs of RB bytes of a row (SPLIT: two of half), 16 bytes
+  // a lane, instead of 8 bytes from each of 64 places.  16-byte chunk c of a row sits at
   // slot c ^ (row % CPR).  The stores are streaming (non-temporal): they cover
   // whole 64-byte pieces at least and the outputs do not push operands out of L2
   // (skewed experts: 817 us with 8-byte stores, 741 staged, 736 streaming).
   constexpr int ES = sizeof(OutT), RB = 16 * FN * ES, CPR = RB / 16, REG = 16 * FM * RB;
-  static_assert(NW / 2 * REG <= (BM + BN) * F8_BK && 64 % CPR == 0, "epilogue");
+  static_assert(REG <= 16 * 1024 && 64 % CPR == 0, "epilogue");
   f8_wait_barrier<0>();
-  uint8_t* const reg = (wave < NW / 2 ? s0.a : s1.a) + wave % (NW / 2) * REG;
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -519,10 +557,12 @@ __device__ __forceinline__ void f8_tile(const F8Args& p, F8Stage s0, F8Stage s1,
                static_cast<uint32_t>(rows) * n * ES);
   constexpr int RPI = 64 / CPR;  // rows per store
   const int pr = lane / CPR, pc = lane % CPR;
-  const int col = wn * 16 * FN + pc * (16 / ES);
+  const int lc = pc * (16 / ES);
+  const int col = SPLIT ? wn * 8 * FN + lc + (lc < 8 * FN ? 0 : 128 - 8 * FN) : wn * 16 * FN + lc;
 #pragma unroll
   for (int r0 = 0; r0 < 16 * FM; r0 += RPI) {
-    const int lrow = r0 + pr, row = wm * FM * 16 + lrow;
+    const int lrow = r0 + pr;
+    const int row = SPLIT_A ? wm * 64 + lrow + (lrow & 64) : wm * FM * 16 + lrow;
     const u32x4 v = *reinterpret_cast<const u32x4*>(reg + lrow * RB + (pc ^ (lrow % CPR)) * 16);
     __builtin_amdgcn_raw_buffer_store_b128(
         v, orsrc, row < rows && col < cols ? (static_cast<uint32_t>(row) * n + n0 + col) * ES : F8_OUT,
@@ -546,39 +586,57 @@ __global__ __launch_bounds__(64 * WM * WN)
   f8_zero_outside<OutT>(p);
   const F8Tile t = f8_find<BM, BN, 64>(p);  // two workgroups per CU
   if (t.rows == 0) return;
+  static_assert(BN <= 128, "halves");
   constexpr int B = BM * F8_BK;  // b's rows follow a's
-  const F8Stage st0{s0, s0 + B}, st1{s1, s1 + B}, st2{s2, NST == 4 ? s2 + B : s2},
-      st3{s3, NST == 4 ? s3 + B : s3};
+  static_assert(BM <= 128, "halves");
+  auto stage = [](uint8_t* s) { return F8Stage{s, s, s + B, s + B}; };
+  const F8Stage st0 = stage(s0), st1 = stage(s1), st2 = NST == 4 ? stage(s2) : st0,
+                st3 = NST == 4 ? stage(s3) : st1;
+  // a wavefront's part of the stages for its outputs
+  constexpr int NW = WM * WN, REG = 16 * FM * 16 * FN * sizeof(OutT);
+  static_assert(NW / 2 * REG <= STAGE, "epilogue");
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  uint8_t* const reg = (wave < NW / 2 ? s0 : s1) + wave % (NW / 2) * REG;
   if constexpr (FM >= 4) {
     if (t.rows <= BM / 2) {  // a group's last tile: half the work
-      f8_tile<WM, WN, FM / 2, FN, NST, STREAM, OutT>(p, st0, st1, st2, st3, ssa0, ssa1, t);
+      f8_tile<WM, WN, FM / 2, FN, NST, STREAM, OutT>(p, st0, st1, st2, st3, ssa0, ssa1, ssa0, reg,
+                                                     t);
       return;
     }
   }
-  f8_tile<WM, WN, FM, FN, NST, STREAM, OutT>(p, st0, st1, st2, st3, ssa0, ssa1, t);
+  f8_tile<WM, WN, FM, FN, NST, STREAM, OutT>(p, st0, st1, st2, st3, ssa0, ssa1, ssa0, reg, t);
 }
 
 // 256 x 256 tiles; a group's last tile, where it has at most 128 or 64 rows, does a
 // half or a quarter of the work.  It keeps its place among the group's tiles,
-// which share b's panels in L2.
+// which share b's panels in L2.  Such a low tile's step is shorter than its loads
+// take, so it has three stages of 48 KB where the tall one has two of 64 (128
+// experts, n 7168, k 2048, of 128 rows each 424 -> 392 us, of very unequal rows
+// 714 -> 705): LDS arrays that make up either.
 template <bool STREAM, typename OutT>
 __global__ __launch_bounds__(512)
     __attribute__((amdgpu_waves_per_eu(2, 2))) void f8_mm_large_kernel(F8Args p) {
-  __shared__ __attribute__((aligned(16))) uint8_t s0[512 * F8_BK];
-  __shared__ __attribute__((aligned(16))) uint8_t s1[512 * F8_BK];
-  __shared__ __attribute__((aligned(16))) float ssa0[256 * 4];
-  __shared__ __attribute__((aligned(16))) float ssa1[256 * 4];
+  constexpr int Q = 128 * F8_BK;  // 128 rows
+  __shared__ __attribute__((aligned(16))) uint8_t s0[3 * Q], s1[3 * Q], t0[Q], t1[Q], u[Q];
+  __shared__ __attribute__((aligned(16))) float ssa0[256 * 4], ssa1[256 * 4], ssa2[128 * 4];
   f8_zero_outside<OutT>(p);
   const F8Tile t = f8_find<256, 256, 32>(p);
   if (t.rows == 0) return;
-  constexpr int B = 256 * F8_BK;
-  const F8Stage st0{s0, s0 + B}, st1{s1, s1 + B};
-  if (t.rows > 128)
-    f8_tile<2, 4, 8, 4, 2, STREAM, OutT>(p, st0, st1, st0, st1, ssa0, ssa1, t);
-  else if (t.rows > 64)
-    f8_tile<2, 4, 4, 4, 2, STREAM, OutT>(p, st0, st1, st0, st1, ssa0, ssa1, t);
-  else
-    f8_tile<1, 8, 4, 2, 2, STREAM, OutT>(p, st0, st1, st0, st1, ssa0, ssa1, t);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  uint8_t* const reg = wave < 3   ? s0 + wave * Q
+                       : wave < 6 ? s1 + (wave - 3) * Q
+                                  : (wave < 7 ? t0 : t1);
+  if (t.rows > 128) {
+    const F8Stage st0{s0, t0, s0 + Q, s0 + 2 * Q}, st1{s1, t1, s1 + Q, s1 + 2 * Q};
+    f8_tile<2, 4, 8, 4, 2, STREAM, OutT>(p, st0, st1, st0, st1, ssa0, ssa1, ssa0, reg, t);
+  } else {
+    const F8Stage st0{s0, s0, s0 + Q, s0 + 2 * Q}, st1{s1, s1, s1 + Q, s1 + 2 * Q},
+        st2{u, u, t0, t1};
+    if (t.rows > 64)
+      f8_tile<2, 4, 4, 4, 3, STREAM, OutT>(p, st0, st1, st2, st0, ssa0, ssa1, ssa2, reg, t);
+    else
+      f8_tile<1, 8, 4, 2, 3, STREAM, OutT>(p, st0, st1, st2, st0, ssa0, ssa1, ssa2, reg, t);
+  }
 }
 
 // ---------------------------------------------------------------------------

@@ -181,6 +181,56 @@ def test_grouped_against_oracle(gpu, indptr, m, n, k):
                str(indptr))
 
 
+# (m_indptr or None, m, n, k): enough tiles of 256 x 256 to fill the chip, groups
+# that end in tiles of every height, more than 64 blocks of k and a last one of 16,
+# a last panel of one 128-column block and of a little more
+LARGE = [
+    ([3, 703, 803, 833, 833, 1000], 1004, 9872, 8704),
+    ([0, 700, 828, 892, 892, 1000], 1000, 9856, 8208),
+    ([0, 1500, 1628, 1692, 6000], 6000, 2064, 528),
+    ([0, 257, 300, 300, 1100], 1101, 9984, 144),
+    (None, 3400, 3984, 400),
+    (None, 2500, 5008, 8464),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32], ids=str)
+@pytest.mark.parametrize("indptr,m,n,k", LARGE, ids=str)
+def test_large_tiles_against_oracle(gpu, indptr, m, n, k, dtype):
+    """The rows at the ends of every tile and the columns at the ends of some panels."""
+    print(f"large tiles {indptr} rows {m} n {n} k {k} {dtype}", flush=True)
+    g = synth.gen(m + n + k, gpu)
+    E = 1 if indptr is None else len(indptr) - 1
+    code = lambda *shape: (torch.randint(0, 0x7F, shape, generator=g, device=gpu, dtype=torch.uint8) +
+                           128 * torch.randint(0, 2, shape, generator=g, device=gpu, dtype=torch.uint8))
+    small = 2.0 ** -8 if dtype == torch.float16 else 1.0
+    scale = lambda *lead: small * torch.rand(*lead, fp8_scale_cols(k), generator=g, device=gpu)
+    a, b, sa, sb = code(m, k), code(E, n, k), scale(m), scale(E, -(-n // 128))
+    out = torch.full((m, n), 7.0, dtype=dtype, device=gpu)
+    if indptr is None:
+        mm_fp8_block(a.view(F8), b[0].view(F8), sa, sb[0], out=out, out_dtype=dtype)
+        groups = [(0, m)]
+    else:
+        grouped_mm_fp8_block(a.view(F8), sa, b.view(F8), sb,
+                             torch.tensor(indptr, dtype=torch.int32, device=gpu), out=out,
+                             out_dtype=dtype)
+        groups = list(zip(indptr[:-1], indptr[1:]))
+        assert (out[:indptr[0]] == 7.0).all() and (out[indptr[-1]:] == 7.0).all()
+    torch.cuda.synchronize()
+    blocks = sorted({0, 1, 2, 3, n // 256, -(-n // 128) - 2, -(-n // 128) - 1})
+    for e, (lo, hi) in enumerate(groups):
+        rows = sorted({r for t in range(lo, hi, 64) for r in (t, t + 17, t + 63) if r < hi} |
+                      ({hi - 1} if hi > lo else set()))[-60:]
+        if not rows:
+            continue
+        for blk in blocks:
+            cols = slice(blk * 128, min(blk * 128 + 128, n))
+            ops = (_u8(a[rows]), _np(sa[rows]), _u8(b[e, cols]), _np(sb[e, blk:blk + 1]))
+            ref, mag = F.mm_fp8_block(*ops)
+            _check(out[rows][:, cols], ref, mag, F.group_maxima(*ops), k, dtype,
+                   f"group {e} block {blk}")
+
+
 def test_grouped_many_experts_and_fresh_out(gpu):
     """1024 experts, most of them empty; a fresh out is zero outside the groups."""
     g = synth.gen(6)
