@@ -863,13 +863,16 @@ mi_status f8_dispatch(const F8Args& p, hipStream_t s, const char* what) {
               : tiles(64, 64) <= 512)
     return f8_launch<2, 2, 2, 2, 4, OutT>(p, s, what);
   if constexpr (sizeof(OutT) == 2) {
-    // 256 x 256 tiles have the fewest bytes per MFMA, but have to fill the chip
-    // (m 4096: 222 against 286; m 1024, 128 such tiles: 81 against 66; 8 groups of
-    // 192 rows, n = k = 4096: 56 against 48, of 256 rows 58 against 75).  A group has
-    // half a tile more than its rows fill; below 104 rows the 128-row tiles are as
-    // good (64 experts, n 2048, k 4096, 96 rows: 105 and 108)
-    const long large = grouped ? E * (2 * rows + 256) / 512 * ((n + 255) / 256) : tiles(256, 256);
-    if (rows >= 104 && large >= 192) return f8_launch_large<OutT>(p, s, what);
+    // 256 x 256 tiles have the fewest bytes per MFMA, but one runs per CU, not two.
+    // They are taken where the 128 x 128 tiles need more than one round (n = k = 4096:
+    // m 2048, one round of 512, 44 against 35, m 2304 44 against 53; 16 groups of 192
+    // rows 70 against 91; where very unequal groups fill a second round of the large
+    // tiles they lose: 12 of 256 rows on average, k 2048, 55 against 45).  A group has
+    // half a tile more than its rows fill.  Below 56 rows the 128-row tiles are better
+    // (64 experts, n 2048, k 4096: 80 rows 97 against 99, 48 rows 89 against 87).
+    const long m_tiles = grouped ? E * (2 * rows + 128) / 256 : (rows + 127) / 128;
+    if (rows >= 56 && m_tiles * ((n + 127) / 128) > 512)
+      return f8_launch_large<OutT>(p, s, what);
   }
   // fp32 outputs stay here: fp16 fragments of a 256-row tile would not fit the
   // registers (m 4096: 450; with 128 x 64 tiles 569)
