@@ -633,7 +633,8 @@ def fp8_scale_cols(k: int) -> int:
 
 def _fp8_out(name, x, codes, scales, codes_shape, scale_shape):
     if codes is None:
-        codes = torch.empty(codes_shape, dtype=_F8, device=x.device)
+        codes = (torch.empty_like(x, dtype=_F8) if x.shape == codes_shape and x.is_contiguous()
+                 else torch.empty(codes_shape, dtype=_F8, device=x.device))
     elif not (codes.dtype == _F8 and codes.shape == codes_shape and codes.is_contiguous()):
         raise ValueError(f"{name}: codes must be contiguous float8_e4m3fn of shape "
                          f"{tuple(codes_shape)}")
