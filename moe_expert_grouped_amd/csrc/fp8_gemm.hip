@@ -71,7 +71,8 @@ __device__ __forceinline__ uint32_t f8_scan(uint32_t v) {
   return v;
 }
 
-// m-tile and n-panel of the L-th tile: GM m-tiles sweep the n-panels together
+// m-tile and n-panel of the L-th tile of a group of `count` m-tiles: GM of them
+// sweep the n-panels together
 template <uint32_t GM>
 __device__ __forceinline__ void f8_order(uint32_t L, uint32_t count, uint32_t nt, int& mt,
                                          int& ni) {
@@ -81,7 +82,8 @@ __device__ __forceinline__ void f8_order(uint32_t L, uint32_t count, uint32_t nt
   const uint32_t gsize = min(count - first, GM);
   const uint32_t in_grp = L - grp * span;
   // The m-tiles turn by one every 8 panels: consecutive tiles of one place then
-  // are not all of the same height (skewed experts 790 -> 780 us with 128-row tiles)
+  // are not all of the same height (64 experts of about 256 rows, n = k = 4096: 374
+  // and 370 us)
   ni = in_grp / gsize;
   mt = first + (in_grp % gsize + ni / 8) % gsize;
 }
@@ -98,6 +100,9 @@ struct F8Tile {
 // full tiles: 128 experts, n 2048, k 7168, 4096 rows of very unequal groups 383
 // against 361 us, n 1536 with 16384 rows 413 against 402; equal groups lose a
 // little by the chunks (64 experts, n = k = 4096, 256 rows each: 381 and 386).
+// The list has group after group, so that a place's b panels are a group's and its
+// rows of a stay in L2 over their panels (m-tiles of several groups sweeping together:
+// 128 very unequal experts 706 us, 688 this way).
 // Every wavefront reads m_indptr itself: a lane has ceil(E / 64) experts, and
 // where that is more than one, a second round resolves the lane's.
 template <int BM, int BN, uint32_t CM>
@@ -131,12 +136,7 @@ __device__ __forceinline__ F8Tile f8_find(const F8Args& p) {
   const uint32_t chunk = max((total + 8 * rounds - 1) / (8 * rounds), 1u);
   const uint32_t round = slot / chunk, L = (round * 8 + xcd) * chunk + slot % chunk;
   if (round >= rounds || L >= total) return f;
-  int mt, ni;
-  // 256-row tiles, 4, 6 and 8 together: m 4096, n = k = 8192 217, 213 and 219 us; 64
-  // experts, n = k = 2048, 512 rows each 169, 163 and 168; 64-row tiles: 8 together
-  // 29.9, 16 31.0 at m 256
-  f8_order<BM >= 256 ? 6 : 8>(L, count, nt, mt, ni);
-  int owner = __builtin_popcountll(__ballot(upto <= static_cast<uint32_t>(mt)));
+  int owner = __builtin_popcountll(__ballot(upto * nt <= L));
   f.e = owner * per;
   if (per > 1) {
     const uint32_t base = __builtin_amdgcn_readlane(before, owner);
@@ -146,15 +146,21 @@ __device__ __forceinline__ F8Tile f8_find(const F8Args& p) {
     cnt = tiles(s, t);
     upto = base + f8_scan(cnt);
     before = upto - cnt;
-    owner = __builtin_popcountll(__ballot(upto <= static_cast<uint32_t>(mt)));
+    owner = __builtin_popcountll(__ballot(upto * nt <= L));
     f.e += owner;
   }
   const int s_own = __builtin_amdgcn_readlane(s, owner), t_own = __builtin_amdgcn_readlane(t, owner);
-  f.m0 = s_own + (mt - static_cast<int>(__builtin_amdgcn_readlane(before, owner))) * BM;
+  // 256-row tiles, 4, 6 and 8 together: m 4096, n = k = 8192 223, 220 and 227 us;
+  // 64-row tiles: 8 together 29.9, 16 31.0 at m 256
+  int mt, ni;
+  f8_order<BM >= 256 ? 6 : 8>(L - __builtin_amdgcn_readlane(before, owner) * nt,
+                              __builtin_amdgcn_readlane(cnt, owner), nt, mt, ni);
+  f.m0 = s_own + mt * BM;
   f.n0 = ni * BN;
-  // in [s_own, t_own) where m_indptr is what it has to be; the counts of groups
-  // that overlap may pass 32 bits
-  f.rows = f.m0 >= s_own && f.m0 < t_own ? min(t_own - f.m0, BM) : 0;
+  // all so where m_indptr is what it has to be; the tiles of groups that overlap may
+  // pass 32 bits, and then no tile outside the operands may come of it
+  const bool in = f.e < p.E && static_cast<uint32_t>(ni) < nt && f.m0 >= s_own && f.m0 < t_own;
+  f.rows = in ? min(t_own - f.m0, BM) : 0;
   return f;
 }
 
