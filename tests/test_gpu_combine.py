@@ -156,3 +156,33 @@ def test_empty_calls(gpu):
                                       grad_rows=torch.ones_like(rows))
     assert not gr.any()
     torch.cuda.synchronize()
+
+
+def test_views_broadcast_gradients_and_shared_rows(gpu):
+    """Strided and broadcast inputs give what their copies give; two slots may read
+    the same row on the way back to the tokens."""
+    T, k, H, P = 9, 3, 264, 20
+    g = synth.gen(81)
+    rows = torch.randn(P, 2 * H, generator=g).to(torch.bfloat16).to(gpu)[:, ::2]
+    perm = torch.randint(0, P, (T, k), generator=g, dtype=torch.int32)
+    w = torch.rand(k, T, generator=g).to(gpu).t()
+    print("moe_combine_rows of shared rows, views", flush=True)
+    got = moe_combine_rows(rows, perm.to(gpu), w, out_dtype=torch.float32)
+    ref, mag = C.combine_rows(_np(rows), perm.numpy(), _np(w), T, k)
+    _near(got, ref, (k + 1) * U * mag, torch.float32, "shared rows")
+    gx = moe_permute_rows_backward(rows, perm.to(gpu), k, out_dtype=torch.float32)
+    ref, mag = C.combine_rows(_np(rows), perm.numpy(), None, T, k)
+    _near(gx, ref, (k + 1) * U * mag, torch.float32, "gradient of a shared copy")
+
+    print("moe_combine_rows_backward of a broadcast gradient", flush=True)
+    own = torch.randperm(T * k, generator=g).to(torch.int32).to(gpu)
+    rows = torch.randn(T * k, 2 * H, generator=g).to(gpu)[:, ::2]
+    for go in (torch.randn(1, H, generator=g).to(gpu).expand(T, H),
+               torch.randn(T, 1, generator=g).to(gpu).expand(T, H),
+               torch.ones((), device=gpu).expand(T, H)):
+        a = moe_combine_rows_backward(go, rows, own, w)
+        b = moe_combine_rows_backward(go.contiguous(), rows.contiguous(), own, w.contiguous())
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+        ref, ref_w, mag, _ = C.combine_rows_backward(_np(go), _np(rows), own.cpu().numpy(), _np(w))
+        _near(a[0], ref, 0.0, torch.float32, "rows' gradient")
+        _near(a[1], ref_w, (H + 1) * U * mag, torch.float32, "weights' gradient")

@@ -499,3 +499,25 @@ def test_grouped_fresh_out_is_zero_outside_the_groups(gpu, indptr, m):
         inside[indptr[0]:indptr[-1]] = True
         assert not v[~inside].any() and np.isfinite(v).all()
         assert not inside.any() or (v[inside] != 0).any(axis=1).all()
+
+
+def test_quantise_and_norm_views(gpu):
+    """Strided views give what their copies give, on a side stream too."""
+    g = synth.gen(83)
+    x = torch.randn(70, 3, 544, generator=g).to(torch.bfloat16).to(gpu)
+    w = torch.randn(2 * 544, generator=g).to(gpu)[::2]
+    u8 = lambda t: t.view(torch.uint8)
+    torch.cuda.synchronize()
+    print("fp8_quantize and add_rmsnorm_fp8 of views", flush=True)
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        got = [fp8_quantize(x[:, 1]), fp8_quantize(x.transpose(0, 1), block_rows=128),
+               fp8_quantize(x[:, 0], swiglu=True),
+               add_rmsnorm_fp8(x[:, 1], w, x[:, 2], with_norm=True)]
+    s.synchronize()
+    c = lambda t: t.contiguous()
+    want = [fp8_quantize(c(x[:, 1])), fp8_quantize(c(x.transpose(0, 1)), block_rows=128),
+            fp8_quantize(c(x[:, 0]), swiglu=True),
+            add_rmsnorm_fp8(c(x[:, 1]), c(w), c(x[:, 2]), with_norm=True)]
+    for a, b in zip(got, want):
+        assert all(p.is_contiguous() and torch.equal(u8(p), u8(q)) for p, q in zip(a, b))
