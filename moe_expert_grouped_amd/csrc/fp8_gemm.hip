@@ -90,6 +90,7 @@ __device__ __forceinline__ void f8_order(uint32_t L, uint32_t count, uint32_t nt
 
 struct F8Tile {
   int e, m0, rows, n0;  // rows == 0: this workgroup has no tile
+  bool alone;           // the group's only m-tile
 };
 
 // The tile of BM rows and BN columns of this workgroup.  The grid is an upper
@@ -121,7 +122,7 @@ __device__ __forceinline__ F8Tile f8_find(const F8Args& p) {
     }
   };
   auto tiles = [](int s, int t) { return static_cast<uint32_t>(t - s + BM - 1) / BM; };
-  F8Tile f{0, 0, 0, 0};
+  F8Tile f{0, 0, 0, 0, false};
   uint32_t cnt = 0;
   int s = 0, t = 0;
   for (int e = lane * per; e < min((lane + 1) * per, p.E); ++e) {
@@ -161,6 +162,7 @@ __device__ __forceinline__ F8Tile f8_find(const F8Args& p) {
   // pass 32 bits, and then no tile outside the operands may come of it
   const bool in = f.e < p.E && static_cast<uint32_t>(ni) < nt && f.m0 >= s_own && f.m0 < t_own;
   f.rows = in ? min(t_own - f.m0, BM) : 0;
+  f.alone = t_own - s_own <= BM;
   return f;
 }
 
@@ -321,7 +323,7 @@ __device__ __forceinline__ void f8_tile(const F8Args& p, F8Stage s0, F8Stage s1,
   // m-tiles: they share the panel) and every group has its own start.  With one
   // start for all, workgroups ask for the same bytes of rows that are a power of
   // two apart, and those lie in a few memory channels.
-  const int rot = STREAM && k % 512 == 0 ? (n0 / BN + e) % (KT / 4) * 4 : 0;
+  const int rot = STREAM && k % 4096 == 0 ? (n0 / BN + e) % (KT / 4) * 4 : 0;
   auto block = [&](int kt) { return !STREAM || kt + rot < KT ? kt + rot : kt + rot - KT; };
   // A step past the last loads zeros (its lane offsets are out of range): the
   // steps stay free of branches, which keep the compiler from moving a region's
@@ -579,6 +581,19 @@ __device__ __forceinline__ void f8_tile(const F8Args& p, F8Stage s0, F8Stage s1,
 // Tiles of one shape.  Two wavefronts per SIMD: 256 registers each, all of them
 // usable by the VALU, which adds the MFMAs' results.
 template <int WM, int WN, int FM, int FN, int NST, bool STREAM, typename OutT>
+__device__ __forceinline__ void f8_mid_tile(const F8Args& p, const F8Stage* st, float* ssa0,
+                                            float* ssa1, uint8_t* reg, const F8Tile& t) {
+  if constexpr (FM >= 4) {
+    if (t.rows <= 8 * FM * WM) {  // a group's last tile: half the work
+      f8_tile<WM, WN, FM / 2, FN, NST, STREAM, OutT>(p, st[0], st[1], st[2], st[3], ssa0, ssa1,
+                                                     ssa0, reg, t);
+      return;
+    }
+  }
+  f8_tile<WM, WN, FM, FN, NST, STREAM, OutT>(p, st[0], st[1], st[2], st[3], ssa0, ssa1, ssa0, reg,
+                                             t);
+}
+template <int WM, int WN, int FM, int FN, int NST, bool STREAM, typename OutT>
 __global__ __launch_bounds__(64 * WM * WN)
     __attribute__((amdgpu_waves_per_eu(2, 2))) void f8_mm_kernel(F8Args p) {
   constexpr int BM = 16 * FM * WM, BN = 16 * FN * WN, STAGE = (BM + BN) * F8_BK;
@@ -592,25 +607,19 @@ __global__ __launch_bounds__(64 * WM * WN)
   f8_zero_outside<OutT>(p);
   const F8Tile t = f8_find<BM, BN, 64>(p);  // two workgroups per CU
   if (t.rows == 0) return;
-  static_assert(BN <= 128, "halves");
+  static_assert(BM <= 128 && BN <= 128, "halves");
   constexpr int B = BM * F8_BK;  // b's rows follow a's
-  static_assert(BM <= 128, "halves");
   auto stage = [](uint8_t* s) { return F8Stage{s, s, s + B, s + B}; };
-  const F8Stage st0 = stage(s0), st1 = stage(s1), st2 = NST == 4 ? stage(s2) : st0,
-                st3 = NST == 4 ? stage(s3) : st1;
+  const F8Stage st[4] = {stage(s0), stage(s1), stage(NST == 4 ? s2 : s0), stage(NST == 4 ? s3 : s1)};
   // a wavefront's part of the stages for its outputs
   constexpr int NW = WM * WN, REG = 16 * FM * 16 * FN * sizeof(OutT);
   static_assert(NW / 2 * REG <= STAGE, "epilogue");
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   uint8_t* const reg = (wave < NW / 2 ? s0 : s1) + wave % (NW / 2) * REG;
-  if constexpr (FM >= 4) {
-    if (t.rows <= BM / 2) {  // a group's last tile: half the work
-      f8_tile<WM, WN, FM / 2, FN, NST, STREAM, OutT>(p, st0, st1, st2, st3, ssa0, ssa1, ssa0, reg,
-                                                     t);
-      return;
-    }
-  }
-  f8_tile<WM, WN, FM, FN, NST, STREAM, OutT>(p, st0, st1, st2, st3, ssa0, ssa1, ssa0, reg, t);
+  if (STREAM && t.alone)
+    f8_mid_tile<WM, WN, FM, FN, NST, STREAM, OutT>(p, st, ssa0, ssa1, reg, t);
+  else
+    f8_mid_tile<WM, WN, FM, FN, NST, false, OutT>(p, st, ssa0, ssa1, reg, t);
 }
 
 // 256 x 256 tiles; a group's last tile, where it has at most 128 or 64 rows, does a
@@ -619,6 +628,24 @@ __global__ __launch_bounds__(64 * WM * WN)
 // take, so it has three stages of 48 KB where the tall one has two of 64 (128
 // experts, n 7168, k 2048, of 128 rows each 424 -> 392 us, of very unequal rows
 // 714 -> 705): LDS arrays that make up either.
+template <bool STREAM, typename OutT>
+__device__ __forceinline__ void f8_large_tile(const F8Args& p, uint8_t* s0, uint8_t* s1,
+                                              uint8_t* t0, uint8_t* t1, uint8_t* u, float* ssa0,
+                                              float* ssa1, float* ssa2, uint8_t* reg,
+                                              const F8Tile& t) {
+  constexpr int Q = 128 * F8_BK;
+  if (t.rows > 128) {
+    const F8Stage st0{s0, t0, s0 + Q, s0 + 2 * Q}, st1{s1, t1, s1 + Q, s1 + 2 * Q};
+    f8_tile<2, 4, 8, 4, 2, STREAM, OutT>(p, st0, st1, st0, st1, ssa0, ssa1, ssa0, reg, t);
+  } else {
+    const F8Stage st0{s0, s0, s0 + Q, s0 + 2 * Q}, st1{s1, s1, s1 + Q, s1 + 2 * Q},
+        st2{u, u, t0, t1};
+    if (t.rows > 64)
+      f8_tile<2, 4, 4, 4, 3, STREAM, OutT>(p, st0, st1, st2, st0, ssa0, ssa1, ssa2, reg, t);
+    else
+      f8_tile<1, 8, 4, 2, 3, STREAM, OutT>(p, st0, st1, st2, st0, ssa0, ssa1, ssa2, reg, t);
+  }
+}
 template <bool STREAM, typename OutT>
 __global__ __launch_bounds__(512)
     __attribute__((amdgpu_waves_per_eu(2, 2))) void f8_mm_large_kernel(F8Args p) {
@@ -632,17 +659,10 @@ __global__ __launch_bounds__(512)
   uint8_t* const reg = wave < 3   ? s0 + wave * Q
                        : wave < 6 ? s1 + (wave - 3) * Q
                                   : (wave < 7 ? t0 : t1);
-  if (t.rows > 128) {
-    const F8Stage st0{s0, t0, s0 + Q, s0 + 2 * Q}, st1{s1, t1, s1 + Q, s1 + 2 * Q};
-    f8_tile<2, 4, 8, 4, 2, STREAM, OutT>(p, st0, st1, st0, st1, ssa0, ssa1, ssa0, reg, t);
-  } else {
-    const F8Stage st0{s0, s0, s0 + Q, s0 + 2 * Q}, st1{s1, s1, s1 + Q, s1 + 2 * Q},
-        st2{u, u, t0, t1};
-    if (t.rows > 64)
-      f8_tile<2, 4, 4, 4, 3, STREAM, OutT>(p, st0, st1, st2, st0, ssa0, ssa1, ssa2, reg, t);
-    else
-      f8_tile<1, 8, 4, 2, 3, STREAM, OutT>(p, st0, st1, st2, st0, ssa0, ssa1, ssa2, reg, t);
-  }
+  if (STREAM && t.alone)
+    f8_large_tile<STREAM, OutT>(p, s0, s1, t0, t1, u, ssa0, ssa1, ssa2, reg, t);
+  else
+    f8_large_tile<false, OutT>(p, s0, s1, t0, t1, u, ssa0, ssa1, ssa2, reg, t);
 }
 
 // ---------------------------------------------------------------------------
@@ -799,17 +819,15 @@ mi_status f8_grid(const F8Args& p, int bm, int bn, long cm, int threads, const c
   return MI_OK;
 }
 
-// Whether a product of groups streams b: its panels are read about once (groups
-// of up to a tile's rows on average), and the next call would hardly find them in
-// the 256 MB memory-side cache.  Then b is loaded with the non-temporal policy
-// and every panel has its own first step.  64 experts, n 2048, k 4096, 16 rows
-// each: 130 us, non-temporal 119, with own first steps 81; k 2048: 51.8 and 48.4;
-// skewed 128 experts of 15 MB: 744 and 727 (non-temporal).  Panels read twice or
-// found in the cache lose (128-row tiles of 256 rows each 468 and 489, 16 experts
-// of 1 MB 9.5 and 11.5).
-bool f8_stream_b(const F8Args& p, int bm) {
-  return p.m_indptr != nullptr && p.m_rows / p.E <= bm &&
-         static_cast<int64_t>(p.E) * p.n * p.k >= (128LL << 20);
+// Whether groups of one m-tile stream b: its panels are read once, and where all of b
+// is large the next call would hardly find them in the 256 MB memory-side cache.
+// Then b is loaded with the non-temporal policy, and with k a multiple of 4096 every
+// panel has its own first step (n 2048, 64 experts of 16 rows: k 4096 neither 127 us,
+// non-temporal 119, both 82; k 2048 51 and 44; k 2560 61 and 55; 128 experts of 15 MB,
+// very unequal: 666 and 664, with groups of several m-tiles streamed too 691).  Panels
+// found in the cache lose (16 experts of 1 MB 9.5 and 11.5).
+bool f8_stream_b(const F8Args& p) {
+  return p.m_indptr != nullptr && static_cast<int64_t>(p.E) * p.n * p.k >= (128LL << 20);
 }
 
 #define F8_LAUNCH(KERNEL_, BM_, BN_, CM_, THREADS_)                      \
@@ -823,7 +841,7 @@ bool f8_stream_b(const F8Args& p, int bm) {
 
 template <int WM, int WN, int FM, int FN, int NST, typename OutT>
 mi_status f8_launch(const F8Args& p, hipStream_t stream, const char* what) {
-  if (f8_stream_b(p, 16 * FM * WM))
+  if (f8_stream_b(p))
     F8_LAUNCH((f8_mm_kernel<WM, WN, FM, FN, NST, true, OutT>), 16 * FM * WM, 16 * FN * WN, 64,
               64 * WM * WN);
   F8_LAUNCH((f8_mm_kernel<WM, WN, FM, FN, NST, false, OutT>), 16 * FM * WM, 16 * FN * WN, 64,
@@ -832,7 +850,7 @@ mi_status f8_launch(const F8Args& p, hipStream_t stream, const char* what) {
 
 template <typename OutT>
 mi_status f8_launch_large(const F8Args& p, hipStream_t stream, const char* what) {
-  if (f8_stream_b(p, 256)) F8_LAUNCH((f8_mm_large_kernel<true, OutT>), 256, 256, 32, 512);
+  if (f8_stream_b(p)) F8_LAUNCH((f8_mm_large_kernel<true, OutT>), 256, 256, 32, 512);
   F8_LAUNCH((f8_mm_large_kernel<false, OutT>), 256, 256, 32, 512);
 }
 
