@@ -319,10 +319,9 @@ __device__ __forceinline__ void f8_tile(const F8Args& p, F8Stage s0, F8Stage s1,
   }
   const uint32_t tail = (KT - 1) * F8_BK + chunk * 16 < k ? 0u : F8_OUT;
   // STREAM: the steps go through the blocks of k from `rot` on, a multiple of 4
-  // (one load of a's scales), and round the end; every n-panel of b (all its
-  // m-tiles: they share the panel) and every group has its own start.  With one
-  // start for all, workgroups ask for the same bytes of rows that are a power of
-  // two apart, and those lie in a few memory channels.
+  // (one load of a's scales), and round the end; every n-panel of b and every group
+  // has its own start.  With one start for all, workgroups ask for the same bytes of
+  // rows that are a multiple of 4096 apart, and those lie in a few memory channels.
   const int rot = STREAM && k % 4096 == 0 ? (n0 / BN + e) % (KT / 4) * 4 : 0;
   auto block = [&](int kt) { return !STREAM || kt + rot < KT ? kt + rot : kt + rot - KT; };
   // A step past the last loads zeros (its lane offsets are out of range): the
@@ -869,19 +868,19 @@ mi_status f8_dispatch(const F8Args& p, hipStream_t s, const char* what) {
   auto tiles = [&](long bm, long bn) { return (rows + bm - 1) / bm * ((n + bn - 1) / bn); };
   const long active = E < p.m_rows ? E : p.m_rows;  // groups that have rows, at most
   // Few rows.  Dense: as long as the tiles run in one round, or where no other tile
-  // would read b less often (m 16: 15.6 against 17.5 for 64 x 64 tiles; m 24, two
-  // rounds: 27.5 against 17.5); 16 columns per workgroup where 32 do not give every
-  // CU one (m 1, n = k = 4096: 5.8 against 7.4).  Groups: while only a few have rows
-  // (64 experts, n 2048, k 4096: 8 rows 12.8 against 16.2, 16 rows 25 against 21).
+  // would read b less often (m 16: 15.8 against 17.3 for 64 x 64 tiles; m 24, two
+  // rounds: 27.6 against 17.3); 16 columns per workgroup where 32 do not give every
+  // CU one (m 1, n = k = 4096: 6.3 against 7.8).  Groups: while only a few have rows
+  // (64 experts, n 2048, k 4096: 8 rows 12.4 against 16.3, 16 rows 26.8 against 21.9).
   if (!grouped && tiles(16, 16) <= 256) return f8_launch_few<1, 1, 4, 4, OutT>(p, s, what);
   if (grouped ? rows <= 16 && active * ((n + 31) / 32) <= 512
               : rows <= 16 || tiles(16, 32) <= 256)
     return f8_launch_few<1, 2, 4, 2, OutT>(p, s, what);
   // 64 x 64 tiles with four stages.  Dense: while they run in one round of two
-  // workgroups per CU (m 256: 32 against 42 for 128 x 128; m 384: 48 against 43).
+  // workgroups per CU (m 256: 31 against 42 for 128 x 128; m 384: 47 against 43).
   // Groups of up to 48 rows: while the 128 x 128 tiles would not fill such a round (8
-  // experts, n = k = 4096, 16 rows: 25 against 32; 64 experts, n 2048: 89 against 81),
-  // with a long k two (64 experts, n 1536, k 7168, 4 rows: 109 against 123).
+  // experts, n = k = 4096, 16 rows: 23 against 31; 64 experts, n 2048: 87 against 82),
+  // with a long k two (64 experts, n 1536, k 7168, 4 rows: 109 against 124).
   const long panels = active * ((n + 127) / 128);
   if (grouped ? rows <= 48 && (panels < 512 || (panels <= 1024 && p.k > 4096))
               : tiles(64, 64) <= 512)
@@ -899,7 +898,7 @@ mi_status f8_dispatch(const F8Args& p, hipStream_t s, const char* what) {
       return f8_launch_large<OutT>(p, s, what);
   }
   // fp32 outputs stay here: fp16 fragments of a 256-row tile would not fit the
-  // registers (m 4096: 450; with 128 x 64 tiles 569)
+  // registers (m 4096: 436; with 128 x 64 tiles 569)
   return f8_launch<2, 2, 4, 4, 2, OutT>(p, s, what);
 }
 
