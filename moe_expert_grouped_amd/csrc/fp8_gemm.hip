@@ -878,11 +878,12 @@ mi_status f8_dispatch(const F8Args& p, hipStream_t s, const char* what) {
     return f8_launch_few<1, 2, 4, 2, OutT>(p, s, what);
   // 64 x 64 tiles with four stages.  Dense: while they run in one round of two
   // workgroups per CU (m 256: 31 against 42 for 128 x 128; m 384: 47 against 43).
-  // Groups of up to 48 rows: while the 128 x 128 tiles would not fill such a round (8
-  // experts, n = k = 4096, 16 rows: 23 against 31; 64 experts, n 2048: 87 against 82),
-  // with a long k two (64 experts, n 1536, k 7168, 4 rows: 109 against 124).
+  // Groups of up to 48 rows: where the 128 x 128 tiles leave a first or second round
+  // of 512 at most half full (8 experts, n = k = 4096, 16 rows: 23 against 31; 40
+  // experts, n 2048, k 4096, 8 rows: 62 against 69; 24: 40 against 35; 64: 87 against
+  // 82).
   const long panels = active * ((n + 127) / 128);
-  if (grouped ? rows <= 48 && (panels < 512 || (panels <= 1024 && p.k > 4096))
+  if (grouped ? rows <= 48 && (panels <= 256 || (panels > 512 && panels <= 768))
               : tiles(64, 64) <= 512)
     return f8_launch<2, 2, 2, 2, 4, OutT>(p, s, what);
   if constexpr (sizeof(OutT) == 2) {
