@@ -868,14 +868,18 @@ mi_status f8_dispatch(const F8Args& p, hipStream_t s, const char* what) {
   auto tiles = [&](long bm, long bn) { return (rows + bm - 1) / bm * ((n + bn - 1) / bn); };
   const long active = E < p.m_rows ? E : p.m_rows;  // groups that have rows, at most
   // Few rows.  Dense: as long as the tiles run in one round, or where no other tile
-  // would read b less often (m 16: 15.8 against 17.3 for 64 x 64 tiles; m 24, two
-  // rounds: 27.6 against 17.3); 16 columns per workgroup where 32 do not give every
-  // CU one (m 1, n = k = 4096: 6.3 against 7.8).  Groups: while only a few have rows
-  // (64 experts, n 2048, k 4096: 8 rows 12.4 against 16.3, 16 rows 26.8 against 21.9).
-  if (!grouped && tiles(16, 16) <= 256) return f8_launch_few<1, 1, 4, 4, OutT>(p, s, what);
+  // would read b less often (m 16: 15.2 against 17.3 for 64 x 64 tiles; m 24, two
+  // rounds: 27.6 against 17.3).  Groups: while only a few have rows (64 experts, n
+  // 2048, k 4096: 8 rows 12.7 against 16.3, 16 rows 26.8 against 21.9).  16 columns per
+  // workgroup while that is one round, 32 leave CUs idle there (m 1, n = k = 4096: 5.3
+  // against 6.9; m 4, n = k = 8192: 14.4 against 12.2).  Eight wavefronts with a step
+  // each in flight: more of them, or more steps, hold more lines than they gain (m 4:
+  // four with two steps 13.1, eight with two 13.1, sixteen with one 13.5).
+  if (grouped ? rows <= 16 && active * ((n + 15) / 16) <= 256 : tiles(16, 16) <= 256)
+    return f8_launch_few<1, 1, 8, 1, OutT>(p, s, what);
   if (grouped ? rows <= 16 && active * ((n + 31) / 32) <= 512
               : rows <= 16 || tiles(16, 32) <= 256)
-    return f8_launch_few<1, 2, 4, 2, OutT>(p, s, what);
+    return f8_launch_few<1, 2, 8, 1, OutT>(p, s, what);
   // 64 x 64 tiles with four stages.  Dense: while they run in one round of two
   // workgroups per CU (m 256: 31 against 42 for 128 x 128; m 384: 47 against 43).
   // Groups of up to 48 rows: where the 128 x 128 tiles leave a first or second round
