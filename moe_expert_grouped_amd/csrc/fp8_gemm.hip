@@ -869,15 +869,20 @@ mi_status f8_dispatch(const F8Args& p, hipStream_t s, const char* what) {
   const long active = E < p.m_rows ? E : p.m_rows;  // groups that have rows, at most
   // Few rows.  Dense: as long as the tiles run in one round, or where no other tile
   // would read b less often (m 16: 15.2 against 17.3 for 64 x 64 tiles; m 24, two
-  // rounds: 27.6 against 17.3).  Groups: while only a few have rows (64 experts, n
-  // 2048, k 4096: 8 rows 12.7 against 16.3, 16 rows 26.8 against 21.9).  16 columns per
-  // workgroup while that is one round, 32 leave CUs idle there (m 1, n = k = 4096: 5.3
-  // against 6.9; m 4, n = k = 8192: 14.4 against 12.2).  Eight wavefronts with a step
-  // each in flight: more of them, or more steps, hold more lines than they gain (m 4:
-  // four with two steps 13.1, eight with two 13.1, sixteen with one 13.5).
-  if (grouped ? rows <= 16 && active * ((n + 15) / 16) <= 256 : tiles(16, 16) <= 256)
+  // rounds: 27.6 against 17.3).  Groups: up to 10 rows, beyond which some have two
+  // tiles of 16 and b is read twice (8 experts, n 1024, k 4096: 10 rows 9.0 against
+  // 10.5, 12 rows 15.7), in one round (n 2048, k 2048: two rounds, 2 rows 8.5 against
+  // 7.7) or two where a group has one row or the MFMAs are the slower ones of fp32
+  // outputs (64 experts, n 2048, k 4096: 8 rows in all 12.7 against 16.3, 16 rows 26.8
+  // against 21.9).  16 columns per workgroup while that is one round, 32 leave CUs
+  // idle there (m 1, n = k = 4096: 5.3 against 6.9; m 4, n = k = 8192: 14.4 against
+  // 12.2).  Eight wavefronts with a step each in flight: more of them, or more steps,
+  // hold more lines than they gain (m 4: four with two steps 13.1, eight with two 13.1,
+  // sixteen with one 13.5).
+  if (grouped ? rows <= 10 && active * ((n + 15) / 16) <= 256 : tiles(16, 16) <= 256)
     return f8_launch_few<1, 1, 8, 1, OutT>(p, s, what);
-  if (grouped ? rows <= 16 && active * ((n + 31) / 32) <= 512
+  const long at_most = rows <= 1 || sizeof(OutT) == 4 ? 512 : 256;
+  if (grouped ? rows <= 10 && active * ((n + 31) / 32) <= at_most
               : rows <= 16 || tiles(16, 32) <= 256)
     return f8_launch_few<1, 2, 8, 1, OutT>(p, s, what);
   // 64 x 64 tiles with four stages.  Dense: while they run in one round of two
