@@ -616,19 +616,18 @@ def _one_gpu(name, first, *others):
     return i
 
 
-# the current device, and its current stream's handle without a Stream object
-# around it (1.9 us less a call)
-_current_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
-
-
 def _launch(i, fn, *args):
-    """Enqueue on GPU `i`'s current stream, with `i` the current device for the launch."""
-    if _current_device() == i:
-        status = fn(*args, _raw_stream(i))
+    """Enqueue on GPU `i`'s current stream, with `i` the current device for the launch.
+
+    torch's own accessors give the device and the stream's handle without a Stream
+    object around it (1.9 us less a call).  They are looked up here: a torch without
+    GPU support has none, and its tensors are refused before this."""
+    c = torch._C
+    if c._cuda_getDevice() == i:
+        status = fn(*args, c._cuda_getCurrentRawStream(i))
     else:
         with torch.cuda.device(i):
-            status = fn(*args, _raw_stream(i))
+            status = fn(*args, c._cuda_getCurrentRawStream(i))
     if status:
         check(status)
 
