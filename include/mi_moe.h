@@ -552,12 +552,17 @@ MI_API mi_status mi_moe_combine_rows(const void* rows, mi_dtype rows_dtype, int6
  *     grad_weights[t, j] = sum_c rows[perm[t * top_k + j], c] * grad_out[t, c]
  * and 0 for the weight of a slot whose entry is outside [0, num_rows).
  *   inverse       int32 [num_rows], the permuted_idx_to_expanded_idx that goes with
- *                 perm: rows whose entry is negative get zeros, so every row is
- *                 written.  NULL: rows no slot points at are untouched
+ *                 perm.  Every row is then written, once: with the gradient of the slot
+ *                 that the inverse names for it, or with zeros where the entry names
+ *                 none or one that perm does not point at that row.  NULL: rows no
+ *                 slot points at are untouched
  *   grad_rows     rows_dtype [num_rows, hidden_size]
  *   grad_weights  fp32 [num_tokens, top_k], or NULL (rows is then not read and may be)
- * Requirements: as above; the outputs may not overlap an input or each other.  Two slots with the same row (an
- * invalid permutation) leave one of the two gradients there.
+ * Requirements: as above; the outputs may not overlap an input or each other.
+ * grad_rows needs a row for every slot: where two slots point at one row, which
+ * mi_moe_combine_rows takes, the row's gradient would be their sum.  It is not: with
+ * the inverse it is the named slot's, without it each element is either slot's.
+ * grad_weights is right for them too.
  */
 MI_API mi_status mi_moe_combine_rows_backward(
     const void* grad_out, mi_dtype grad_dtype, const void* rows, mi_dtype rows_dtype,

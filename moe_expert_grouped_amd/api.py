@@ -833,7 +833,8 @@ def moe_combine_rows(rows: torch.Tensor, expanded_idx_to_permuted_idx: torch.Ten
     (bf16, fp16 or fp32 ``[num_rows, H]``, permuted order) back in token order
     ``[T, H]``.  Slots whose entry lies outside ``[0, num_rows)`` contribute
     nothing.  fp32 sums in slot order, one rounding to ``out_dtype`` (the
-    rows' type by default).  ``topk_weights`` fp32 ``[T, top_k]``."""
+    rows' type by default).  ``topk_weights`` fp32 ``[T, top_k]``.  Slots may share
+    a row here; :func:`moe_combine_rows_backward` needs one row a slot."""
     _need(topk_weights.dim() == 2 and topk_weights.dtype == torch.float32 and
           topk_weights.shape[1] >= 1, "moe_combine_rows: topk_weights must be float32 [T, top_k]")
     T, top_k = topk_weights.shape
@@ -871,9 +872,12 @@ def moe_combine_rows_backward(grad_out: torch.Tensor, rows: torch.Tensor,
 
     With ``permuted_idx_to_expanded_idx`` (the inverse that
     :func:`moe_route_permutation` returns, one entry per row) the call writes
-    every row, zeros where no slot points.  Without it rows no slot points at
-    are zero in a fresh ``grad_rows`` and untouched in a caller's.  Each row may
-    be pointed at once.
+    every row: the gradient of the slot the inverse names, zeros where that slot
+    does not point at the row (it was taken out of the permutation) or there is
+    none.  Without it rows no slot points at are zero in a fresh ``grad_rows`` and
+    untouched in a caller's.  Each row may be pointed at once: of two slots that
+    share a row, ``grad_rows`` has the named slot's gradient, not the sum (without
+    the inverse either's, element by element).
     """
     name = "moe_combine_rows_backward"
     _need(rows.dim() == 2 and rows.dtype in _DT,

@@ -119,8 +119,12 @@ __global__ __launch_bounds__(256) void combine_kernel(const T* __restrict__ rows
 }
 
 // One wavefront per slot: w * go[t] to the slot's row, and the dot product of
-// the row with go[t].  Wavefront u also writes zeros to row u where the inverse
-// permutation says that no slot points at it.
+// the row with go[t].  With the inverse permutation a row's one writer is the slot
+// that the inverse names, if that slot points at the row; else wavefront p writes
+// zeros to row p.  So every row is written once, whatever the two arrays hold
+// (slots taken out of one of them, two slots with one row): the order of the
+// wavefronts does not matter and no row is left as it was.  The inverse costs a
+// second, dependent 4-byte read a slot, which the rows' loads do not wait for.
 template <typename T, typename GoT>
 __global__ __launch_bounds__(256) void combine_backward_kernel(
     const GoT* __restrict__ go, const T* __restrict__ rows, int64_t num_rows, int h,
@@ -141,6 +145,7 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(
         const GoT* g = go + u / top_k * h;
         const T* src = rows + static_cast<int64_t>(p) * h;
         T* dst = grad_rows + static_cast<int64_t>(p) * h;
+        const bool writer = inverse == nullptr || inverse[p] == u;
         for (int col = lane * N; col < h; col += 64 * N) {
           float y[N];
           load_n<GoT, N>(g + col, y);
@@ -152,7 +157,7 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(
           }
 #pragma unroll
           for (int i = 0; i < N; ++i) y[i] *= w;
-          store_n<T, N>(dst + col, y);
+          if (writer) store_n<T, N>(dst + col, y);
         }
       }
       if (grad_w != nullptr) {
@@ -161,7 +166,12 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(
         if (lane == 0) gst<float>(grad_w + u, dot);
       }
     }
-    if (inverse != nullptr && u < num_rows && inverse[u] < 0) {
+    bool empty = false;
+    if (inverse != nullptr && u < num_rows) {
+      const int s = inverse[u];
+      empty = s < 0 || s >= slots || perm[s] != u;
+    }
+    if (empty) {
       const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       for (int col = lane * N; col < h; col += 64 * N)
         store_n<T, N>(grad_rows + u * h + col, z);
