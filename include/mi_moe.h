@@ -461,7 +461,8 @@ MI_API int64_t mi_fp8_scale_cols(int64_t k); /* 4 * ceil(k / 512) */
 /*
  * The producer of those operands:
  *     scale = max(amax(block) / 448, 2^-126),  code = e4m3_rne(y * (1 / scale))
- * in fp32, with y = x, or with swiglu y = silu(gate) * up of rows [gate | up].
+ * in fp32, with y = x, or with swiglu y = silu(gate) * up of rows [gate | up]
+ * (8 fp32 roundings at most, at every gate: exp is good to a step of its result).
  * An all-zero block has scale 2^-126 and zero codes.  A block holding a NaN or
  * an infinity has that as its scale and dequantises to NaN throughout.
  *   x       dtype [batch, rows, k] (swiglu: [batch, rows, 2k]), MI_BF16, MI_F16 or MI_F32
