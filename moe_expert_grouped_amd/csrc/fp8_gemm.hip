@@ -17,11 +17,16 @@
 // exponent among them and keeps 13 bits below it (measured: 2^3 beside 2^16 is
 // kept, 2^2 is not, at any of the 8 places; beyond them everything is fp32).  A
 // product of two e4m3 codes has 6 fraction bits, so only products under 2^-7 of
-// their group's largest lose any: at most 7 * 2^-13 of a group's largest term,
-// 1.5e-5 of the result on normally distributed codes.  That is far below the
-// rounding to a 16-bit output and accepted there for twice the rate.  An fp32
-// output would show it: there the codes are converted to fp16 (exact) and
-// multiplied with v_mfma_f32_16x16x32_f16, which sums in fp32 throughout.
+// their group's largest lose any: at most 7 * 2^-13 = 8.5e-4 of a group's largest
+// term.  That bound is under a rounding to bf16 (2^-8) but over one to fp16 (2^-11),
+// and an output that nearly cancels keeps the error of its terms.  On normally
+// distributed codes the error is 2e-5 of the outputs' rms, 6e-5 and 9e-5 with one
+// column of k in 64 20 and 100 times larger (a CPU model, k 4096); it then exceeds
+// fp16's half step for 2, 8 and 11 outputs in a hundred, bf16's for 0.4, 0.9 and 1.5,
+// all small ones.  16-bit outputs accept that for twice the rate, and the entry points
+// say so; a caller who needs fp32 sums asks for an fp32 output.  There the codes are
+// converted to fp16 (exact) and multiplied with v_mfma_f32_16x16x32_f16, which sums in
+// fp32 throughout.
 #include "common.hpp"
 
 namespace mi {
