@@ -510,6 +510,9 @@ MI_API mi_status mi_add_rmsnorm_fp8(const void* x, const void* residual, const v
  * to fp16 (2^-11) mostly, and neither for an output that nearly cancels.  A caller
  * who needs fp32 sums takes MI_F32 and rounds, at half the rate for many rows.
  * A NaN code or scale makes the outputs NaN that its row and column reach.
+ * The gradient of a's rows is the same product of the output's gradient (quantised 1
+ * x 128 along n) with b's codes transposed to [k, n] and its scales to [ceil(k / 128),
+ * mi_fp8_scale_cols(n)]: the transpose without the padding, padded anew.
  *   a, a_scale   uint8 [m, k], fp32 [m, cols]            (1 x 128 scales)
  *   b, b_scale   uint8 [n, k], fp32 [ceil(n / 128), cols] (128 x 128 scales)
  *   out          out_dtype [m, n] (MI_BF16, MI_F16 or MI_F32)

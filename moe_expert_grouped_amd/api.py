@@ -744,6 +744,10 @@ def mm_fp8_block(a: torch.Tensor, b: torch.Tensor, a_scale: torch.Tensor, b_scal
     ``7 * 2**-13`` of that product for each 8, 2e-5 of the outputs' rms on normally
     distributed codes, 1e-4 with large outlier columns.  For fp32 sums in a 16-bit
     result ask for float32 and convert.
+
+    The gradient of the rows is the same product: the output's gradient, quantised
+    with ``block_rows=1``, times ``b.t()`` with the scales ``b_scale[:, :ceil(K / 128)].t()``
+    padded with zeros to ``fp8_scale_cols(N)`` columns.
     """
     _need(a.dtype == _F8 and b.dtype == _F8 and a.dim() == 2 and b.dim() == 2 and
           a.shape[1] == b.shape[1],
@@ -778,7 +782,8 @@ def grouped_mm_fp8_block(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor
     ``m_indptr`` int32 ``(batch+1,)`` read on the device.  Rows outside the
     groups of a caller-provided ``out`` are untouched (a fresh ``out`` is
     zero-filled there).  The sums have the precision that :func:`mm_fp8_block`
-    states: fp32 for float32 outputs, fewer bits for 16-bit ones.
+    states: fp32 for float32 outputs, fewer bits for 16-bit ones.  The rows' gradient
+    is given there too, with ``b.transpose(1, 2)`` and each expert's scales so.
     """
     _need(a.dtype == _F8 and b.dtype == _F8 and a.dim() == 2 and b.dim() == 3 and
           a.shape[1] == b.shape[2],
