@@ -460,7 +460,7 @@ MI_API int64_t mi_fp8_scale_cols(int64_t k); /* 4 * ceil(k / 512) */
 
 /*
  * The producer of those operands:
- *     scale = max(amax(block) / 448, 2^-126),  code = e4m3_rne(y * (1 / scale))
+ *     scale = max(amax(block) / 448, 2^-126),  code = e4m3_rne(y / scale)
  * in fp32, with y = x, or with swiglu y = silu(gate) * up of rows [gate | up]
  * (8 fp32 roundings at most, at every gate: exp is good to a step of its result).
  * An all-zero block has scale 2^-126 and zero codes.  A block holding a NaN or
