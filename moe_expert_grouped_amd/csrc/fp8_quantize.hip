@@ -73,48 +73,55 @@ __device__ __forceinline__ uint32_t amax8(const float* y) {
 }
 
 // silu(g) = g E' / (1 + E) with E = exp(-|g|) in [0, 1] and E' = 1 or, below zero, E:
-// nothing overflows.  E = 2^t 2^r with t = fl(-|g| log2 e) and the rest r = -|g| log2 e
-// - t from the fma and log2 e's own rest; |r| < 2^-16, so 2^r is 1 + r ln 2.  Without r
-// the result would be off by |g| half steps at a negative gate (65 at -85).  2^24 E is
-// what is computed, as v_exp gives zero for a subnormal result; the 24 is rounded into
-// t before r is taken (t + 24 - 24 is exact for what is left), so nothing may be
-// contracted here.  Past -150 E is zero, and an infinite gate below zero gives NaN.
+// nothing overflows.  E = 2^t e^r with t = fl(-|g| log2 e) and the rest r = -|g| - t ln 2
+// from the fma and ln 2's own rest; |r| < 2^-16, so e^r is 1 + r.  Without r the result
+// would be off by |g| half steps at a negative gate (65 at -85).  2^24 E is what is
+// computed, as v_exp gives zero for a subnormal result; the 24 is rounded into t before
+// r is taken (t + 24 - 24 is exact for what is left), so nothing may be contracted
+// here.  Past -150 E is zero, and an infinite gate below zero gives NaN.
 // 1 / (1 + E) is v_rcp and one Newton step.  At most 7 roundings, 9 with up and the
 // scale's division.  65536 x 2048 of bf16 rows [gate | up], VALU and memory close to
-// each other: a bare exp and a full division are as fast, expf and a full division
-// take 13% more.
+// each other: 127 us; a bare exp and full divisions 128, expf and full divisions 13% more.
 __device__ __forceinline__ float silu(float g) {
 #pragma clang fp contract(off)
-  constexpr float L = 1.44269502f, REST = 1.92596299e-8f, LN2 = 0.693147181f, UP = 0x1p-24f;
-  const float v = fmaxf(-fabsf(g), -150.f);
-  const float t = v * L + 24.f;
-  const float r = __builtin_fmaf(v, REST, __builtin_fmaf(v, L, 24.f - t));
+  constexpr float L = 1.44269502f, LN2 = 0.693147182f, REST = -1.90465430e-9f, UP = 0x1p-24f;
+  const float v = __builtin_amdgcn_fmed3f(-fabsf(g), -150.f, 0.f);
+  const float t = v * L + 24.f, u = 24.f - t;
+  const float r = __builtin_fmaf(u, REST, __builtin_fmaf(u, LN2, v));
   const float p = __builtin_amdgcn_exp2f(t);
-  const float e = __builtin_fmaf(p, r * LN2, p);
+  const float e = __builtin_fmaf(p, r, p);
   const float d = __builtin_fmaf(e, UP, 1.f), q = __builtin_amdgcn_rcpf(d);
   return (g >= 0.f ? g : g * e * UP) * __builtin_fmaf(__builtin_fmaf(-d, q, 1.f), q, q);
 }
 
-// the scale of a block from its amax bits; a NaN stays a NaN
+// The quotient a / b from inv, 1 / b to a step: one correction by the exact remainder,
+// which then rounds as a division does (3 operations where a division has 11; 448 was
+// tried with every mantissa of a)
+__device__ __forceinline__ float quotient(float a, float b, float inv) {
+  const float q = a * inv;
+  return __builtin_fmaf(__builtin_fmaf(q, -b, a), inv, q);
+}
+
+// the scale of a block from its amax bits; a NaN stays a NaN, an infinity itself
 __device__ __forceinline__ float block_scale(uint32_t m) {
-  const float s = __fdiv_rn(__uint_as_float(m), F8Q_MAX);
+  const float a = __uint_as_float(m);
+  const float s = m < 0x7f800000u ? quotient(a, F8Q_MAX, 1.f / F8Q_MAX) : a;
   return s < F8Q_MIN_SCALE ? F8Q_MIN_SCALE : s;
 }
 
-// The codes of y / s.  The quotient is y * (1 / s) and one correction by its exact
-// remainder, which rounds as a division does; without it a value within two roundings
-// of a tie between two codes may take the wrong one (8 x 2000 x 4112 of fp32: 2.1e-5
-// of the codes' rms against 2.3e-6, the same time; SwiGLU rows 1% more).
+// The codes of y / s.  Without the quotients' correction a value within two roundings of
+// a tie between two codes may take the wrong one (8 x 2000 x 4112 of fp32: 2.1e-5 of the
+// codes' rms against 2.3e-6).
 __device__ __forceinline__ u32x2 codes8(const float* y, float s) {
-  const float inv = __fdiv_rn(1.f, s);
-  // an infinite scale (inv is 0) has no remainder: finite values keep code 0
-  const float d = inv > 0.f ? -s : 0.f;
+  const float rcp = __builtin_amdgcn_rcpf(s);  // good to a step, and a Newton step on it
+  float inv = __builtin_fmaf(__builtin_fmaf(-s, rcp, 1.f), rcp, rcp);
+  // an infinite scale has no remainder: numbers get code 0, infinities NaN
+  const bool inf = s == __builtin_inff();
+  if (inf) inv = 0.f;
+  const float d = inf ? 0.f : s;
   float q[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    q[i] = y[i] * inv;
-    q[i] = __builtin_fmaf(__builtin_fmaf(q[i], d, y[i]), inv, q[i]);
-  }
+  for (int i = 0; i < 8; ++i) q[i] = quotient(y[i], d, inv);
   int lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
   lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], lo, true);
   int hi = __builtin_amdgcn_cvt_pk_fp8_f32(q[4], q[5], 0, false);
@@ -138,7 +145,7 @@ __device__ __forceinline__ void quantise_unit(const float* y, int col, int k, ui
 // 1 x 128 blocks: a wavefront per unit.  Bound by memory: x is read once with
 // 16-byte loads (fp32: two), and a block's amax takes 4 exchanges among its 16
 // lanes, no LDS and no barrier.  65536 x 2048 of bf16 [gate | up]: 675 MB in
-// 132 us, 5.1 TB/s, the rate of a large copy.
+// 127 to 131 us by card, 5.2 TB/s, the rate of a large copy.
 template <typename T, bool GLU>
 __global__ __launch_bounds__(256) void f8_rows_kernel(const T* __restrict__ x, int64_t units,
                                                       int k, int upr, uint8_t* __restrict__ codes,
