@@ -488,6 +488,9 @@ MI_API mi_status mi_fp8_quantize(const void* x, int64_t batch, int64_t rows, int
  *   residual_out  dtype [num_tokens, hidden_size]; may be residual or x itself
  *   norm_out      the same shape, or NULL (a router that reads the normed rows)
  *   codes, scales uint8 [num_tokens, hidden_size], fp32 [num_tokens, cols]
+ * The squares' sum is fp32: a row with |h| past about 1.8e19 has an infinite one and
+ * gives zeros, and with eps 0 one of zeros (or of |h| below 3e-23 throughout) gives NaN
+ * or infinities.
  * Requirements: hidden_size % 16 == 0, eps >= 0, all 16-byte aligned; no other
  * overlap of an output with another tensor.  num_tokens == 0 is a no-op.
  */

@@ -87,8 +87,8 @@ __device__ __forceinline__ void f8_order(uint32_t L, uint32_t count, uint32_t nt
   const uint32_t gsize = min(count - first, GM);
   const uint32_t in_grp = L - grp * span;
   // The m-tiles turn by one every 8 panels: consecutive tiles of one place then
-  // are not all of the same height (64 experts of about 256 rows, n = k = 4096: 374
-  // and 370 us)
+  // are not all of the same height (128 very unequal experts, n 7168, k 2048: 684 us
+  // without, 679 with; 64 experts of about 256 rows, n = k = 4096: 354 both)
   ni = in_grp / gsize;
   mt = first + (in_grp % gsize + ni / 8) % gsize;
 }
@@ -103,12 +103,13 @@ struct F8Tile {
 // neighbours of the list of tiles, which its L2 serves: without groups one
 // contiguous run, of groups' tiles chunks of up to CM, what an XCD runs at once,
 // from the whole list.  With one run each an XCD may get all of a large group's
-// full tiles: 128 experts, n 2048, k 7168, 4096 rows of very unequal groups 383
-// against 361 us, n 1536 with 16384 rows 413 against 402; equal groups lose a
-// little by the chunks (64 experts, n = k = 4096, 256 rows each: 381 and 386).
+// full tiles.  One run and chunks, us: 64 experts of about 256 rows, n = k = 4096, 367
+// and 354, of 256 rows each 297 both; very unequal groups go either way: 128 experts,
+// k 7168, n 1536, 16384 rows 348 and 338, n 2048, 4096 rows 346 and 356; k 2048, n 7168,
+// 32768 rows 675 and 679.
 // The list has group after group, so that a place's b panels are a group's and its
-// rows of a stay in L2 over their panels (m-tiles of several groups sweeping together:
-// 128 very unequal experts 706 us, 688 this way).
+// rows of a stay in L2 over their panels (m-tiles of several groups sweeping together
+// took 2.5% more on very unequal experts, before the steps that followed).
 // Every wavefront reads m_indptr itself: a lane has ceil(E / 64) experts, and
 // where that is more than one, a second round resolves the lane's.
 template <int BM, int BN, uint32_t CM>
@@ -156,8 +157,8 @@ __device__ __forceinline__ F8Tile f8_find(const F8Args& p) {
     f.e += owner;
   }
   const int s_own = __builtin_amdgcn_readlane(s, owner), t_own = __builtin_amdgcn_readlane(t, owner);
-  // 256-row tiles, 4, 6 and 8 together: m 4096, n = k = 8192 223, 220 and 227 us;
-  // 64-row tiles: 8 together 29.9, 16 31.0 at m 256
+  // 256-row tiles, 4, 6 and 8 together: m 4096, n = k = 8192 222.9, 222.9 and 223.2 us,
+  // very unequal groups 679, 678 and 680; 64-row tiles, 8 and 16 at m 256: 30.1 and 30.2
   int mt, ni;
   f8_order<BM >= 256 ? 6 : 8>(L - __builtin_amdgcn_readlane(before, owner) * nt,
                               __builtin_amdgcn_readlane(cnt, owner), nt, mt, ni);
@@ -229,8 +230,9 @@ __device__ __forceinline__ f32x4 f8_block(const F8Frag<false>& b, const F8Frag<f
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b.v, a.v, z, 0, 0, 0, 0, 0, 0);
 }
 // a quarter of it on top of d: the four of a block depend on each other, so those
-// of several blocks are issued in turn (64 experts, n = k = 4096, 256 rows each:
-// 637 -> 614 us; m 333, n 1744, k 2064: 10.2 -> 9.9)
+// of several blocks are issued in turn (block after block and in turn, us: 64 experts of
+// about 256 rows, n = k = 4096, 587 and 581; m 4096, n = k = 8192 457 and 451; m 333,
+// n 1744, k 2064 9.6 and 9.5)
 __device__ __forceinline__ f32x4 f8_quarter(const F8Frag<true>& b, const F8Frag<true>& a, int c,
                                             f32x4 d) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(b.v[c], a.v[c], d, 0, 0, 0);
@@ -366,7 +368,7 @@ __device__ __forceinline__ void f8_tile(const F8Args& p, F8Stage s0, F8Stage s1,
   // c = 0, 2, 1, 3 for g = 0 .. 3; a and b use the same chunks, so the order of k
   // inside the MFMA is theirs.  The LDS serves lanes l and l + 32 together: their
   // chunks have to differ in the lowest bit, which 0, 1, 2, 3 does not give (every
-  // read then took twice its 4 cycles: 323 against 260 us at m 4096, n = k = 8192)
+  // read then takes twice its 4 cycles: 226 against 222 us at m 4096, n = k = 8192)
   const int r = lane & 15, g = lane >> 4;
   uint32_t fo[2];
 #pragma unroll
@@ -547,7 +549,8 @@ __device__ __forceinline__ void f8_tile(const F8Args& p, F8Stage s0, F8Stage s1,
   // a lane, instead of 8 bytes from each of 64 places.  16-byte chunk c of a row sits at
   // slot c ^ (row % CPR).  The stores are streaming (non-temporal): they cover
   // whole 64-byte pieces at least and the outputs do not push operands out of L2
-  // (skewed experts: 817 us with 8-byte stores, 741 staged, 736 streaming).
+  // (128 very unequal experts: 687 us with ordinary stores, 679 streaming; 8-byte stores
+  // from the lanes themselves took 10% more than these rows when they were replaced).
   constexpr int ES = sizeof(OutT), RB = 16 * FN * ES, CPR = RB / 16, REG = 16 * FM * RB;
   static_assert(REG <= 16 * 1024 && 64 % CPR == 0, "epilogue");
   f8_wait_barrier<0>();
@@ -629,9 +632,10 @@ __global__ __launch_bounds__(64 * WM * WN)
 // 256 x 256 tiles; a group's last tile, where it has at most 128 or 64 rows, does a
 // half or a quarter of the work.  It keeps its place among the group's tiles,
 // which share b's panels in L2.  Such a low tile's step is shorter than its loads
-// take, so it has three stages of 48 KB where the tall one has two of 64 (128
-// experts, n 7168, k 2048, of 128 rows each 424 -> 392 us, of very unequal rows
-// 714 -> 705): LDS arrays that make up either.
+// take, so it has three stages of 48 KB where the tall one has two of 64: LDS arrays
+// that make up either.  Two stages and three, us: 128 experts, n 7168, k 2048, of 128
+// rows each 438 and 404, of very unequal rows 693 and 678; 64 of about 256 rows,
+// n = k = 4096, where few tiles are low, 348 and 354.
 template <bool STREAM, typename OutT>
 __device__ __forceinline__ void f8_large_tile(const F8Args& p, uint8_t* s0, uint8_t* s1,
                                               uint8_t* t0, uint8_t* t1, uint8_t* u, float* ssa0,
@@ -826,10 +830,11 @@ mi_status f8_grid(const F8Args& p, int bm, int bn, long cm, int threads, const c
 // Whether groups of one m-tile stream b: its panels are read once, and where all of b
 // is large the next call would hardly find them in the 256 MB memory-side cache.
 // Then b is loaded with the non-temporal policy, and with k a multiple of 4096 every
-// panel has its own first step (n 2048, 64 experts of 16 rows: k 4096 neither 127 us,
-// non-temporal 119, both 82; k 2048 51 and 44; k 2560 61 and 55; 128 experts of 15 MB,
-// very unequal: 666 and 664, with groups of several m-tiles streamed too 691).  Panels
-// found in the cache lose (16 experts of 1 MB 9.5 and 11.5).
+// panel has its own first step (us; n 2048, 64 experts of 16 rows: k 4096 neither 129,
+// non-temporal 120, both 85; k 2560, 335 MB, 61 and 55; k 2048, 268 MB, which the next
+// call of a loop partly finds again, 43 and 45; 128 experts of 15 MB, very unequal: 682
+// and 679, with groups of several m-tiles streamed too 708).  Panels found in the cache
+// lose (16 experts of 1 MB 9.5 and 11.5).
 bool f8_stream_b(const F8Args& p) {
   return p.m_indptr != nullptr && static_cast<int64_t>(p.E) * p.n * p.k >= (128LL << 20);
 }
@@ -893,9 +898,10 @@ mi_status f8_dispatch(const F8Args& p, hipStream_t s, const char* what) {
   // 64 x 64 tiles with four stages.  Dense: while they run in one round of two
   // workgroups per CU (m 256: 31 against 42 for 128 x 128; m 384: 47 against 43).
   // Groups of up to 48 rows: where the 128 x 128 tiles leave a first or second round
-  // of 512 at most half full (8 experts, n = k = 4096, 16 rows: 23 against 31; 40
-  // experts, n 2048, k 4096, 8 rows: 62 against 69; 24: 40 against 35; 64: 87 against
-  // 82).
+  // of 512 at most half full (8 experts, n = k = 4096, 16 rows: 23 against 31; n 2048,
+  // k 4096, 48 experts of 12 and 48 rows 65 and 75 against 72 and 76, 32 of 16 rows 44
+  // against 40, 64 of 16 rows 89 against 85).  In a third round it is no rule: 80 experts
+  // of 16 rows 115 against 122, of 48 rows 129 against 126; 72 of 40 rows 119 against 117.
   const long panels = active * ((n + 127) / 128);
   if (grouped ? rows <= 48 && (panels <= 256 || (panels > 512 && panels <= 768))
               : tiles(64, 64) <= 512)
