@@ -33,6 +33,12 @@
  *   - mi_grouped_mm_fp8_block its ragged per-expert form
  *   - mi_moe_combine_rows     permuted rows -> token rows with the routing weights, and
  *   - mi_moe_combine_rows_backward  its gradients
+ *   - mi_mm_lora              a shared projection with the low-rank adapters of many requests
+ *                             beside it, and
+ *   - mi_mm_lora_backward     the gradients of its rows and of every adapter
+ *   - mi_moe_route_topk       router logits -> top_k experts and weights,
+ *   - mi_moe_balance_loss     per-expert counts and the balance loss, and
+ *   - mi_moe_route_backward   the gradient of the logits through both
  *
  * Conventions shared by every entry point
  *   - All tensor pointers are DEVICE pointers owned by the caller.  The library
@@ -587,6 +593,131 @@ MI_API mi_status mi_moe_combine_rows_backward(
     int64_t num_rows, int64_t hidden_size, const int32_t* perm, const int32_t* inverse,
     const float* weights, int64_t num_tokens, int64_t top_k, void* grad_rows,
     float* grad_weights, void* stream);
+
+/*
+ * A shared projection with the low-rank adapters of many requests beside it: with
+ * l = lora_ids[t],
+ *     v[t]   = x[t] @ lora_a[l]^T                                      fp32
+ *     out[t] = x[t] @ w^T + bias + lora_scale[l] * v[t] @ lora_b[l]^T  rounded once
+ * A row whose id lies outside [0, num_adapters) has the projection alone.
+ *   x           dtype [m, k] (MI_BF16 or MI_F16);  w dtype [n, k]
+ *   lora_a      dtype [num_adapters, rank, k];  lora_b dtype [num_adapters, n, rank].
+ *               Adapters of lower rank are padded with zeros
+ *   lora_ids    int32 [m], in any order;  lora_scale fp32 [num_adapters], NULL: 1
+ *   bias        dtype [n] or NULL
+ *   out         out_dtype [m, n] (dtype or MI_F32)
+ *   act         fp32 [m, rank] or NULL: v, 0 for rows without an adapter, which
+ *               mi_mm_lora_backward takes
+ *   workspace   at least mi_mm_lora_workspace_size(..., 0) bytes, 256-byte aligned, no
+ *               initialisation needed
+ * v is kept to 16 bits at least (24 for fp32 outputs) for the second product, and all
+ * sums are fp32.  What one request's rows or adapter hold, NaN among it, changes no
+ * other request's rows.
+ * Requirements: n % 8 == 0, k % 8 == 0, rank a multiple of 8 in [8, 256],
+ * num_adapters in [1, 1024], everything but lora_ids and lora_scale 16-byte aligned,
+ * out and act overlap nothing.  n or k of 2^20 or more, or n * k of 2^30 or more,
+ * returns MI_EUNSUPPORTED.  m == 0 is a no-op.
+ */
+MI_API size_t mi_mm_lora_workspace_size(int64_t m, int64_t n, int64_t k, int64_t num_adapters,
+                                     int64_t rank, int backward);
+MI_API mi_status mi_mm_lora(const void* x, int64_t m, int64_t k, mi_dtype dtype, const void* w,
+                         int64_t n, const void* lora_a, const void* lora_b,
+                         int64_t num_adapters, int64_t rank, const int32_t* lora_ids,
+                         const float* lora_scale, const void* bias, void* out,
+                         mi_dtype out_dtype, float* act, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/*
+ * Its gradients, given grad_out of out (dtype [m, n]); w, bias and lora_scale are
+ * frozen.  With u[t] = grad_out[t] @ lora_b[l]:
+ *     grad_x[t] = grad_out[t] @ w + lora_scale[l] * u[t] @ lora_a[l]      rounded once
+ *     grad_a[l] = lora_scale[l] * sum_{t of l} u[t]^T x[t]
+ *     grad_b[l] = lora_scale[l] * sum_{t of l} grad_out[t]^T v[t]
+ * grad_a and grad_b are written for every adapter, zeros where it has no row.  The
+ * sums run in an order that depends on the sizes and ids alone: equal inputs give
+ * equal bits.
+ *   act         v as mi_mm_lora left it, or NULL: computed again from x
+ *   grad_x      dtype [m, k], or NULL (w is then not read)
+ *   grad_a      grad_dtype [num_adapters, rank, k] (dtype or MI_F32), and
+ *   grad_b      grad_dtype [num_adapters, n, rank]; both or neither (x is then not read)
+ *   workspace   at least mi_mm_lora_workspace_size(..., 1) bytes
+ * Requirements: as above; the gradients overlap nothing.  grad_a and grad_b of more
+ * rows than a 31-bit byte offset reaches (m * max(n, k) of 2^30 or more) return
+ * MI_EUNSUPPORTED.  m == 0 writes zeros to grad_a and grad_b.
+ */
+MI_API mi_status mi_mm_lora_backward(const void* grad_out, const void* x, int64_t m, int64_t k,
+                                  mi_dtype dtype, const void* w, int64_t n, const void* lora_a,
+                                  const void* lora_b, int64_t num_adapters, int64_t rank,
+                                  const int32_t* lora_ids, const float* lora_scale,
+                                  const float* act, void* grad_x, void* grad_a, void* grad_b,
+                                  mi_dtype grad_dtype, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/*
+ * The router's choice: topk_ids[t] are the top_k largest logits of token t, in falling
+ * order, ties to the lowest index, and
+ *     topk_weights[t, j] = softmax(logits[t])[topk_ids[t, j]]            fp32
+ * divided by their sum over j if renormalize is not 0.  A logit of -inf is never
+ * chosen: where a token has fewer than top_k others the rest has id -1 and weight 0.
+ * NaN is above every number and makes the token's weights NaN.
+ *   logits       logits_dtype [num_tokens, num_experts] (bf16, fp16 or fp32)
+ *   token_mask   uint8 [num_tokens] or NULL: tokens with 0 (padding) get ids -1 and
+ *                weights 0, and their logits are not looked at
+ *   topk_weights fp32, topk_ids int32 [num_tokens, top_k]: the operands of
+ *                mi_moe_route_permutation and mi_moe_combine_rows
+ * Requirements: num_experts in [1, 1024], top_k in [1, min(num_experts, 64)],
+ * num_tokens * top_k < 2^31; the outputs overlap nothing.  num_tokens == 0 is a no-op.
+ */
+MI_API mi_status mi_moe_route_topk(const void* logits, mi_dtype logits_dtype, int64_t num_tokens,
+                                int64_t num_experts, int64_t top_k, int renormalize,
+                                const uint8_t* token_mask, float* topk_weights,
+                                int32_t* topk_ids, void* stream);
+
+/*
+ * The balance of a batch, over the tokens that token_mask leaves in:
+ *     counts[e] = choices of expert e in topk_ids     (ids outside [0, num_experts): none)
+ *     loss      = coef * num_experts * sum_e f[e] * P[e]
+ *     slopes[e] = coef * num_experts * f[e] / tokens  (d loss / d softmax(logits[t])[e])
+ * with f = counts / sum(counts) and P[e] the mean of softmax(logits[t])[e].  With no
+ * token or no choice, loss and slopes are 0.  All sums run in an order that depends on
+ * the sizes alone.
+ *   given_counts  int32 [num_experts] or NULL: f is taken from these instead (counts
+ *                 summed over more tokens than the call's, such as other ranks')
+ *   loss          fp32 [1];  counts int32 [num_experts];  slopes fp32 [num_experts]
+ *   workspace     at least mi_moe_balance_loss_workspace_size() bytes, 4-byte aligned
+ * num_tokens == 0 writes zeros.
+ */
+MI_API size_t mi_moe_balance_loss_workspace_size(int64_t num_tokens, int64_t num_experts);
+MI_API mi_status mi_moe_balance_loss(const void* logits, mi_dtype logits_dtype,
+                                  int64_t num_tokens, int64_t num_experts,
+                                  const int32_t* topk_ids, int64_t top_k,
+                                  const uint8_t* token_mask, const int32_t* given_counts,
+                                  float coef, float* loss, int32_t* counts, float* slopes,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The gradient of the logits: with p = softmax(logits[t]) and
+ *     q = grad_loss * slopes + (grad_weights[t] scattered to topk_ids[t]),
+ *     grad_logits[t] = p * (q - sum_e p[e] q[e])
+ * and for renormalised weights, instead of grad_weights in q, at topk_ids[t, j] beside it
+ *     topk_weights[t, j] * (grad_weights[t, j] - sum_i grad_weights[t, i] * topk_weights[t, i]).
+ * Slots whose id lies outside [0, num_experts) have no gradient; tokens that token_mask
+ * takes out get zeros.
+ *   grad_weights  fp32 [num_tokens, top_k], or NULL: nothing comes through the weights
+ *                 (topk_ids and topk_weights are then not read)
+ *   topk_weights  as mi_moe_route_topk left them; read for renormalised weights only
+ *   slopes        fp32 [num_experts] of mi_moe_balance_loss with grad_loss fp32 [1], or both
+ *                 NULL
+ *   grad_logits   grad_dtype [num_tokens, num_experts]; may be logits itself (of its type),
+ *                 else overlaps nothing
+ */
+MI_API mi_status mi_moe_route_backward(const void* logits, mi_dtype logits_dtype,
+                                    int64_t num_tokens, int64_t num_experts,
+                                    const int32_t* topk_ids, const float* topk_weights,
+                                    const float* grad_weights, int64_t top_k, int renormalize,
+                                    const float* slopes, const float* grad_loss,
+                                    const uint8_t* token_mask, void* grad_logits,
+                                    mi_dtype grad_dtype, void* stream);
 
 #ifdef __cplusplus
 }

@@ -41,6 +41,13 @@ EXPORTS = [
     "mi_grouped_mm_fp8_block",
     "mi_moe_combine_rows",
     "mi_moe_combine_rows_backward",
+    "mi_mm_lora_workspace_size",
+    "mi_mm_lora",
+    "mi_mm_lora_backward",
+    "mi_moe_route_topk",
+    "mi_moe_balance_loss_workspace_size",
+    "mi_moe_balance_loss",
+    "mi_moe_route_backward",
 ]
 
 _lib = None
@@ -132,6 +139,23 @@ def lib() -> ctypes.CDLL:
         L.mi_moe_combine_rows_backward.restype = I32
         L.mi_moe_combine_rows_backward.argtypes = [P, I32, P, I32, I64, I64, P, P, P, I64, I64,
                                                    P, P, P]
+        L.mi_mm_lora_workspace_size.restype = SZ
+        L.mi_mm_lora_workspace_size.argtypes = [I64, I64, I64, I64, I64, I32]
+        L.mi_mm_lora.restype = I32
+        L.mi_mm_lora.argtypes = [P, I64, I64, I32, P, I64, P, P, I64, I64, P, P, P, P, I32, P, P,
+                                 SZ, P]
+        L.mi_mm_lora_backward.restype = I32
+        L.mi_mm_lora_backward.argtypes = [P, P, I64, I64, I32, P, I64, P, P, I64, I64, P, P, P, P,
+                                          P, P, I32, P, SZ, P]
+        L.mi_moe_route_topk.restype = I32
+        L.mi_moe_route_topk.argtypes = [P, I32, I64, I64, I64, I32, P, P, P, P]
+        L.mi_moe_balance_loss_workspace_size.restype = SZ
+        L.mi_moe_balance_loss_workspace_size.argtypes = [I64, I64]
+        L.mi_moe_balance_loss.restype = I32
+        L.mi_moe_balance_loss.argtypes = [P, I32, I64, I64, P, I64, P, P, F32, P, P, P, P, SZ, P]
+        L.mi_moe_route_backward.restype = I32
+        L.mi_moe_route_backward.argtypes = [P, I32, I64, I64, P, P, P, I64, I32, P, P, P, P, I32,
+                                            P]
         _lib = L
     return _lib
 

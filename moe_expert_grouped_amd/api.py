@@ -46,6 +46,13 @@ __all__ = [
     "moe_combine_rows",
     "moe_combine_rows_backward",
     "moe_permute_rows_backward",
+    "mm_lora",
+    "mm_lora_backward",
+    "lora_mm_workspace_bytes",
+    "moe_route_topk",
+    "moe_balance_loss",
+    "moe_route_backward",
+    "balance_workspace_bytes",
 ]
 
 _DT = {torch.bfloat16: MI_BF16, torch.float16: MI_F16, torch.float32: MI_F32}
@@ -924,3 +931,310 @@ def moe_combine_rows_backward(grad_out: torch.Tensor, rows: torch.Tensor,
             _ptr(inverse), topk_weights.data_ptr(), T, top_k, grad_rows.data_ptr(),
             _ptr(grad_weights))
     return grad_rows, grad_weights
+
+
+# ---------------------------------------------------------------------------
+# a projection with low-rank adapters
+# ---------------------------------------------------------------------------
+
+_HALF = (torch.bfloat16, torch.float16)
+
+
+def lora_mm_workspace_bytes(m, n, k, num_adapters, rank, *, backward: bool = False) -> int:
+    """Workspace of :func:`mm_lora` (or of :func:`mm_lora_backward`)."""
+    return int(_lib.lib().mi_mm_lora_workspace_size(m, n, k, num_adapters, rank, int(backward)))
+
+
+def _lora_operands(name, rows, cols, w, lora_a, lora_b, lora_ids, lora_scale):
+    """(M, K, N, L, R) of x (or grad_out, of `cols` columns) and the adapters' operands."""
+    if not (rows.dim() == 2 and rows.dtype in _HALF):
+        raise ValueError(f"{name}: the rows must be a bfloat16 or float16 matrix")
+    if not (w.dim() == 2 and w.dtype == rows.dtype and w.shape[cols] == rows.shape[1]):
+        raise ValueError(f"{name}: w must be [N, K] of the rows' type")
+    (N, K), M = w.shape, rows.shape[0]
+    if not (lora_a.dim() == 3 and lora_a.dtype == rows.dtype and lora_a.shape[2] == K):
+        raise ValueError(f"{name}: lora_a must be [L, R, K] of the rows' type")
+    L, R = lora_a.shape[:2]
+    if not (lora_b.shape == (L, N, R) and lora_b.dtype == rows.dtype):
+        raise ValueError(f"{name}: lora_b must be [L, N, R] of the rows' type")
+    if not (lora_ids.dtype == torch.int32 and lora_ids.shape == (M,)):
+        raise ValueError(f"{name}: lora_ids must be int32 [M]")
+    if not (lora_scale is None or (lora_scale.dtype == torch.float32 and
+                                   lora_scale.shape == (L,))):
+        raise ValueError(f"{name}: lora_scale must be float32 [L]")
+    return M, K, N, L, R
+
+
+def _workspace(name, workspace, need, device):
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    if not (workspace.dtype == torch.uint8 and workspace.is_contiguous()):
+        raise ValueError(f"{name}: workspace must be a contiguous uint8 tensor")
+    return workspace
+
+
+def mm_lora(x: torch.Tensor, w: torch.Tensor, lora_a: torch.Tensor, lora_b: torch.Tensor,
+            lora_ids: torch.Tensor, lora_scale: torch.Tensor | None = None, *,
+            bias: torch.Tensor | None = None, out: torch.Tensor | None = None,
+            out_dtype: torch.dtype | None = None, with_act: bool = False,
+            act: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """``out[t] = x[t] @ w^T + bias + lora_scale[l] * (x[t] @ lora_a[l]^T) @ lora_b[l]^T``
+    with ``l = lora_ids[t]``: a projection that many requests share, each with its own
+    low-rank adapter.
+
+    ``x`` bf16 or fp16 ``[M, K]``, ``w`` ``[N, K]``, ``lora_a`` ``[L, R, K]``, ``lora_b``
+    ``[L, N, R]`` and ``bias`` ``[N]`` of that type; ``lora_ids`` int32 ``[M]`` in any order,
+    a row whose id lies outside ``[0, L)`` has the projection alone; ``lora_scale`` fp32
+    ``[L]`` (default 1).  K, N and R are multiples of 8, R at most 256, L at most 1024.
+    fp32 sums, one rounding to ``out_dtype`` (x's type, the default, or float32).
+
+    With ``with_act`` (or a tensor ``act``) the call returns ``(out, act)``: ``act`` fp32
+    ``[M, R]`` is ``x[t] @ lora_a[l]^T``, which :func:`mm_lora_backward` takes.
+    """
+    name = "mm_lora"
+    M, K, N, L, R = _lora_operands(name, x, 1, w, lora_a, lora_b, lora_ids, lora_scale)
+    out_dtype = x.dtype if out_dtype is None else out_dtype
+    _need(out_dtype in (x.dtype, torch.float32), "mm_lora: out_dtype must be x's type or float32")
+    _need(bias is None or (bias.shape == (N,) and bias.dtype == x.dtype),
+          "mm_lora: bias must be [N] of x's type")
+    gpu = _one_gpu(name, x, w, lora_a, lora_b, lora_ids, lora_scale, bias, out, act, workspace)
+    x, w, lora_a, lora_b, lora_ids = (x.contiguous(), w.contiguous(), lora_a.contiguous(),
+                                      lora_b.contiguous(), lora_ids.contiguous())
+    lora_scale = None if lora_scale is None else lora_scale.contiguous()
+    bias = None if bias is None else bias.contiguous()
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=x.device)
+    else:
+        _own_out(name, "[M, N]", out, (M, N), out_dtype)
+    if act is None and with_act:
+        act = torch.empty((M, R), dtype=torch.float32, device=x.device)
+    _need(act is None or (act.shape == (M, R) and act.dtype == torch.float32 and
+                          act.is_contiguous()), "mm_lora: act must be contiguous float32 [M, R]")
+    L_ = _lib.lib()
+    workspace = _workspace(name, workspace, L_.mi_mm_lora_workspace_size(M, N, K, L, R, 0),
+                           x.device)
+    _launch(gpu, L_.mi_mm_lora, x.data_ptr(), M, K, _DT[x.dtype], w.data_ptr(), N,
+            lora_a.data_ptr(), lora_b.data_ptr(), L, R, lora_ids.data_ptr(), _ptr(lora_scale),
+            _ptr(bias), out.data_ptr(), _DT[out_dtype], _ptr(act), workspace.data_ptr(),
+            workspace.numel())
+    return out if act is None else (out, act)
+
+
+def mm_lora_backward(grad_out: torch.Tensor, x: torch.Tensor, w: torch.Tensor,
+                     lora_a: torch.Tensor, lora_b: torch.Tensor, lora_ids: torch.Tensor,
+                     lora_scale: torch.Tensor | None = None, *, act: torch.Tensor | None = None,
+                     with_x: bool = True, with_adapters: bool = True,
+                     grad_dtype: torch.dtype | None = None, grad_x: torch.Tensor | None = None,
+                     grad_a: torch.Tensor | None = None, grad_b: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None):
+    """``(grad_x, grad_a, grad_b)`` of :func:`mm_lora` for ``grad_out`` ``[M, N]`` of x's type;
+    ``w``, the bias and the scales are frozen::
+
+        grad_x[t] = grad_out[t] @ w + lora_scale[l] * (grad_out[t] @ lora_b[l]) @ lora_a[l]
+        grad_a[l] = lora_scale[l] * sum_t (grad_out[t] @ lora_b[l])^T x[t]     t with id l
+        grad_b[l] = lora_scale[l] * sum_t grad_out[t]^T (x[t] @ lora_a[l]^T)
+
+    ``grad_a`` and ``grad_b`` are like the banks, in ``grad_dtype`` (the banks' type, the
+    default, or float32), zeros for an adapter without rows.  ``act`` is the forward's;
+    without it, it is computed again.  ``with_x=False`` or ``with_adapters=False`` leaves
+    those gradients out (None).  Equal inputs give equal bits.
+    """
+    name = "mm_lora_backward"
+    M, K, N, L, R = _lora_operands(name, grad_out, 0, w, lora_a, lora_b, lora_ids, lora_scale)
+    _need(x.shape == (M, K) and x.dtype == grad_out.dtype,
+          "mm_lora_backward: x must be [M, K] of grad_out's type")
+    grad_dtype = x.dtype if grad_dtype is None else grad_dtype
+    _need(grad_dtype in (x.dtype, torch.float32),
+          "mm_lora_backward: grad_dtype must be the banks' type or float32")
+    _need(with_x or with_adapters, "mm_lora_backward: no gradient is asked for")
+    _need(with_x or grad_x is None, "mm_lora_backward: grad_x needs with_x")
+    _need(with_adapters or (grad_a is None and grad_b is None),
+          "mm_lora_backward: grad_a and grad_b need with_adapters")
+    _need(act is None or (act.shape == (M, R) and act.dtype == torch.float32),
+          "mm_lora_backward: act must be float32 [M, R]")
+    gpu = _one_gpu(name, grad_out, x, w, lora_a, lora_b, lora_ids, lora_scale, act, grad_x,
+                   grad_a, grad_b, workspace)
+    grad_out, x, w, lora_a, lora_b, lora_ids = (
+        grad_out.contiguous(), x.contiguous(), w.contiguous(), lora_a.contiguous(),
+        lora_b.contiguous(), lora_ids.contiguous())
+    lora_scale = None if lora_scale is None else lora_scale.contiguous()
+    act = None if act is None else act.contiguous()
+
+    def own(t, what, shape, dtype):
+        if t is None:
+            return torch.empty(shape, dtype=dtype, device=x.device)
+        _need(t.shape == shape and t.dtype == dtype and t.is_contiguous(),
+              f"mm_lora_backward: {what} must be contiguous {tuple(shape)} of its type")
+        return t
+
+    if with_x:
+        grad_x = own(grad_x, "grad_x", (M, K), x.dtype)
+    if with_adapters:
+        grad_a = own(grad_a, "grad_a", (L, R, K), grad_dtype)
+        grad_b = own(grad_b, "grad_b", (L, N, R), grad_dtype)
+    L_ = _lib.lib()
+    workspace = _workspace(name, workspace, L_.mi_mm_lora_workspace_size(M, N, K, L, R, 1),
+                           x.device)
+    _launch(gpu, L_.mi_mm_lora_backward, grad_out.data_ptr(), x.data_ptr(), M, K, _DT[x.dtype],
+            w.data_ptr(), N, lora_a.data_ptr(), lora_b.data_ptr(), L, R, lora_ids.data_ptr(),
+            _ptr(lora_scale), _ptr(act), _ptr(grad_x), _ptr(grad_a), _ptr(grad_b),
+            _DT[grad_dtype], workspace.data_ptr(), workspace.numel())
+    return grad_x, grad_a, grad_b
+
+
+# ---------------------------------------------------------------------------
+# router
+# ---------------------------------------------------------------------------
+
+def _router_logits(name, logits, token_mask):
+    if not (logits.dim() == 2 and logits.dtype in _DT):
+        raise ValueError(f"{name}: logits must be [T, E] bf16, fp16 or fp32")
+    if not (token_mask is None or (token_mask.dtype in (torch.bool, torch.uint8) and
+                                   token_mask.shape == (logits.shape[0],))):
+        raise ValueError(f"{name}: token_mask must be bool or uint8 [T]")
+
+
+def moe_route_topk(logits: torch.Tensor, top_k: int, *, renormalize: bool = True,
+                   token_mask: torch.Tensor | None = None,
+                   topk_weights: torch.Tensor | None = None,
+                   topk_ids: torch.Tensor | None = None):
+    """``(topk_weights, topk_ids)`` of the router's ``logits`` (bf16, fp16 or fp32 ``[T, E]``):
+    the ``top_k`` largest of every token in falling order, ties to the lowest expert, and
+    their softmax probabilities in fp32, divided by their sum with ``renormalize``.  They
+    are the operands of :func:`moe_route_permutation` and :func:`moe_combine_rows`.
+
+    A logit of -inf is never chosen: where a token has fewer than ``top_k`` others, the
+    rest has id -1 and weight 0.  NaN is above every number and makes its token's weights
+    NaN.  Tokens that ``token_mask`` (bool or uint8 ``[T]``) takes out, padding, have ids -1
+    and weights 0.  E is at most 1024, ``top_k`` at most 64.
+    """
+    name = "moe_route_topk"
+    _router_logits(name, logits, token_mask)
+    top_k = int(top_k)
+    T, E = logits.shape
+    gpu = _one_gpu(name, logits, token_mask, topk_weights, topk_ids)
+    logits = logits.contiguous()
+    token_mask = None if token_mask is None else token_mask.contiguous()
+    _need(1 <= top_k <= min(E, 64), "moe_route_topk: top_k must be in [1, min(E, 64)]")
+    if topk_weights is None:
+        topk_weights = torch.empty((T, top_k), dtype=torch.float32, device=logits.device)
+    if topk_ids is None:
+        topk_ids = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
+    for t, dt in ((topk_weights, torch.float32), (topk_ids, torch.int32)):
+        _need(t.shape == (T, top_k) and t.dtype == dt and t.is_contiguous(),
+              "moe_route_topk: topk_weights and topk_ids must be contiguous float32 and int32 "
+              "[T, top_k]")
+    _launch(gpu, _lib.lib().mi_moe_route_topk, logits.data_ptr(), _DT[logits.dtype], T, E, top_k,
+            int(renormalize), _ptr(token_mask), topk_weights.data_ptr(), topk_ids.data_ptr())
+    return topk_weights, topk_ids
+
+
+def balance_workspace_bytes(num_tokens, num_experts) -> int:
+    """Workspace of :func:`moe_balance_loss`."""
+    return int(_lib.lib().mi_moe_balance_loss_workspace_size(num_tokens, num_experts))
+
+
+def moe_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, *, coef: float = 1.0,
+                     token_mask: torch.Tensor | None = None,
+                     given_counts: torch.Tensor | None = None,
+                     loss: torch.Tensor | None = None, counts: torch.Tensor | None = None,
+                     slopes: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None):
+    """``(loss, counts, slopes)`` of a batch's routing: ``counts`` int32 ``[E]`` are the choices
+    of every expert in ``topk_ids`` (int32 ``[T, top_k]``, ids outside ``[0, E)`` are none),
+    ``loss = coef * E * sum_e f[e] * P[e]`` an fp32 scalar with ``f = counts / sum(counts)``
+    and ``P`` the mean of ``softmax(logits)``, and ``slopes`` fp32 ``[E]`` the loss's derivative
+    by each token's probabilities, which :func:`moe_route_backward` takes.  Tokens that
+    ``token_mask`` takes out count nowhere.  With ``given_counts`` (int32 ``[E]``: counts summed
+    over more than these tokens, such as all ranks' or micro-batches') ``f`` is theirs.
+    """
+    name = "moe_balance_loss"
+    _router_logits(name, logits, token_mask)
+    T, E = logits.shape
+    _need(topk_ids.dtype == torch.int32 and topk_ids.dim() == 2 and topk_ids.shape[0] == T and
+          topk_ids.shape[1] >= 1, "moe_balance_loss: topk_ids must be int32 [T, top_k]")
+    _need(given_counts is None or (given_counts.dtype == torch.int32 and
+                                   given_counts.shape == (E,)),
+          "moe_balance_loss: given_counts must be int32 [E]")
+    gpu = _one_gpu(name, logits, topk_ids, token_mask, given_counts, loss, counts, slopes,
+                   workspace)
+    logits, topk_ids = logits.contiguous(), topk_ids.contiguous()
+    token_mask = None if token_mask is None else token_mask.contiguous()
+    given_counts = None if given_counts is None else given_counts.contiguous()
+    if loss is None:
+        loss = torch.empty((), dtype=torch.float32, device=logits.device)
+    if counts is None:
+        counts = torch.empty(E, dtype=torch.int32, device=logits.device)
+    if slopes is None:
+        slopes = torch.empty(E, dtype=torch.float32, device=logits.device)
+    _need(loss.numel() == 1 and loss.dtype == torch.float32 and
+          counts.shape == (E,) and counts.dtype == torch.int32 and counts.is_contiguous() and
+          slopes.shape == (E,) and slopes.dtype == torch.float32 and slopes.is_contiguous(),
+          "moe_balance_loss: loss must be one float32, counts int32 [E], slopes float32 [E]")
+    L_ = _lib.lib()
+    workspace = _workspace(name, workspace, L_.mi_moe_balance_loss_workspace_size(T, E),
+                           logits.device)
+    _launch(gpu, L_.mi_moe_balance_loss, logits.data_ptr(), _DT[logits.dtype], T, E,
+            topk_ids.data_ptr(), topk_ids.shape[1], _ptr(token_mask), _ptr(given_counts),
+            float(coef), loss.data_ptr(), counts.data_ptr(), slopes.data_ptr(),
+            workspace.data_ptr(), workspace.numel())
+    return loss, counts, slopes
+
+
+def moe_route_backward(logits: torch.Tensor, *, topk_ids: torch.Tensor | None = None,
+                       topk_weights: torch.Tensor | None = None,
+                       grad_weights: torch.Tensor | None = None, renormalize: bool = True,
+                       slopes: torch.Tensor | None = None,
+                       grad_loss: torch.Tensor | None = None,
+                       token_mask: torch.Tensor | None = None,
+                       grad_dtype: torch.dtype | None = None,
+                       grad_logits: torch.Tensor | None = None) -> torch.Tensor:
+    """The gradient of ``logits`` through the weights of :func:`moe_route_topk`
+    (``grad_weights`` fp32 ``[T, top_k]``, with its ``topk_ids`` and, where they were
+    renormalised, its ``topk_weights``), through the loss of :func:`moe_balance_loss` (its
+    ``slopes`` with ``grad_loss``, one fp32 value on the GPU), or through both.
+
+    Slots whose id lies outside ``[0, E)`` have no gradient; tokens that ``token_mask`` takes
+    out get zeros.  ``grad_logits`` ``[T, E]`` is of ``grad_dtype`` (the logits' type by
+    default) and may be ``logits`` itself.
+    """
+    name = "moe_route_backward"
+    _router_logits(name, logits, token_mask)
+    T, E = logits.shape
+    top_k = 1
+    _need(grad_weights is not None or slopes is not None,
+          "moe_route_backward: grad_weights or slopes is needed")
+    if grad_weights is not None:
+        _need(grad_weights.dtype == torch.float32 and grad_weights.dim() == 2 and
+              grad_weights.shape[0] == T and grad_weights.shape[1] >= 1,
+              "moe_route_backward: grad_weights must be float32 [T, top_k]")
+        top_k = grad_weights.shape[1]
+        _need(topk_ids is not None and topk_ids.dtype == torch.int32 and
+              topk_ids.shape == grad_weights.shape,
+              "moe_route_backward: grad_weights needs topk_ids, int32 [T, top_k]")
+        _need(not renormalize or (topk_weights is not None and
+                                  topk_weights.dtype == torch.float32 and
+                                  topk_weights.shape == grad_weights.shape),
+              "moe_route_backward: renormalised weights need topk_weights, float32 [T, top_k]")
+    _need((slopes is None) == (grad_loss is None),
+          "moe_route_backward: slopes and grad_loss are given together")
+    _need(slopes is None or (slopes.dtype == torch.float32 and slopes.shape == (E,) and
+                             grad_loss.dtype == torch.float32 and grad_loss.numel() == 1),
+          "moe_route_backward: slopes must be float32 [E] and grad_loss one float32")
+    gpu = _one_gpu(name, logits, topk_ids, topk_weights, grad_weights, slopes, grad_loss,
+                   token_mask, grad_logits)
+    logits = logits.contiguous()
+    topk_ids, topk_weights, grad_weights, slopes, token_mask = (
+        None if t is None else t.contiguous()
+        for t in (topk_ids, topk_weights, grad_weights, slopes, token_mask))
+    if grad_logits is None:
+        grad_logits = torch.empty((T, E), dtype=grad_dtype or logits.dtype, device=logits.device)
+    _need(grad_logits.shape == (T, E) and grad_logits.dtype in _DT and
+          grad_dtype in (None, grad_logits.dtype) and grad_logits.is_contiguous(),
+          "moe_route_backward: grad_logits must be contiguous [T, E] of grad_dtype (bf16, fp16 or "
+          "fp32)")
+    _launch(gpu, _lib.lib().mi_moe_route_backward, logits.data_ptr(), _DT[logits.dtype], T, E,
+            _ptr(topk_ids), _ptr(topk_weights), _ptr(grad_weights), top_k, int(renormalize),
+            _ptr(slopes), _ptr(grad_loss), _ptr(token_mask), grad_logits.data_ptr(),
+            _DT[grad_logits.dtype])
+    return grad_logits

@@ -1,0 +1,1176 @@
+// A shared projection with the low-rank adapters of many requests beside it, and
+// the gradients, on gfx950.  With l = ids[t] the adapter of row t (none where it
+// lies outside [0, L)):
+//
+//   v[t]   = x[t] A[l]^T                                   [R], fp32
+//   out[t] = x[t] w^T + bias + s[l] v[t] B[l]^T            [N], rounded once
+//   u[t]   = go[t] B[l]                                    [R], fp32
+//   gx[t]  = go[t] w + s[l] u[t] A[l]                      [K], rounded once
+//   gA[l]  = s[l] sum_{t of l} u[t]^T x[t]                 [R, K]
+//   gB[l]  = s[l] sum_{t of l} go[t]^T v[t]                [N, R]
+//
+// Steps, each a launch on the caller's stream:
+//   plan    one workgroup sorts the rows by adapter (stable), cuts every adapter's
+//           rows into items of 16 and its items into chunks
+//   shrink  v (or u) of an item; kept as three bf16 pieces whose sum has 24 bits,
+//           so that the second product runs on bf16 MFMAs without a rounding of v
+//   mm      the dense product over rows in sorted order, the adapters' part added
+//           to the same accumulators before the one rounding
+//   grads   gA and gB of a chunk of an adapter's rows, from the pieces; partial sums
+//           where an adapter has several chunks
+//   reduce  those partial sums in order
+#include "common.hpp"
+
+namespace mi {
+namespace {
+
+typedef __attribute__((address_space(3))) void* lds_void_ptr;
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4* lds_s16x4_ptr;
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+
+constexpr int LM_MAX_ADAPTERS = 1024;
+constexpr int LM_MAX_RANK = 256;
+constexpr int LM_ITEM = 16;            // rows of an item
+constexpr int LM_BK = 64;              // 128 bytes of a row of x: one step
+constexpr uint32_t LM_OUT = 0x80000000u;  // past every descriptor's range
+
+__device__ __forceinline__ lds_void_ptr lm_lds(void* p) { return (lds_void_ptr)(p); }
+
+// the sorted rows and what is cut from them
+struct LmPlan {
+  i32x2* order;      // [T] {row, adapter}; rows without one last, adapter L
+  int* seg;         // [L + 1] first position of every adapter
+  i32x4* items;      // {adapter, first position, rows, 0}
+  int* slot_row;    // [16 * items] row of every slot of an item, -1: none
+  i32x4* chunks;     // {adapter, first item, items, place of its partial sums or -1}
+  i32x4* spans;      // [L] {first chunk, chunks, first partial place or -1, 0}
+  int* totals;      // items, chunks
+  uint16_t* zeros;  // a row of zeros
+};
+
+// ---------------------------------------------------------------------------
+// plan
+// ---------------------------------------------------------------------------
+constexpr int PL_T = 1024, PL_W = PL_T / 64;
+
+// exclusive block sums of v, all of it in `total`
+__device__ __forceinline__ uint64_t pl_scan(uint64_t v, uint64_t* s, uint64_t* total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  uint64_t incl = v;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const uint64_t up = __shfl_up(incl, o, 64);
+    if (lane >= o) incl += up;
+  }
+  __syncthreads();
+  if (lane == 63) s[wave] = incl;
+  __syncthreads();
+  uint64_t before = 0, all = 0;
+  for (int w = 0; w < PL_W; ++w) {
+    if (w < wave) before += s[w];
+    all += s[w];
+  }
+  *total = all;
+  return before + incl - v;
+}
+
+// lanes of the wavefront that hold the same value
+__device__ __forceinline__ uint64_t pl_peers(int v, int bits) {
+  uint64_t peers = ~0ull;
+  for (int b = 0; b < bits; ++b) {
+    const bool bit = (v >> b) & 1;
+    const uint64_t bal = __ballot(bit);
+    peers &= bit ? bal : ~bal;
+  }
+  return peers;
+}
+
+__global__ __launch_bounds__(PL_T) void lm_plan_kernel(const int32_t* __restrict__ ids, int T,
+                                                       int L, int chunk_items, int zero_chunks,
+                                                       LmPlan p) {
+  __shared__ int s_cnt[PL_W * (LM_MAX_ADAPTERS + 1)];  // [PL_W][L + 1]
+  __shared__ int s_item0[LM_MAX_ADAPTERS], s_seg[LM_MAX_ADAPTERS];
+  __shared__ uint64_t s_scan[PL_W];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  for (int i = tid; i < PL_W * (L + 1); i += PL_T) s_cnt[i] = 0;
+  for (int i = tid; i < zero_chunks; i += PL_T)
+    gst<u32x4>(p.zeros + i * 8, u32x4{0, 0, 0, 0});
+  __syncthreads();
+  // a wavefront has a run of rows, 64 at a time
+  const int per = ((T + PL_W - 1) / PL_W + 63) & ~63;
+  const int r0 = min(wave * per, T), r1 = min(r0 + per, T);
+  const int bits = 32 - __builtin_clz(L);  // ids 0 .. L
+  int* const cnt = s_cnt + wave * (L + 1);
+  auto id_of = [&](int r) {
+    const int id = r < r1 ? gld<int32_t>(ids + r) : L;
+    return id < 0 || id > L ? L : id;
+  };
+  for (int r = r0; r < r1; r += 64) {
+    const int id = id_of(r + lane);
+    const uint64_t live = __ballot(r + lane < r1);
+    const uint64_t peers = pl_peers(id, bits) & live;
+    if (r + lane < r1 && (peers & ((1ull << lane) - 1)) == 0) cnt[id] += __popcll(peers);
+    __builtin_amdgcn_wave_barrier();
+  }
+  __syncthreads();
+  // thread l: adapter l
+  int rows = 0;
+  if (tid < L)
+    for (int w = 0; w < PL_W; ++w) rows += s_cnt[w * (L + 1) + tid];
+  const int items = (rows + LM_ITEM - 1) / LM_ITEM;
+  const int chunks = tid < L ? max((items + chunk_items - 1) / chunk_items, 1) : 0;
+  uint64_t all_rows, all_chunks;
+  const uint64_t a = pl_scan(static_cast<uint64_t>(rows) | static_cast<uint64_t>(items) << 32,
+                             s_scan, &all_rows);
+  const uint64_t b = pl_scan(static_cast<uint64_t>(chunks) |
+                                 static_cast<uint64_t>(chunks > 1 ? chunks : 0) << 32,
+                             s_scan, &all_chunks);
+  const int seg = static_cast<int>(a), item0 = static_cast<int>(a >> 32);
+  const int chunk0 = static_cast<int>(b), part0 = static_cast<int>(b >> 32);
+  if (tid < L) {
+    s_seg[tid] = seg;
+    s_item0[tid] = item0;
+    gst<int>(p.seg + tid, seg);
+    for (int c = 0; c < chunks; ++c)
+      gst<i32x4>(p.chunks + chunk0 + c,
+                i32x4{tid, item0 + c * chunk_items, min(items - c * chunk_items, chunk_items),
+                     chunks > 1 ? part0 + c : -1});
+    gst<i32x4>(p.spans + tid, i32x4{chunk0, chunks, chunks > 1 ? part0 : -1, 0});
+    for (int i = rows; i < items * LM_ITEM; ++i) gst<int>(p.slot_row + item0 * LM_ITEM + i, -1);
+    int run = seg;
+    for (int w = 0; w < PL_W; ++w) {
+      const int c = s_cnt[w * (L + 1) + tid];
+      s_cnt[w * (L + 1) + tid] = run;
+      run += c;
+    }
+  }
+  if (tid == 0) {
+    const int in = static_cast<int>(all_rows);
+    gst<int>(p.seg + L, in);
+    gst<int>(p.totals, static_cast<int>(all_rows >> 32));
+    gst<int>(p.totals + 1, static_cast<int>(all_chunks));
+    int run = in;
+    for (int w = 0; w < PL_W; ++w) {
+      const int c = s_cnt[w * (L + 1) + L];
+      s_cnt[w * (L + 1) + L] = run;
+      run += c;
+    }
+  }
+  __syncthreads();
+  for (int r = r0; r < r1; r += 64) {
+    const int row = r + lane, id = id_of(row);
+    const uint64_t live = __ballot(row < r1);
+    const uint64_t peers = pl_peers(id, bits) & live;
+    const uint64_t below = peers & ((1ull << lane) - 1);
+    int pos = 0;
+    if (row < r1) {
+      pos = cnt[id] + __popcll(below);
+      // pos < T holds where the ids did not change between the passes
+      if (pos < T) gst<i32x2>(p.order + pos, i32x2{row, id});
+      if (id < L && pos < T) {
+        const int rank = pos - s_seg[id], item = s_item0[id] + rank / LM_ITEM;
+        gst<int>(p.slot_row + item * LM_ITEM + rank % LM_ITEM, row);
+        if (rank % LM_ITEM == 0)
+          gst<i32x4>(p.items + item, i32x4{id, pos, 0, 0});
+      }
+    }
+    // LDS operations of one wavefront complete in order
+    __builtin_amdgcn_wave_barrier();
+    if (row < r1 && below == 0) cnt[id] = pos + __popcll(peers);
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// numbers
+// ---------------------------------------------------------------------------
+template <bool F16>
+__device__ __forceinline__ f32x4 lm_mfma(u32x4 a, u32x4 b, f32x4 c) {
+  if constexpr (F16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
+                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// bf16 pieces of v: each the rounding of what the ones before leave, 24 bits together;
+// where the first is not finite the others are 0
+struct LmPieces { uint16_t p[3]; };
+__device__ __forceinline__ LmPieces lm_pieces(float v) {
+  LmPieces o;
+  float rest = v;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const __bf16 h = static_cast<__bf16>(rest);
+    o.p[i] = __builtin_bit_cast(uint16_t, h);
+    rest = (o.p[i] & 0x7f80) == 0x7f80 ? 0.f : rest - static_cast<float>(h);
+  }
+  return o;
+}
+
+// eight fp16 values as two bf16 pieces, exact: fp16 has 11 bits, and no exponent that
+// bf16 lacks (not finite: second piece 0)
+__device__ __forceinline__ void lm_split(u32x4 h, u32x4& hi, u32x4& lo) {
+  const f16x8 f = __builtin_bit_cast(f16x8, h);
+  bf16x8 a, b;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float v = static_cast<float>(f[i]);
+    a[i] = static_cast<__bf16>(v);
+    const float rest = v - static_cast<float>(a[i]);
+    b[i] = static_cast<__bf16>(rest == rest ? rest : 0.f);
+  }
+  hi = __builtin_bit_cast(u32x4, a);
+  lo = __builtin_bit_cast(u32x4, b);
+}
+
+// eight values of one column, down the rows: two transposed reads of four rows
+__device__ __forceinline__ u32x4 lm_column(const uint8_t* first, const uint8_t* second) {
+  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_ptr)(first));
+  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_ptr)(second));
+  const u32x2 x = __builtin_bit_cast(u32x2, a), y = __builtin_bit_cast(u32x2, b);
+  return u32x4{x[0], x[1], y[0], y[1]};
+}
+
+// ---------------------------------------------------------------------------
+// shrink: one item's rows times its adapter's matrix.
+//   BT == false: bank [L, R, C], v[t, r] = sum_c x[t, c] bank[l, r, c]
+//   BT == true:  bank [L, C, R], v[t, r] = sum_c x[t, c] bank[l, c, r]
+// A workgroup has 16 rows and 16 NB ranks; its wavefronts take steps of 64 columns
+// in turn, and their sums are added in order in LDS.
+// ---------------------------------------------------------------------------
+struct LmShrink {
+  const void* x;          // [T, C]
+  const void* bank;
+  const float* scale;     // [L] or null
+  const float* act;       // [T, R]: also split these into pieces_t2, or null
+  LmPlan plan;
+  float* out;             // [T, R] unscaled, or null
+  uint16_t* pieces;       // [T, 3 RP] scaled, or null
+  uint16_t* pieces_t;     // [3 RP, slots] scaled, or null
+  uint16_t* pieces_t2;    // the same of act
+  int T, C, L, R, RP, slots;
+};
+
+constexpr int SH_W = 8;
+
+template <bool F16, bool BT, int NB>
+__global__ __launch_bounds__(64 * SH_W) void lm_shrink_kernel(LmShrink a) {
+  __shared__ __attribute__((aligned(16))) uint8_t s_buf[SH_W * 64 * NB * 32];
+  static_assert(64 * NB * 32 >= NB * 64 * 16, "the sums fit the stages");
+  const int item = blockIdx.x;
+  if (item >= gld<int>(a.plan.totals)) return;
+  const i32x4 it = gld<i32x4>(a.plan.items + item);
+  const int l = it.x;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int rank0 = blockIdx.y * 16 * NB;
+  const int row = gld<int>(a.plan.slot_row + item * LM_ITEM + r);
+  const int C = a.C, R = a.R, KT = (C + LM_BK - 1) / LM_BK;
+  const __amdgpu_buffer_rsrc_t xr =
+      buf_rsrc(a.x, static_cast<uint32_t>(a.T) * static_cast<uint32_t>(C) * 2u);
+  const __amdgpu_buffer_rsrc_t br =
+      buf_rsrc(static_cast<const uint16_t*>(a.bank) + static_cast<int64_t>(l) * R * C,
+               static_cast<uint32_t>(R) * static_cast<uint32_t>(C) * 2u);
+  const uint32_t vx = row >= 0 ? static_cast<uint32_t>(row) * C * 2 : LM_OUT;
+  f32x4 acc[NB];
+#pragma unroll
+  for (int j = 0; j < NB; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int kt = wave; kt < KT; kt += SH_W) {
+    u32x4 fx[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = kt * LM_BK + 32 * h + 8 * g;
+      fx[h] = buf_ld128(xr, c < C ? vx + c * 2 : LM_OUT, 0);
+    }
+    if constexpr (!BT) {
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int c = kt * LM_BK + 32 * h + 8 * g, rk = rank0 + 16 * j + r;
+          const u32x4 fb = buf_ld128(
+              br, c < C && rk < R ? (static_cast<uint32_t>(rk) * C + c) * 2 : LM_OUT, 0);
+          acc[j] = lm_mfma<F16>(fb, fx[h], acc[j]);
+        }
+    } else {
+      // this wavefront's stage: 64 rows of 16 NB ranks
+      uint8_t* const st = s_buf + wave * (64 * NB * 32);
+      constexpr int CPR = 2 * NB;  // 16-byte pieces of a row
+      u32x4 q[CPR];
+#pragma unroll
+      for (int i = 0; i < CPR; ++i) {
+        const int at = i * 64 + lane, c = kt * LM_BK + at / CPR, rk = rank0 + at % CPR * 8;
+        q[i] = buf_ld128(br, c < C && rk < R ? (static_cast<uint32_t>(c) * R + rk) * 2 : LM_OUT, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < CPR; ++i)
+        *reinterpret_cast<u32x4*>(st + (i * 64 + lane) * 16) = q[i];
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint8_t* at = st + (32 * h + 8 * g + (r >> 2)) * (NB * 32) + j * 32 + (r & 3) * 8;
+          acc[j] = lm_mfma<F16>(lm_column(at, at + 4 * NB * 32), fx[h], acc[j]);
+        }
+      __builtin_amdgcn_wave_barrier();
+    }
+  }
+  __syncthreads();
+  f32x4* const red = reinterpret_cast<f32x4*>(s_buf);
+#pragma unroll
+  for (int j = 0; j < NB; ++j) red[(wave * NB + j) * 64 + lane] = acc[j];
+  __syncthreads();
+  // quad q: ranks 16 j + 4 g .. of the row at slot q % 16
+  for (int q = tid; q < NB * 64; q += 64 * SH_W) {
+    f32x4 v = red[q];
+    for (int w = 1; w < SH_W; ++w) v += red[w * NB * 64 + q];
+    const int rk = rank0 + 16 * (q >> 6) + 4 * ((q & 63) >> 4);
+    if (rk >= a.RP) continue;
+    const int slot = item * LM_ITEM + (q & 15);
+    const int t = gld<int>(a.plan.slot_row + slot);
+    const float s = a.scale != nullptr ? gld<float>(a.scale + l) : 1.f;
+    auto put = [&](f32x4 w, uint16_t* rows, uint16_t* cols) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = t >= 0 && rk < R ? w[i] * s : 0.f;
+      LmPieces p[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p[i] = lm_pieces(w[i]);
+#pragma unroll
+      for (int c = 0; c < 3; ++c) {
+        if (rows != nullptr && t >= 0)
+          gst<u32x2>(rows + (static_cast<int64_t>(t) * 3 + c) * a.RP + rk,
+                     u32x2{p[0].p[c] | static_cast<uint32_t>(p[1].p[c]) << 16,
+                           p[2].p[c] | static_cast<uint32_t>(p[3].p[c]) << 16});
+        if (cols != nullptr)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            gst<uint16_t>(cols + (static_cast<int64_t>(c) * a.RP + rk + i) * a.slots + slot,
+                          p[i].p[c]);
+      }
+    };
+    if (a.out != nullptr && t >= 0 && rk < R)
+      gst<f32x4>(a.out + static_cast<int64_t>(t) * R + rk, v);
+    if (a.pieces != nullptr || a.pieces_t != nullptr) put(v, a.pieces, a.pieces_t);
+    if (a.act != nullptr) {
+      const f32x4 w = t >= 0 && rk < R ? gld<f32x4>(a.act + static_cast<int64_t>(t) * R + rk)
+                                       : f32x4{0.f, 0.f, 0.f, 0.f};
+      put(w, nullptr, a.pieces_t2);
+    }
+  }
+}
+
+// rows without an adapter have zeros for activations
+__global__ __launch_bounds__(256) void lm_zero_act_kernel(const int32_t* __restrict__ ids, int T,
+                                                          int L, int quads, float* act) {
+  const int64_t n = static_cast<int64_t>(T) * quads;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n;
+       i += static_cast<int64_t>(gridDim.x) * 256) {
+    const int id = gld<int32_t>(ids + i / quads);
+    if (id < 0 || id >= L) gst<f32x4>(act + i * 4, f32x4{0.f, 0.f, 0.f, 0.f});
+  }
+}
+
+// ---------------------------------------------------------------------------
+// mm: out = x w^T (BT: x w) plus the pieces times the adapters' matrix
+//   BT == false: w [n, k], bank [L, n, R]
+//   BT == true:  w [k, n], bank [L, R, n]
+// ---------------------------------------------------------------------------
+struct LmMm {
+  const void* x;          // [T, k]
+  const void* w;
+  const void* bank;
+  const void* bias;       // [n] or null
+  const uint16_t* pieces; // [T, 3 RP]
+  LmPlan plan;
+  void* out;              // [T, n]
+  int T, k, n, L, R, RP;
+};
+
+// chunk c (16 bytes) of LDS row R sits at slot c ^ lm_swz(R)
+__device__ __forceinline__ int lm_swz(int row) { return (row & 7) ^ ((row >> 3) & 1); }
+// 32-byte pieces of a transposed tile's row (BN / 16 of them): the 16 rows that a
+// transposed read touches lie in 8 different ones of 256 bytes
+template <int BN>
+__device__ __forceinline__ int lm_tswz(int row) {
+  if constexpr (BN >= 128) return (row & 3) | ((row >> 3) & 1) << 2;
+  else return ((row >> 1) & 1) | ((row >> 3) & 1) << 1;
+}
+
+template <int N>
+__device__ __forceinline__ void lm_wait_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));  // vmcnt(N) lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
+}
+
+template <bool F16, bool BT, int WM, int WN, int FM, int FN, int NST, typename OutT>
+__device__ __forceinline__ void lm_tile(const LmMm& p, uint8_t* smem, i32x2* s_order) {
+  constexpr int NW = WM * WN, BM = 16 * FM * WM, BN = 16 * FN * WN;
+  constexpr int NIA = BM / 8 / NW, NIB = BN / 8 / NW;
+  constexpr int STAGE = (BM + BN) * 128;
+  static_assert(NIA * 8 * NW == BM && NIB * 8 * NW == BN, "tile");
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const int r = lane & 15, g = lane >> 4;
+  const int k = p.k, n = p.n, KT = (k + LM_BK - 1) / LM_BK;
+  // the tile
+  const int nt = (n + BN - 1) / BN, mt = (p.T + BM - 1) / BM;
+  const int total = nt * mt, per = (total + 7) / 8;
+  const int tile = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if (static_cast<int>(blockIdx.x >> 3) >= per || tile >= total) return;
+  constexpr int GM = BM >= 256 ? 4 : 8;
+  const int grp = tile / (GM * nt), in = tile - grp * GM * nt, gsz = min(mt - grp * GM, GM);
+  const int m0 = (grp * GM + in % gsz) * BM, n0 = in / gsz * BN;
+  const int rows = min(p.T - m0, BM), cols = min(n - n0, BN);
+
+  for (int i = tid; i < BM; i += 64 * NW)
+    s_order[i] = i < rows ? gld<i32x2>(p.plan.order + m0 + i) : i32x2{-1, p.L};
+  __syncthreads();
+
+  const __amdgpu_buffer_rsrc_t ar =
+      buf_rsrc(p.x, static_cast<uint32_t>(p.T) * static_cast<uint32_t>(k) * 2u);
+  const __amdgpu_buffer_rsrc_t br =
+      buf_rsrc(p.w, static_cast<uint32_t>(n) * static_cast<uint32_t>(k) * 2u);
+  const int lr = lane >> 3, chunk = (lane & 7) ^ lr ^ (wave & 1);
+  uint32_t va[NIA], vb[NIB];
+#pragma unroll
+  for (int i = 0; i < NIA; ++i) {
+    const int row = s_order[8 * (NW * i + wave) + lr].x;
+    va[i] = row >= 0 ? (static_cast<uint32_t>(row) * k + chunk * 8) * 2 : LM_OUT;
+  }
+  constexpr int CPW = BN / 8;  // 16-byte pieces of a transposed tile's row
+#pragma unroll
+  for (int i = 0; i < NIB; ++i) {
+    if constexpr (!BT) {
+      const int row = 8 * (NW * i + wave) + lr;
+      vb[i] = row < cols ? (static_cast<uint32_t>(n0 + row) * k + chunk * 8) * 2 : LM_OUT;
+    } else {
+      const int at = (NW * i + wave) * 64 + lane, row = at / CPW, c = at % CPW;
+      const int col = (((c >> 1) ^ lm_tswz<BN>(row)) * 2 + (c & 1)) * 8;
+      vb[i] = col < cols ? (static_cast<uint32_t>(row) * n + n0 + col) * 2 : LM_OUT;
+    }
+  }
+  const uint32_t tail = (KT - 1) * LM_BK + chunk * 8 < k ? 0u : LM_OUT;
+  auto dma = [&](int st, int kt) {
+    const int kb = min(kt, KT - 1);
+    const uint32_t drop = kt >= KT ? LM_OUT : 0u, dropa = kt >= KT ? LM_OUT : kt == KT - 1 ? tail : 0u;
+    const uint32_t so = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(kb) * (LM_BK * 2));
+    const uint32_t sob = BT ? __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(kb) * LM_BK * n * 2) : so;
+#pragma unroll
+    for (int i = 0; i < NIA; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, lm_lds(smem + st * STAGE + (NW * i + wave) * 1024),
+                                               16, va[i] | dropa, so, 0, 0);
+#pragma unroll
+    for (int i = 0; i < NIB; ++i) {
+      uint32_t d = BT ? drop : dropa;
+      if (BT && kt == KT - 1) {  // rows past k
+        const int row = ((NW * i + wave) * 64 + lane) / CPW;
+        d = kb * LM_BK + row < k ? 0u : LM_OUT;
+      }
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          br, lm_lds(smem + st * STAGE + BM * 128 + (NW * i + wave) * 1024), 16, vb[i] | d, sob, 0, 0);
+    }
+  };
+
+  f32x4 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  // lane (r, g) of half h holds 8 values from chunk ck[h] on
+  int ck[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) ck[h] = (((g & 1) << 1) | (g >> 1)) + 4 * h;
+  auto frag_a = [&](const uint8_t* st, int i, int h) {
+    return *reinterpret_cast<const u32x4*>(st + ((wm * FM + i) * 16 + r) * 128 + (ck[h] ^ lm_swz(r)) * 16);
+  };
+  auto frag_t = [&](const uint8_t* st, int j, int c8) {  // rows c8 .. c8 + 7 of column block j
+    const int pc = wn * FN + j, row = c8 + (r >> 2);
+    const uint8_t* a = st + row * (BN * 2) + ((pc ^ lm_tswz<BN>(row)) * 32) + (r & 3) * 8;
+    const int row2 = row + 4;
+    const uint8_t* b = st + row2 * (BN * 2) + ((pc ^ lm_tswz<BN>(row2)) * 32) + (r & 3) * 8;
+    return lm_column(a, b);
+  };
+  auto frag_b = [&](const uint8_t* st, int j, int h) {
+    if constexpr (BT)
+      return frag_t(st, j, ck[h] * 8);
+    else
+      return *reinterpret_cast<const u32x4*>(st + ((wn * FN + j) * 16 + r) * 128 + (ck[h] ^ lm_swz(r)) * 16);
+  };
+
+#pragma unroll
+  for (int s = 0; s < NST - 1; ++s) dma(s, s);
+  constexpr int FLY = (NST - 2) * (NIA + NIB);
+  int st = 0;
+  for (int kt = 0; kt < KT; ++kt) {
+    lm_wait_barrier<FLY>();
+    dma((st + NST - 1) % NST, kt + NST - 1);
+    const uint8_t* sa = smem + st * STAGE;
+    const uint8_t* sb = sa + BM * 128;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      u32x4 fb[FN];
+#pragma unroll
+      for (int j = 0; j < FN; ++j) fb[j] = frag_b(sb, j, h);
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        const u32x4 fa = frag_a(sa, i, h);
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = lm_mfma<F16>(fb[j], fa, acc[i][j]);
+      }
+    }
+    st = st + 1 == NST ? 0 : st + 1;
+  }
+  lm_wait_barrier<0>();
+
+  // the adapters, one run of rows after another.  The reduction runs over slots of 16
+  // ranks, all of the first piece, then the second (fp32 outputs: the third), two
+  // slots an MFMA.
+  constexpr int NP = sizeof(OutT) == 4 ? 3 : 2;
+  const int nb = p.RP / 16, ns = NP * nb;
+  int row_at[FM], id_at[FM];
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const i32x2 o = s_order[(wm * FM + i) * 16 + r];
+    row_at[i] = o.x;
+    id_at[i] = o.y;
+  }
+  for (int at = 0; at < rows;) {
+    const int l = __builtin_amdgcn_readfirstlane(s_order[at].y);
+    if (l >= p.L) break;  // the rows without an adapter are last
+    const int end = max(min(gld<int>(p.plan.seg + l + 1) - m0, rows), at + 1);
+    const __amdgpu_buffer_rsrc_t lr_ =
+        buf_rsrc(static_cast<const uint16_t*>(p.bank) + static_cast<int64_t>(l) * p.R * n,
+                 static_cast<uint32_t>(p.R) * static_cast<uint32_t>(n) * 2u);
+    auto add = [&](int s2, const u32x4* fb) {  // slots 2 s2 and 2 s2 + 1
+      u32x4 hi[FN], lo[FN];
+      if constexpr (F16) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j) lm_split(fb[j], hi[j], lo[j]);
+      }
+      const bool live = 2 * s2 + (g >> 1) < ns;
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        const int b0 = (wm * FM + i) * 16;
+        if (b0 + 16 <= at || b0 >= end) continue;
+        u32x4 fv = {0, 0, 0, 0};
+        if (live && id_at[i] == l)
+          fv = gld<u32x4>(p.pieces + static_cast<int64_t>(row_at[i]) * 3 * p.RP + s2 * 32 + g * 8);
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          f32x4 d = lm_mfma<false>(F16 ? hi[j] : fb[j], fv, acc[i][j]);
+          if constexpr (F16) d = lm_mfma<false>(lo[j], fv, d);
+          // a NaN in this adapter's bank is not another row's
+          if (id_at[i] == l) acc[i][j] = d;
+        }
+      }
+    };
+    if constexpr (!BT) {
+      for (int s2 = 0; 2 * s2 < ns; ++s2) {
+        const int rk = (2 * s2 + (g >> 1)) % nb * 16 + (g & 1) * 8;
+        u32x4 fb[FN];
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          const int c = (wn * FN + j) * 16 + r;
+          fb[j] = buf_ld128(lr_, c < cols && rk < p.R ? (static_cast<uint32_t>(n0 + c) * p.R + rk) * 2 : LM_OUT, 0);
+        }
+        add(s2, fb);
+      }
+    } else {
+      // ranks 16 RB at a time through LDS, all pieces of them
+      constexpr int RB = STAGE * NST / (BN * 32) < 4 ? STAGE * NST / (BN * 32) : 4;
+      for (int j0 = 0; j0 < nb; j0 += RB) {
+        const int part = min(nb - j0, RB);
+        __syncthreads();
+        for (int q = tid; q < part * 16 * CPW; q += 64 * NW) {
+          const int row = q / CPW, c = q % CPW;
+          const int col = (((c >> 1) ^ lm_tswz<BN>(row)) * 2 + (c & 1)) * 8, rk = j0 * 16 + row;
+          const u32x4 v = buf_ld128(lr_, col < cols && rk < p.R ? (static_cast<uint32_t>(rk) * n + n0 + col) * 2 : LM_OUT, 0);
+          *reinterpret_cast<u32x4*>(smem + q * 16) = v;
+        }
+        __syncthreads();
+        // slots of these ranks: piece by piece, 16 ranks an MFMA half
+        for (int s = 0; s < NP * part; s += 2) {
+          const int mine = min(s + (g >> 1), NP * part - 1);
+          const int pc = mine / part, jb = mine % part;
+          const bool live = s + (g >> 1) < NP * part;
+          u32x4 fb[FN], hi[FN], lo[FN];
+#pragma unroll
+          for (int j = 0; j < FN; ++j) {
+            fb[j] = frag_t(smem, j, jb * 16 + (g & 1) * 8);
+            if constexpr (F16) lm_split(fb[j], hi[j], lo[j]);
+          }
+#pragma unroll
+          for (int i = 0; i < FM; ++i) {
+            const int b0 = (wm * FM + i) * 16;
+            if (b0 + 16 <= at || b0 >= end) continue;
+            u32x4 fv = {0, 0, 0, 0};
+            if (live && id_at[i] == l)
+              fv = gld<u32x4>(p.pieces + (static_cast<int64_t>(row_at[i]) * 3 + pc) * p.RP + (j0 + jb) * 16 + (g & 1) * 8);
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+              f32x4 d = lm_mfma<false>(F16 ? hi[j] : fb[j], fv, acc[i][j]);
+              if constexpr (F16) d = lm_mfma<false>(lo[j], fv, d);
+              if (id_at[i] == l) acc[i][j] = d;
+            }
+          }
+        }
+      }
+    }
+    at = end;
+  }
+
+  // acc[i][j][q]: row 16 i + r, column 16 j + 4 g + q of the wavefront's
+  constexpr int ES = sizeof(OutT);
+#pragma unroll
+  for (int j = 0; j < FN; ++j) {
+    const int c = (wn * FN + j) * 16 + 4 * g;
+    if (c >= cols) continue;
+    f32x4 bias = {0.f, 0.f, 0.f, 0.f};
+    if (p.bias != nullptr) {
+      const u32x2 raw = gld<u32x2>(static_cast<const uint16_t*>(p.bias) + n0 + c);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint16_t h = static_cast<uint16_t>(raw[q >> 1] >> (16 * (q & 1)));
+        bias[q] = F16 ? static_cast<float>(__builtin_bit_cast(_Float16, h)) : bf16_bits_to_f32(h);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      if (row_at[i] < 0) continue;
+      OutT* const o = static_cast<OutT*>(p.out) + static_cast<int64_t>(row_at[i]) * n + n0 + c;
+      const f32x4 v = acc[i][j] + bias;
+      if constexpr (ES == 4) {
+        gst<f32x4>(o, v);
+      } else {
+        typedef OutT t4 __attribute__((ext_vector_type(4)));
+        gst<u32x2>(o, __builtin_bit_cast(u32x2, __builtin_convertvector(v, t4)));
+      }
+    }
+  }
+}
+
+template <bool F16, bool BT, int WM, int WN, int FM, int FN, int NST, typename OutT>
+__global__ __launch_bounds__(64 * WM * WN)
+    __attribute__((amdgpu_waves_per_eu(2))) void lm_mm_kernel(LmMm p) {
+  constexpr int BM = 16 * FM * WM, BN = 16 * FN * WN;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[NST * (BM + BN) * 128];
+  __shared__ i32x2 s_order[BM];
+  lm_tile<F16, BT, WM, WN, FM, FN, NST, OutT>(p, smem, s_order);
+}
+
+// ---------------------------------------------------------------------------
+// grads: for a chunk of an adapter's rows, 128 columns of x (or go) and 16 NB ranks,
+//   ROWS == false: ga[l, r, c] = sum_t u[t, r] x[t, c]
+//   ROWS == true:  gb[l, c, r] = sum_t v[t, r] go[t, c]
+// from the transposed pieces.  Stages of 64 rows of x; a wavefront has 32 columns.
+// ---------------------------------------------------------------------------
+struct LmGrad {
+  const void* x;             // [T, C]
+  const uint16_t* pieces_t;  // [3 RP, slots]
+  LmPlan plan;
+  float* part;               // [places, R, C] (ROWS: [places, C, R])
+  void* out;                 // [L, R, C] (ROWS: [L, C, R])
+  int C, R, RP, slots;
+};
+
+constexpr int GR_BN = 128, GR_BK = 64, GR_STAGE = GR_BK * GR_BN * 2;
+
+template <bool F16, bool ROWS, int NB, typename OutT>
+__device__ __forceinline__ void lm_grad(const LmGrad& a, uint8_t* smem, i32x4 ch, int c0, int rank0) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int C = a.C, R = a.R;
+  const int s0 = ch.y * LM_ITEM, s1 = s0 + ch.z * LM_ITEM;  // slots
+  const int KT = (s1 - s0 + GR_BK - 1) / GR_BK;
+  constexpr int CPW = GR_BN / 8, NI = GR_STAGE / 1024 / 4;  // 4 rows an instruction, 4 instructions
+  auto dma = [&](int st, int kt) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int at = (4 * i + wave) * 64 + lane, row = at / CPW, c = at % CPW;
+      const int col = c0 + (((c >> 1) ^ lm_tswz<GR_BN>(row)) * 2 + (c & 1)) * 8;
+      const int slot = s0 + kt * GR_BK + row;
+      const int t = slot < s1 ? gld<int>(a.plan.slot_row + slot) : -1;
+      const uint16_t* src = t >= 0 && col < C
+                                ? static_cast<const uint16_t*>(a.x) + static_cast<int64_t>(t) * C + col
+                                : a.plan.zeros;
+      __builtin_amdgcn_global_load_lds((const MI_GLOBAL void*)(src),
+                                       lm_lds(smem + st * GR_STAGE + (4 * i + wave) * 1024), 16, 0, 0);
+    }
+  };
+  f32x4 acc[NB][2];
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) acc[b][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (KT > 0) dma(0, 0);
+  for (int kt = 0; kt < KT; ++kt) {
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+    __syncthreads();
+    if (kt + 1 < KT) dma((kt + 1) & 1, kt + 1);
+    const uint8_t* st = smem + (kt & 1) * GR_STAGE;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      u32x4 fx[2], fl[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int pc = wave * 2 + j, row = 32 * h + 8 * g + (r >> 2), row2 = row + 4;
+        fx[j] = lm_column(st + row * (GR_BN * 2) + (pc ^ lm_tswz<GR_BN>(row)) * 32 + (r & 3) * 8,
+                          st + row2 * (GR_BN * 2) + (pc ^ lm_tswz<GR_BN>(row2)) * 32 + (r & 3) * 8);
+        if constexpr (F16) lm_split(fx[j], fx[j], fl[j]);
+      }
+      const int slot = s0 + kt * GR_BK + 32 * h + 8 * g;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const int rk = rank0 + 16 * b + r;
+#pragma unroll
+        for (int c = 0; c < 3; ++c) {
+          u32x4 fp = {0, 0, 0, 0};
+          if (slot < s1 && rk < a.RP)
+            fp = gld<u32x4>(a.pieces_t + (static_cast<int64_t>(c) * a.RP + rk) * a.slots + slot);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            acc[b][j] = ROWS ? lm_mfma<false>(fp, fx[j], acc[b][j]) : lm_mfma<false>(fx[j], fp, acc[b][j]);
+            if constexpr (F16) {
+              if (c < 2)
+                acc[b][j] = ROWS ? lm_mfma<false>(fp, fl[j], acc[b][j]) : lm_mfma<false>(fl[j], fp, acc[b][j]);
+            }
+          }
+        }
+      }
+    }
+  }
+  // four ranks of column r (ROWS), or four columns of rank r
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int col = c0 + wave * 32 + 16 * j + (ROWS ? r : 4 * g);
+      const int rk = rank0 + 16 * b + (ROWS ? 4 * g : r);
+      if (col >= C || rk >= R) continue;
+      const int64_t in = ROWS ? static_cast<int64_t>(col) * R + rk : static_cast<int64_t>(rk) * C + col;
+      const int64_t size = static_cast<int64_t>(R) * C;
+      if (ch.w >= 0) {
+        gst<f32x4>(a.part + ch.w * size + in, acc[b][j]);
+      } else if constexpr (sizeof(OutT) == 4) {
+        gst<f32x4>(static_cast<float*>(a.out) + ch.x * size + in, acc[b][j]);
+      } else {
+        typedef OutT t4 __attribute__((ext_vector_type(4)));
+        gst<u32x2>(static_cast<OutT*>(a.out) + ch.x * size + in,
+                   __builtin_bit_cast(u32x2, __builtin_convertvector(acc[b][j], t4)));
+      }
+    }
+}
+
+template <bool F16, int NB, typename OutT>
+__global__ __launch_bounds__(256) void lm_grad_kernel(LmGrad ga, LmGrad gb) {
+  __shared__ __attribute__((aligned(16))) uint8_t smem[2 * GR_STAGE];
+  const int chunk = blockIdx.y;
+  if (chunk >= gld<int>(ga.plan.totals + 1)) return;
+  const i32x4 ch = gld<i32x4>(ga.plan.chunks + chunk);
+  const int pa = (ga.C + GR_BN - 1) / GR_BN;
+  const int rank0 = blockIdx.z * 16 * NB;
+  if (static_cast<int>(blockIdx.x) < pa)
+    lm_grad<F16, false, NB, OutT>(ga, smem, ch, blockIdx.x * GR_BN, rank0);
+  else
+    lm_grad<F16, true, NB, OutT>(gb, smem, ch, (blockIdx.x - pa) * GR_BN, rank0);
+}
+
+template <typename OutT>
+__global__ __launch_bounds__(256) void lm_reduce_kernel(LmGrad ga, LmGrad gb) {
+  const i32x4 span = gld<i32x4>(ga.plan.spans + blockIdx.y);
+  if (span.z < 0) return;
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    const LmGrad& a = which ? gb : ga;
+    const int64_t size = static_cast<int64_t>(a.R) * a.C;
+    for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4; i < size;
+         i += static_cast<int64_t>(gridDim.x) * 1024) {
+      f32x4 v = gld<f32x4>(a.part + span.z * size + i);
+      for (int c = 1; c < span.y; ++c) v += gld<f32x4>(a.part + (span.z + c) * size + i);
+      if constexpr (sizeof(OutT) == 4) {
+        gst<f32x4>(static_cast<float*>(a.out) + blockIdx.y * size + i, v);
+      } else {
+        typedef OutT t4 __attribute__((ext_vector_type(4)));
+        gst<u32x2>(static_cast<OutT*>(a.out) + blockIdx.y * size + i,
+                   __builtin_bit_cast(u32x2, __builtin_convertvector(v, t4)));
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+struct LmSizes {
+  int64_t T, N, K, L, R;
+  int64_t rp() const { return (R + 15) / 16 * 16; }
+  // rows of one pass: a row's place in x or go is a 31-bit byte offset
+  int64_t pass() const {
+    const int64_t wide = N > K ? N : K, fit = ((1LL << 31) - 1) / (2 * wide) & ~255LL;
+    const int64_t most = fit < (1LL << 22) ? fit : 1LL << 22;
+    return T < most ? T : most;
+  }
+  static int64_t items(int64_t t, int64_t l) { return t / LM_ITEM + (l < t ? l : t) + 1; }
+  // items of a chunk: 512 rows, and no more than 32 chunks of a call's rows
+  int64_t chunk_items() const {
+    const int64_t i = (T + 16 * 32 - 1) / (16 * 32);
+    return i < 32 ? 32 : i;
+  }
+  int64_t chunks() const { return L + items(T, L) / chunk_items() + 1; }
+  // those of adapters that have several: each but an adapter's last is full
+  int64_t places() const { return 2 * (items(T, L) / chunk_items()) + 2; }
+};
+
+struct LmCarve {
+  uint8_t* at;
+  size_t used = 0;
+  template <typename T>
+  T* take(int64_t n) {
+    T* const p = reinterpret_cast<T*>(at + used);
+    used += (static_cast<size_t>(n) * sizeof(T) + 255) & ~static_cast<size_t>(255);
+    return at == nullptr ? nullptr : p;
+  }
+};
+
+struct LmSpace {
+  LmPlan plan;
+  uint16_t *pieces, *ut, *vt;
+  float *act, *part_a, *part_b;
+  size_t bytes;
+};
+
+LmSpace lm_space(const LmSizes& s, bool backward, void* base) {
+  LmCarve c{static_cast<uint8_t*>(base)};
+  LmSpace o{};
+  const int64_t items = LmSizes::items(s.T, s.L), wide = s.N > s.K ? s.N : s.K;
+  o.plan.order = c.take<i32x2>(s.T);
+  o.plan.seg = c.take<int>(s.L + 1);
+  o.plan.items = c.take<i32x4>(items);
+  o.plan.slot_row = c.take<int>(items * LM_ITEM);
+  o.plan.chunks = c.take<i32x4>(s.chunks());
+  o.plan.spans = c.take<i32x4>(s.L);
+  o.plan.totals = c.take<int>(2);
+  o.plan.zeros = c.take<uint16_t>(8);
+  (void)wide;
+  o.pieces = c.take<uint16_t>(s.T * 3 * s.rp());
+  if (backward) {
+    o.ut = c.take<uint16_t>(items * LM_ITEM * 3 * s.rp());
+    o.vt = c.take<uint16_t>(items * LM_ITEM * 3 * s.rp());
+    o.act = c.take<float>(s.T * s.R);
+    o.part_a = c.take<float>(s.places() * s.R * s.K);
+    o.part_b = c.take<float>(s.places() * s.R * s.N);
+  }
+  o.bytes = c.used;
+  return o;
+}
+
+mi_status lm_check(const char* what, const LmSizes& s, mi_dtype dt) {
+  MI_REQUIRE(dt == MI_BF16 || dt == MI_F16, "%s: x, w and the banks must be bf16 or fp16", what);
+  MI_REQUIRE(s.T >= 0 && s.T < (1LL << 31) - 256, "%s: rows out of range (%lld)", what, (long long)s.T);
+  MI_REQUIRE(s.N >= 8 && s.N % 8 == 0, "%s: n %% 8 == 0 required (got n=%lld)", what, (long long)s.N);
+  MI_REQUIRE(s.K >= 8 && s.K % 8 == 0, "%s: k %% 8 == 0 required (got k=%lld)", what, (long long)s.K);
+  MI_REQUIRE(s.R >= 8 && s.R % 8 == 0 && s.R <= LM_MAX_RANK,
+             "%s: rank must be a multiple of 8 in [8, %d] (got %lld)", what, LM_MAX_RANK, (long long)s.R);
+  MI_REQUIRE(s.L >= 1 && s.L <= LM_MAX_ADAPTERS, "%s: num_adapters must be in [1, %d] (got %lld)", what,
+             LM_MAX_ADAPTERS, (long long)s.L);
+  MI_REQUIRE_SUPPORTED(s.N < (1LL << 20) && s.K < (1LL << 20) && s.N * s.K < (1LL << 30),
+                       "%s: n and k below 2^20 and n * k below 2^30 required (w must fit one "
+                       "31-bit buffer range; got n=%lld, k=%lld)", what, (long long)s.N, (long long)s.K);
+  return MI_OK;
+}
+
+mi_status lm_plan(const LmSizes& s, int64_t rows, const int32_t* ids, const LmPlan& p, hipStream_t st) {
+  hipLaunchKernelGGL(lm_plan_kernel, dim3(1), dim3(PL_T),
+                     0, st, ids, static_cast<int>(rows),
+                     static_cast<int>(s.L), static_cast<int>(s.chunk_items()), 1, p);
+  return launch_status("mm_lora (plan)");
+}
+
+template <bool F16, bool BT>
+mi_status lm_shrink(const LmShrink& a, int64_t items, hipStream_t st) {
+  const int nb = a.RP / 16;
+#define LM_SHRINK(NB_)                                                                              \
+  hipLaunchKernelGGL((lm_shrink_kernel<F16, BT, NB_>),                                              \
+                     dim3(static_cast<unsigned>(items), static_cast<unsigned>((nb + NB_ - 1) / NB_)), \
+                     dim3(64 * SH_W), 0, st, a)
+  if (nb == 1) LM_SHRINK(1);
+  else if (nb == 2) LM_SHRINK(2);
+  else LM_SHRINK(4);
+#undef LM_SHRINK
+  return launch_status("mm_lora (shrink)");
+}
+
+template <bool F16, bool BT, int WM, int WN, int FM, int FN, int NST, typename OutT>
+mi_status lm_mm_launch(const LmMm& a, hipStream_t st) {
+  constexpr int BM = 16 * FM * WM, BN = 16 * FN * WN;
+  const int64_t tiles = static_cast<int64_t>((a.T + BM - 1) / BM) * ((a.n + BN - 1) / BN);
+  hipLaunchKernelGGL((lm_mm_kernel<F16, BT, WM, WN, FM, FN, NST, OutT>),
+                     dim3(static_cast<unsigned>((tiles + 7) / 8 * 8)), dim3(64 * WM * WN), 0, st, a);
+  return launch_status("mm_lora (product)");
+}
+
+template <bool F16, bool BT, typename OutT>
+mi_status lm_mm(const LmMm& a, hipStream_t st) {
+  return lm_mm_launch<F16, BT, 2, 2, 4, 4, 2, OutT>(a, st);
+}
+
+}  // namespace
+}  // namespace mi
+
+extern "C" size_t mi_mm_lora_workspace_size(int64_t m, int64_t n, int64_t k, int64_t num_adapters,
+                                            int64_t rank, int backward) {
+  const mi::LmSizes s{m, n, k, num_adapters, rank};
+  if (mi::lm_check("mm_lora_workspace_size", s, MI_BF16) != MI_OK) return 0;
+  return mi::lm_space(s, backward != 0, nullptr).bytes;
+}
+
+extern "C" mi_status mi_mm_lora(const void* x, int64_t m, int64_t k, mi_dtype dtype, const void* w,
+                                int64_t n, const void* lora_a, const void* lora_b,
+                                int64_t num_adapters, int64_t rank, const int32_t* lora_ids,
+                                const float* lora_scale, const void* bias, void* out,
+                                mi_dtype out_dtype, float* act, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  using namespace mi;
+  clear_error();
+  const char* what = "mm_lora";
+  const LmSizes s{m, n, k, num_adapters, rank};
+  mi_status st = lm_check(what, s, dtype);
+  if (st != MI_OK) return st;
+  MI_REQUIRE(out_dtype == MI_BF16 || out_dtype == MI_F16 || out_dtype == MI_F32,
+             "%s: out_dtype must be bf16, fp16 or fp32", what);
+  MI_REQUIRE_SUPPORTED(out_dtype == MI_F32 || out_dtype == dtype,
+                       "%s: out_dtype must be x's type or fp32", what);
+  if (m == 0) return MI_OK;
+  MI_REQUIRE(x != nullptr && w != nullptr && lora_a != nullptr && lora_b != nullptr &&
+                 lora_ids != nullptr && out != nullptr,
+             "%s: x, w, lora_a, lora_b, lora_ids or out is null", what);
+  MI_REQUIRE(aligned16(x) && aligned16(w) && aligned16(lora_a) && aligned16(lora_b) &&
+                 aligned16(bias) && aligned16(out) && aligned16(act),
+             "%s: x, w, lora_a, lora_b, bias, out and act must be 16-byte aligned", what);
+  const int64_t ob = m * n * (out_dtype == MI_F32 ? 4 : 2), ab = m * rank * 4;
+  const int64_t bank = num_adapters * rank * 2;
+  auto clear_of = [&](const void* o, int64_t bytes) {
+    return !overlap(o, bytes, x, m * k * 2) && !overlap(o, bytes, w, n * k * 2) &&
+           !overlap(o, bytes, lora_a, bank * k) && !overlap(o, bytes, lora_b, bank * n) &&
+           !overlap(o, bytes, lora_ids, m * 4) && !overlap(o, bytes, lora_scale, num_adapters * 4) &&
+           !overlap(o, bytes, bias, n * 2) && !overlap(o, bytes, workspace, workspace_bytes);
+  };
+  MI_REQUIRE(clear_of(out, ob) && clear_of(act, ab) && !overlap(out, ob, act, ab),
+             "%s: out and act may not overlap an input, the workspace or each other", what);
+  const LmSpace sp = lm_space(s, false, workspace);
+  MI_REQUIRE(workspace != nullptr && (reinterpret_cast<uintptr_t>(workspace) & 255) == 0 &&
+                 workspace_bytes >= sp.bytes,
+             "%s: the workspace needs %zu bytes, aligned to 256 (got %zu)", what, sp.bytes, workspace_bytes);
+  hipStream_t hs = static_cast<hipStream_t>(stream);
+  const int64_t es = out_dtype == MI_F32 ? 4 : 2;
+  if (act != nullptr) {
+    const int64_t quads = m * (rank / 4), blocks = (quads + 255) / 256;
+    hipLaunchKernelGGL(lm_zero_act_kernel, dim3(static_cast<unsigned>(blocks < 2048 ? blocks : 2048)),
+                       dim3(256), 0, hs, lora_ids, static_cast<int>(m), static_cast<int>(num_adapters),
+                       static_cast<int>(rank / 4), act);
+    st = launch_status("mm_lora (activations)");
+    if (st != MI_OK) return st;
+  }
+  for (int64_t t0 = 0; t0 < m; t0 += s.pass()) {
+    const int64_t rows = m - t0 < s.pass() ? m - t0 : s.pass();
+    st = lm_plan(s, rows, lora_ids + t0, sp.plan, hs);
+    if (st != MI_OK) return st;
+    LmShrink a{};
+    a.x = static_cast<const uint16_t*>(x) + t0 * k;
+    a.bank = lora_a;
+    a.scale = lora_scale;
+    a.plan = sp.plan;
+    a.out = act == nullptr ? nullptr : act + t0 * rank;
+    a.pieces = sp.pieces;
+    a.T = static_cast<int>(rows);
+    a.C = static_cast<int>(k);
+    a.L = static_cast<int>(num_adapters);
+    a.R = static_cast<int>(rank);
+    a.RP = static_cast<int>(s.rp());
+    const int64_t items = LmSizes::items(rows, num_adapters);
+    st = dtype == MI_F16 ? lm_shrink<true, false>(a, items, hs) : lm_shrink<false, false>(a, items, hs);
+    if (st != MI_OK) return st;
+    LmMm p{};
+    p.x = a.x;
+    p.w = w;
+    p.bank = lora_b;
+    p.bias = bias;
+    p.pieces = sp.pieces;
+    p.plan = sp.plan;
+    p.out = static_cast<uint8_t*>(out) + t0 * n * es;
+    p.T = a.T;
+    p.k = static_cast<int>(k);
+    p.n = static_cast<int>(n);
+    p.L = a.L;
+    p.R = a.R;
+    p.RP = a.RP;
+    st = dtype == MI_F16
+             ? (es == 4 ? lm_mm<true, false, float>(p, hs) : lm_mm<true, false, _Float16>(p, hs))
+             : (es == 4 ? lm_mm<false, false, float>(p, hs) : lm_mm<false, false, __bf16>(p, hs));
+    if (st != MI_OK) return st;
+  }
+  return MI_OK;
+}
+
+extern "C" mi_status mi_mm_lora_backward(const void* grad_out, const void* x, int64_t m, int64_t k,
+                                         mi_dtype dtype, const void* w, int64_t n,
+                                         const void* lora_a, const void* lora_b,
+                                         int64_t num_adapters, int64_t rank,
+                                         const int32_t* lora_ids, const float* lora_scale,
+                                         const float* act, void* grad_x, void* grad_a,
+                                         void* grad_b, mi_dtype grad_dtype, void* workspace,
+                                         size_t workspace_bytes, void* stream) {
+  using namespace mi;
+  clear_error();
+  const char* what = "mm_lora_backward";
+  const LmSizes s{m, n, k, num_adapters, rank};
+  mi_status st = lm_check(what, s, dtype);
+  if (st != MI_OK) return st;
+  MI_REQUIRE(grad_dtype == MI_F32 || grad_dtype == dtype,
+             "%s: grad_a and grad_b must be fp32 or of x's type", what);
+  const bool banks = grad_a != nullptr || grad_b != nullptr;
+  MI_REQUIRE((grad_a == nullptr) == (grad_b == nullptr), "%s: grad_a and grad_b are given together", what);
+  MI_REQUIRE(banks || grad_x != nullptr, "%s: no gradient is asked for", what);
+  MI_REQUIRE(lora_a != nullptr && lora_b != nullptr, "%s: lora_a or lora_b is null", what);
+  MI_REQUIRE(m == 0 || (grad_out != nullptr && lora_ids != nullptr &&
+                        (grad_x == nullptr || w != nullptr) && (!banks || x != nullptr)),
+             "%s: grad_out, x, w or lora_ids is null", what);
+  MI_REQUIRE(aligned16(grad_out) && aligned16(x) && aligned16(w) && aligned16(lora_a) &&
+                 aligned16(lora_b) && aligned16(act) && aligned16(grad_x) && aligned16(grad_a) &&
+                 aligned16(grad_b),
+             "%s: the tensors must be 16-byte aligned", what);
+  if (m == 0 && !banks) return MI_OK;
+  const int64_t bank = num_adapters * rank, ges = grad_dtype == MI_F32 ? 4 : 2;
+  const struct { const void* p; int64_t n; } outs[3] = {
+      {grad_x, m * k * 2}, {grad_a, bank * k * ges}, {grad_b, bank * n * ges}},
+      ins[9] = {{grad_out, m * n * 2}, {x, m * k * 2}, {w, n * k * 2}, {lora_a, bank * k * 2},
+                {lora_b, bank * n * 2}, {lora_ids, m * 4}, {lora_scale, num_adapters * 4},
+                {act, m * rank * 4}, {workspace, static_cast<int64_t>(workspace_bytes)}};
+  for (int i = 0; i < 3; ++i) {
+    for (const auto& in : ins)
+      MI_REQUIRE(!overlap(outs[i].p, outs[i].n, in.p, in.n),
+                 "%s: a gradient may not overlap an input or the workspace", what);
+    for (int j = 0; j < i; ++j)
+      MI_REQUIRE(!overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n),
+                 "%s: the gradients may not overlap each other", what);
+  }
+  const LmSpace sp = lm_space(s, true, workspace);
+  MI_REQUIRE(workspace != nullptr && (reinterpret_cast<uintptr_t>(workspace) & 255) == 0 &&
+                 workspace_bytes >= sp.bytes,
+             "%s: the workspace needs %zu bytes, aligned to 256 (got %zu)", what, sp.bytes, workspace_bytes);
+  hipStream_t hs = static_cast<hipStream_t>(stream);
+  const bool f16 = dtype == MI_F16, several = s.pass() < m;
+  auto shrink = [&](int64_t t0, int64_t rows) {
+    LmShrink a{};
+    a.scale = lora_scale;
+    a.plan = sp.plan;
+    a.T = static_cast<int>(rows);
+    a.L = static_cast<int>(num_adapters);
+    a.R = static_cast<int>(rank);
+    a.RP = static_cast<int>(s.rp());
+    (void)t0;
+    return a;
+  };
+  MI_REQUIRE_SUPPORTED(!several || !banks,
+                       "%s: the adapters' gradients take at most %lld rows of these sizes", what,
+                       (long long)s.pass());
+  if (banks && m == 0) {
+    st = lm_plan(s, 0, lora_ids, sp.plan, hs);
+    if (st != MI_OK) return st;
+  }
+  for (int64_t t0 = 0; t0 < m; t0 += s.pass()) {
+    const int64_t rows = m - t0 < s.pass() ? m - t0 : s.pass();
+    st = lm_plan(s, rows, lora_ids + t0, sp.plan, hs);
+    if (st != MI_OK) return st;
+    const int64_t items = LmSizes::items(rows, num_adapters);
+    const float* v = act;
+    if (banks && act == nullptr) {
+      LmShrink a = shrink(t0, rows);
+      a.x = x;
+      a.bank = lora_a;
+      a.C = static_cast<int>(k);
+      a.out = sp.act;
+      st = f16 ? lm_shrink<true, false>(a, items, hs) : lm_shrink<false, false>(a, items, hs);
+      if (st != MI_OK) return st;
+      v = sp.act;
+    }
+    LmShrink a = shrink(t0, rows);
+    a.x = static_cast<const uint16_t*>(grad_out) + t0 * n;
+    a.bank = lora_b;
+    a.C = static_cast<int>(n);
+    a.pieces = grad_x == nullptr ? nullptr : sp.pieces;
+    a.slots = static_cast<int>(LmSizes::items(m, num_adapters) * LM_ITEM);
+    if (banks) {
+      a.act = v;
+      a.pieces_t = sp.ut;
+      a.pieces_t2 = sp.vt;
+    }
+    st = f16 ? lm_shrink<true, true>(a, items, hs) : lm_shrink<false, true>(a, items, hs);
+    if (st != MI_OK) return st;
+    if (grad_x != nullptr) {
+      LmMm p{};
+      p.x = a.x;
+      p.w = w;
+      p.bank = lora_a;
+      p.pieces = sp.pieces;
+      p.plan = sp.plan;
+      p.out = static_cast<uint16_t*>(grad_x) + t0 * k;
+      p.T = a.T;
+      p.k = static_cast<int>(n);
+      p.n = static_cast<int>(k);
+      p.L = a.L;
+      p.R = a.R;
+      p.RP = a.RP;
+      st = f16 ? lm_mm<true, true, _Float16>(p, hs) : lm_mm<false, true, __bf16>(p, hs);
+      if (st != MI_OK) return st;
+    }
+  }
+  if (!banks) return MI_OK;
+  LmGrad ga{};
+  ga.x = x;
+  ga.pieces_t = sp.ut;
+  ga.plan = sp.plan;
+  ga.part = sp.part_a;
+  ga.out = grad_a;
+  ga.C = static_cast<int>(k);
+  ga.R = static_cast<int>(rank);
+  ga.RP = static_cast<int>(s.rp());
+  ga.slots = static_cast<int>(LmSizes::items(m, num_adapters) * LM_ITEM);
+  LmGrad gb = ga;
+  gb.x = grad_out;
+  gb.pieces_t = sp.vt;
+  gb.part = sp.part_b;
+  gb.out = grad_b;
+  gb.C = static_cast<int>(n);
+  const unsigned panels = static_cast<unsigned>((k + GR_BN - 1) / GR_BN + (n + GR_BN - 1) / GR_BN);
+  const int nb = ga.RP / 16, per = nb == 1 ? 1 : nb == 2 ? 2 : 4;
+  const dim3 grid(panels, static_cast<unsigned>(s.chunks()), static_cast<unsigned>((nb + per - 1) / per));
+  auto launch = [&](auto f, auto o) {
+    constexpr bool F16 = decltype(f)::value;
+    using OutT = decltype(o);
+    if (per == 1) hipLaunchKernelGGL((lm_grad_kernel<F16, 1, OutT>), grid, dim3(256), 0, hs, ga, gb);
+    else if (per == 2) hipLaunchKernelGGL((lm_grad_kernel<F16, 2, OutT>), grid, dim3(256), 0, hs, ga, gb);
+    else hipLaunchKernelGGL((lm_grad_kernel<F16, 4, OutT>), grid, dim3(256), 0, hs, ga, gb);
+    const mi_status one = launch_status("mm_lora_backward (adapters)");
+    if (one != MI_OK || LmSizes::items(m, num_adapters) <= s.chunk_items()) return one;
+    hipLaunchKernelGGL((lm_reduce_kernel<OutT>), dim3(64, static_cast<unsigned>(num_adapters)), dim3(256), 0,
+                       hs, ga, gb);
+    return launch_status("mm_lora_backward (sums)");
+  };
+  if (f16) return ges == 4 ? launch(std::true_type{}, float{}) : launch(std::true_type{}, _Float16{});
+  return ges == 4 ? launch(std::false_type{}, float{}) : launch(std::false_type{}, __bf16{});
+}
