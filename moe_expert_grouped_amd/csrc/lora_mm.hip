@@ -413,26 +413,49 @@ __device__ __forceinline__ void lm_wait_barrier() {
   asm volatile("" ::: "memory");
 }
 
+// Where a tile lies in the call: m-tiles in groups of GM sweep the n-panels together,
+// and each XCD has a contiguous run of that order (workgroup ids go to the 8 in turn).
+struct LmPlace { int m0, n0, rows, cols; };
+template <int BM, int BN>
+__device__ __forceinline__ LmPlace lm_place(const LmMm& p) {
+  const int nt = (p.n + BN - 1) / BN, mt = (p.T + BM - 1) / BM;
+  const int total = nt * mt, per = (total + 7) / 8;
+  const int slot = blockIdx.x >> 3, tile = (blockIdx.x & 7) * per + slot;
+  if (slot >= per || tile >= total) return {0, 0, 0, 0};
+  constexpr int GM = BM >= 256 ? 4 : 8;
+  const int grp = tile / (GM * nt), in = tile - grp * GM * nt, gsz = min(mt - grp * GM, GM);
+  const int m0 = (grp * GM + in % gsz) * BM, n0 = in / gsz * BN;
+  return {m0, n0, min(p.T - m0, BM), min(p.n - n0, BN)};
+}
+
+// One tile of BM = 16 FM WM rows and BN = 16 FN WN columns; WM * WN wavefronts of
+// 16 FM x 16 FN.  w is the MFMA's first operand, so a lane's results are four
+// consecutive columns of one row.
+//
+// Staging: 1 KB a DMA instruction straight into LDS, NST stages, each an array of its
+// own (the compiler then knows which loads a read waits for).  Rows past the call or
+// past n and 16-byte chunks past k load as zeros.
+//
+// A step (64 of k) is FM regions of one 16-row block of x each.  A region reads the
+// fragment of the region after the next and issues its 2 FN MFMAs.  The step's one
+// barrier stands before its last two regions, whose operands are in registers by then:
+// behind it the stage is free for the loads of step kt + NST and the next stage is
+// complete, so the last regions read the next step's first fragments.
 template <bool F16, bool BT, int WM, int WN, int FM, int FN, int NST, typename OutT>
-__device__ __forceinline__ void lm_tile(const LmMm& p, uint8_t* smem, i32x2* s_order) {
+__device__ __forceinline__ void lm_tile(const LmMm& p, const LmPlace& t, uint8_t* s0, uint8_t* s1,
+                                        uint8_t* s2, uint8_t* s3, i32x2* s_order) {
   constexpr int NW = WM * WN, BM = 16 * FM * WM, BN = 16 * FN * WN;
-  constexpr int NIA = BM / 8 / NW, NIB = BN / 8 / NW;
+  constexpr int NIA = BM / 8 / NW, NIB = BN / 8 / NW, NI = NIA + NIB;
   constexpr int STAGE = (BM + BN) * 128;
-  static_assert(NIA * 8 * NW == BM && NIB * 8 * NW == BN, "tile");
+  constexpr int FLY = (NST - 2) * NI;
+  static_assert(NIA * 8 * NW == BM && NIB * 8 * NW == BN && NW % 2 == 0, "tile");
+  static_assert(NST >= 2 && NST <= 4 && FLY < 64 && FM >= 2, "stages");
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
   const int r = lane & 15, g = lane >> 4;
   const int k = p.k, n = p.n, KT = (k + LM_BK - 1) / LM_BK;
-  // the tile
-  const int nt = (n + BN - 1) / BN, mt = (p.T + BM - 1) / BM;
-  const int total = nt * mt, per = (total + 7) / 8;
-  const int tile = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-  if (static_cast<int>(blockIdx.x >> 3) >= per || tile >= total) return;
-  constexpr int GM = BM >= 256 ? 4 : 8;
-  const int grp = tile / (GM * nt), in = tile - grp * GM * nt, gsz = min(mt - grp * GM, GM);
-  const int m0 = (grp * GM + in % gsz) * BM, n0 = in / gsz * BN;
-  const int rows = min(p.T - m0, BM), cols = min(n - n0, BN);
+  const int m0 = t.m0, n0 = t.n0, rows = t.rows, cols = t.cols;
 
   for (int i = tid; i < BM; i += 64 * NW)
     s_order[i] = i < rows ? gld<i32x2>(p.plan.order + m0 + i) : i32x2{-1, p.L};
@@ -450,36 +473,39 @@ __device__ __forceinline__ void lm_tile(const LmMm& p, uint8_t* smem, i32x2* s_o
     va[i] = row >= 0 ? (static_cast<uint32_t>(row) * k + chunk * 8) * 2 : LM_OUT;
   }
   constexpr int CPW = BN / 8;  // 16-byte pieces of a transposed tile's row
+  auto brow = [&](int i) { return ((NW * i + wave) * 64 + lane) / CPW; };
 #pragma unroll
   for (int i = 0; i < NIB; ++i) {
     if constexpr (!BT) {
       const int row = 8 * (NW * i + wave) + lr;
       vb[i] = row < cols ? (static_cast<uint32_t>(n0 + row) * k + chunk * 8) * 2 : LM_OUT;
     } else {
-      const int at = (NW * i + wave) * 64 + lane, row = at / CPW, c = at % CPW;
+      const int row = brow(i), c = lane % CPW;
       const int col = (((c >> 1) ^ lm_tswz<BN>(row)) * 2 + (c & 1)) * 8;
       vb[i] = col < cols ? (static_cast<uint32_t>(row) * n + n0 + col) * 2 : LM_OUT;
     }
   }
   const uint32_t tail = (KT - 1) * LM_BK + chunk * 8 < k ? 0u : LM_OUT;
-  auto dma = [&](int st, int kt) {
+  // Pieces [first, first + count) of the NI loads of a stage.  A step past the last
+  // loads zeros: the steps stay free of branches.
+  auto dma = [&](uint8_t* st, int kt, int first, int count) {
     const int kb = min(kt, KT - 1);
-    const uint32_t drop = kt >= KT ? LM_OUT : 0u, dropa = kt >= KT ? LM_OUT : kt == KT - 1 ? tail : 0u;
+    const uint32_t drop = kt >= KT ? LM_OUT : 0u, dropa = kt == KT - 1 ? tail : drop;
     const uint32_t so = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(kb) * (LM_BK * 2));
-    const uint32_t sob = BT ? __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(kb) * LM_BK * n * 2) : so;
+    const uint32_t sob =
+        BT ? __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(kb) * (LM_BK * 2) * n) : so;
 #pragma unroll
-    for (int i = 0; i < NIA; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, lm_lds(smem + st * STAGE + (NW * i + wave) * 1024),
-                                               16, va[i] | dropa, so, 0, 0);
-#pragma unroll
-    for (int i = 0; i < NIB; ++i) {
-      uint32_t d = BT ? drop : dropa;
-      if (BT && kt == KT - 1) {  // rows past k
-        const int row = ((NW * i + wave) * 64 + lane) / CPW;
-        d = kb * LM_BK + row < k ? 0u : LM_OUT;
+    for (int i = 0; i < NI; ++i) {
+      if (i < first || i >= first + count) continue;
+      if (i < NIA) {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, lm_lds(st + (NW * i + wave) * 1024), 16,
+                                                 va[i < NIA ? i : 0] | dropa, so, 0, 0);
+      } else {
+        const int b = i < NIA ? 0 : i - NIA;
+        const uint32_t d = !BT ? dropa : kb * LM_BK + brow(b) < k ? drop : LM_OUT;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            br, lm_lds(st + BM * 128 + (NW * b + wave) * 1024), 16, vb[b] | d, sob, 0, 0);
       }
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          br, lm_lds(smem + st * STAGE + BM * 128 + (NW * i + wave) * 1024), 16, vb[i] | d, sob, 0, 0);
     }
   };
 
@@ -489,57 +515,93 @@ __device__ __forceinline__ void lm_tile(const LmMm& p, uint8_t* smem, i32x2* s_o
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  // lane (r, g) of half h holds 8 values from chunk ck[h] on
-  int ck[2];
+  // Half h of a step's fragment: lane (r, g) holds the 8 values of chunk ck + 4 h, ck =
+  // 0, 2, 1, 3 for g = 0 .. 3.  The LDS serves lanes l and l + 32 together, and their
+  // chunks have to differ in the lowest bit.
+  const int ck = ((g & 1) << 1) | (g >> 1);
+  struct Frag { u32x4 h[2]; };
+  int fo[2];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) ck[h] = (((g & 1) << 1) | (g >> 1)) + 4 * h;
-  auto frag_a = [&](const uint8_t* st, int i, int h) {
-    return *reinterpret_cast<const u32x4*>(st + ((wm * FM + i) * 16 + r) * 128 + (ck[h] ^ lm_swz(r)) * 16);
+  for (int h = 0; h < 2; ++h) fo[h] = r * 128 + ((ck + 4 * h) ^ lm_swz(r)) * 16;
+  auto frag = [&](const uint8_t* st, int blk) {
+    return Frag{{*reinterpret_cast<const u32x4*>(st + blk * 2048 + fo[0]),
+                 *reinterpret_cast<const u32x4*>(st + blk * 2048 + fo[1])}};
   };
-  auto frag_t = [&](const uint8_t* st, int j, int c8) {  // rows c8 .. c8 + 7 of column block j
-    const int pc = wn * FN + j, row = c8 + (r >> 2);
-    const uint8_t* a = st + row * (BN * 2) + ((pc ^ lm_tswz<BN>(row)) * 32) + (r & 3) * 8;
+  // a transposed tile's rows c8 .. c8 + 7 (c8 % 8 == 0) of column block blk
+  auto column = [&](const uint8_t* st, int blk, int c8) {
+    const int row = c8 + (r >> 2);
+    const uint8_t* a = st + row * (BN * 2) + (blk ^ lm_tswz<BN>(row)) * 32 + (r & 3) * 8;
+    if constexpr (BN >= 128) return lm_column(a, a + 4 * BN * 2);  // row + 4: the same place
     const int row2 = row + 4;
-    const uint8_t* b = st + row2 * (BN * 2) + ((pc ^ lm_tswz<BN>(row2)) * 32) + (r & 3) * 8;
-    return lm_column(a, b);
+    return lm_column(a, st + row2 * (BN * 2) + (blk ^ lm_tswz<BN>(row2)) * 32 + (r & 3) * 8);
   };
-  auto frag_b = [&](const uint8_t* st, int j, int h) {
-    if constexpr (BT)
-      return frag_t(st, j, ck[h] * 8);
-    else
-      return *reinterpret_cast<const u32x4*>(st + ((wn * FN + j) * 16 + r) * 128 + (ck[h] ^ lm_swz(r)) * 16);
-  };
-
-#pragma unroll
-  for (int s = 0; s < NST - 1; ++s) dma(s, s);
-  constexpr int FLY = (NST - 2) * (NIA + NIB);
-  int st = 0;
-  for (int kt = 0; kt < KT; ++kt) {
-    lm_wait_barrier<FLY>();
-    dma((st + NST - 1) % NST, kt + NST - 1);
-    const uint8_t* sa = smem + st * STAGE;
-    const uint8_t* sb = sa + BM * 128;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      u32x4 fb[FN];
-#pragma unroll
-      for (int j = 0; j < FN; ++j) fb[j] = frag_b(sb, j, h);
-#pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        const u32x4 fa = frag_a(sa, i, h);
-#pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = lm_mfma<F16>(fb[j], fa, acc[i][j]);
-      }
+  auto frag_a = [&](const uint8_t* st, int i) { return frag(st, wm * FM + i); };
+  auto frag_b = [&](const uint8_t* st, int j) {
+    if constexpr (BT) {
+      const uint8_t* b = st + BM * 128;
+      return Frag{{column(b, wn * FN + j, ck * 8), column(b, wn * FN + j, ck * 8 + 32)}};
+    } else {
+      return frag(st + BM * 128, wn * FN + j);
     }
-    st = st + 1 == NST ? 0 : st + 1;
+  };
+  // A stage's loads go out PPR per region from the one behind the barrier on, over half
+  // of the regions.
+  constexpr int PPR = (2 * NI + FM - 1) / FM, R0 = FM - 2;
+  Frag fb[FN], fa0, fa1;
+  auto step = [&](uint8_t* pv, uint8_t* st, uint8_t* nx, int kt) {
+    Frag fbx[FN];
+#pragma unroll
+    for (int j = 0; j < FN; ++j) fbx[j] = fb[j];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      if (i == R0) lm_wait_barrier<FLY>();
+      if (i >= R0) dma(st, kt + NST, (i - R0) * PPR, PPR);
+      else if ((i + 2) * PPR < NI) dma(pv, kt + NST - 1, (i + 2) * PPR, PPR);
+      const Frag fax = fa0;
+      fa0 = fa1;
+      fa1 = i < R0 ? frag_a(st, i + 2) : frag_a(nx, i - R0);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          acc[i][j] = lm_mfma<F16>(fbx[j].h[h], fax.h[h], acc[i][j]);
+          if (i == FM - 1 && h == 0) fb[j] = frag_b(nx, j);
+        }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  uint8_t* const sts[4] = {s0, s1, s2, s3};
+  dma(s0, 0, 0, NI);
+  if constexpr (NST >= 3) dma(s1, 1, 0, NI);
+  if constexpr (NST == 4) dma(s2, 2, 0, NI);
+  lm_wait_barrier<FLY>();
+  dma(sts[NST - 1], NST - 1, 0, 2 * PPR);  // the rest in step 0
+  fa0 = frag_a(s0, 0);
+  fa1 = frag_a(s0, 1);
+#pragma unroll
+  for (int j = 0; j < FN; ++j) fb[j] = frag_b(s0, j);
+  for (int kt = 0; kt < KT; kt += NST) {
+#define LM_STEP(S_)                                                                      \
+  if constexpr (S_ < NST) {                                                              \
+    step(sts[(S_ + NST - 1) % NST], sts[S_], sts[(S_ + 1) % NST], kt + S_);              \
+    if (kt + S_ + 1 >= KT) break;                                                        \
   }
+    LM_STEP(0)
+    LM_STEP(1)
+    LM_STEP(2)
+    LM_STEP(3)
+#undef LM_STEP
+  }
+  // the loads of the steps past the last have written their zeros
   lm_wait_barrier<0>();
 
-  // the adapters, one run of rows after another.  The reduction runs over slots of 16
-  // ranks, all of the first piece, then the second (fp32 outputs: the third), two
-  // slots an MFMA.
+  // The adapters, one run of rows after another.  The reduction runs over slots of 16
+  // ranks, all of the first piece, then of the second (fp32 outputs: the third), two
+  // slots an MFMA.  With BT, 64 ranks of the bank at a time go through LDS.
   constexpr int NP = sizeof(OutT) == 4 ? 3 : 2;
-  const int nb = p.RP / 16, ns = NP * nb;
+  constexpr int RB = 4;
+  static_assert(RB * 16 * BN * 2 <= STAGE, "ranks in a stage");
+  const int nb = p.RP / 16;
   int row_at[FM], id_at[FM];
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
@@ -554,77 +616,48 @@ __device__ __forceinline__ void lm_tile(const LmMm& p, uint8_t* smem, i32x2* s_o
     const __amdgpu_buffer_rsrc_t lr_ =
         buf_rsrc(static_cast<const uint16_t*>(p.bank) + static_cast<int64_t>(l) * p.R * n,
                  static_cast<uint32_t>(p.R) * static_cast<uint32_t>(n) * 2u);
-    auto add = [&](int s2, const u32x4* fb) {  // slots 2 s2 and 2 s2 + 1
-      u32x4 hi[FN], lo[FN];
-      if constexpr (F16) {
-#pragma unroll
-        for (int j = 0; j < FN; ++j) lm_split(fb[j], hi[j], lo[j]);
-      }
-      const bool live = 2 * s2 + (g >> 1) < ns;
-#pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        const int b0 = (wm * FM + i) * 16;
-        if (b0 + 16 <= at || b0 >= end) continue;
-        u32x4 fv = {0, 0, 0, 0};
-        if (live && id_at[i] == l)
-          fv = gld<u32x4>(p.pieces + static_cast<int64_t>(row_at[i]) * 3 * p.RP + s2 * 32 + g * 8);
-#pragma unroll
-        for (int j = 0; j < FN; ++j) {
-          f32x4 d = lm_mfma<false>(F16 ? hi[j] : fb[j], fv, acc[i][j]);
-          if constexpr (F16) d = lm_mfma<false>(lo[j], fv, d);
-          // a NaN in this adapter's bank is not another row's
-          if (id_at[i] == l) acc[i][j] = d;
-        }
-      }
-    };
-    if constexpr (!BT) {
-      for (int s2 = 0; 2 * s2 < ns; ++s2) {
-        const int rk = (2 * s2 + (g >> 1)) % nb * 16 + (g & 1) * 8;
-        u32x4 fb[FN];
-#pragma unroll
-        for (int j = 0; j < FN; ++j) {
-          const int c = (wn * FN + j) * 16 + r;
-          fb[j] = buf_ld128(lr_, c < cols && rk < p.R ? (static_cast<uint32_t>(n0 + c) * p.R + rk) * 2 : LM_OUT, 0);
-        }
-        add(s2, fb);
-      }
-    } else {
-      // ranks 16 RB at a time through LDS, all pieces of them
-      constexpr int RB = STAGE * NST / (BN * 32) < 4 ? STAGE * NST / (BN * 32) : 4;
-      for (int j0 = 0; j0 < nb; j0 += RB) {
-        const int part = min(nb - j0, RB);
+    for (int j0 = 0; j0 < nb; j0 += BT ? RB : nb) {
+      const int part = BT ? min(nb - j0, RB) : nb, ns = NP * part;
+      if constexpr (BT) {
         __syncthreads();
         for (int q = tid; q < part * 16 * CPW; q += 64 * NW) {
-          const int row = q / CPW, c = q % CPW;
-          const int col = (((c >> 1) ^ lm_tswz<BN>(row)) * 2 + (c & 1)) * 8, rk = j0 * 16 + row;
-          const u32x4 v = buf_ld128(lr_, col < cols && rk < p.R ? (static_cast<uint32_t>(rk) * n + n0 + col) * 2 : LM_OUT, 0);
-          *reinterpret_cast<u32x4*>(smem + q * 16) = v;
+          const int row = q / CPW, c = q % CPW, rk = j0 * 16 + row;
+          const int col = (((c >> 1) ^ lm_tswz<BN>(row)) * 2 + (c & 1)) * 8;
+          *reinterpret_cast<u32x4*>(s0 + q * 16) = buf_ld128(
+              lr_, col < cols && rk < p.R ? (static_cast<uint32_t>(rk) * n + n0 + col) * 2 : LM_OUT, 0);
         }
         __syncthreads();
-        // slots of these ranks: piece by piece, 16 ranks an MFMA half
-        for (int s = 0; s < NP * part; s += 2) {
-          const int mine = min(s + (g >> 1), NP * part - 1);
-          const int pc = mine / part, jb = mine % part;
-          const bool live = s + (g >> 1) < NP * part;
-          u32x4 fb[FN], hi[FN], lo[FN];
+      }
+      for (int s = 0; s < ns; s += 2) {
+        // this lane's slot: piece pc, ranks 16 (j0 + jb) + 8 (g & 1) ..
+        const int mine = min(s + (g >> 1), ns - 1), pc = mine / part, jb = mine % part;
+        const bool live = s + (g >> 1) < ns;
+        u32x4 fv[FM];
 #pragma unroll
-          for (int j = 0; j < FN; ++j) {
-            fb[j] = frag_t(smem, j, jb * 16 + (g & 1) * 8);
-            if constexpr (F16) lm_split(fb[j], hi[j], lo[j]);
+        for (int i = 0; i < FM; ++i) {
+          fv[i] = u32x4{0, 0, 0, 0};
+          if (live && id_at[i] == l)
+            fv[i] = gld<u32x4>(p.pieces + (static_cast<int64_t>(row_at[i]) * 3 + pc) * p.RP +
+                               (j0 + jb) * 16 + (g & 1) * 8);
+        }
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          u32x4 hi, lo = {0, 0, 0, 0};
+          if constexpr (BT) {
+            hi = column(s0, wn * FN + j, jb * 16 + (g & 1) * 8);
+          } else {
+            const int c = (wn * FN + j) * 16 + r, rk = jb * 16 + (g & 1) * 8;
+            hi = buf_ld128(lr_, c < cols && rk < p.R ? (static_cast<uint32_t>(n0 + c) * p.R + rk) * 2 : LM_OUT, 0);
           }
+          if constexpr (F16) lm_split(hi, hi, lo);
 #pragma unroll
           for (int i = 0; i < FM; ++i) {
             const int b0 = (wm * FM + i) * 16;
             if (b0 + 16 <= at || b0 >= end) continue;
-            u32x4 fv = {0, 0, 0, 0};
-            if (live && id_at[i] == l)
-              fv = gld<u32x4>(p.pieces + (static_cast<int64_t>(row_at[i]) * 3 + pc) * p.RP + (j0 + jb) * 16 + (g & 1) * 8);
-#pragma unroll
-            for (int j = 0; j < FN; ++j) {
-              f32x4 d = lm_mfma<false>(F16 ? hi[j] : fb[j], fv, acc[i][j]);
-              if constexpr (F16) d = lm_mfma<false>(lo[j], fv, d);
-              if (id_at[i] == l) acc[i][j] = d;
-            }
+            f32x4 d = lm_mfma<false>(hi, fv[i], acc[i][j]);
+            if constexpr (F16) d = lm_mfma<false>(lo, fv[i], d);
+            // a NaN in this adapter's bank is not another row's
+            if (id_at[i] == l) acc[i][j] = d;
           }
         }
       }
@@ -632,43 +665,76 @@ __device__ __forceinline__ void lm_tile(const LmMm& p, uint8_t* smem, i32x2* s_o
     at = end;
   }
 
-  // acc[i][j][q]: row 16 i + r, column 16 j + 4 g + q of the wavefront's
-  constexpr int ES = sizeof(OutT);
+  // acc[i][j][q]: row 16 i + r, column 16 j + 4 g + q of the wavefront's.  The outputs go
+  // through the wavefront's own part of the stages, PB blocks of rows at a time, so that
+  // it stores runs of RBY bytes of a row, 16 bytes a lane.  16-byte chunk c of a row sits
+  // at slot c ^ (row % CPR).
+  constexpr int ES = sizeof(OutT), RBY = 16 * FN * ES, CPR = RBY / 16;
+  constexpr int ROOM = NST * STAGE / NW, PB = 16 * FM * RBY <= ROOM ? FM : FM / 2;
+  constexpr int PER = STAGE / (PB * 16 * RBY);  // parts in a stage
+  static_assert(PB * 16 * RBY <= ROOM && NW <= NST * PER && 64 % CPR == 0, "epilogue");
+  uint8_t* const reg = sts[wave / PER] + wave % PER * (PB * 16 * RBY);
+  __syncthreads();  // the ranks of the last run have been read
+  f32x4 bias[FN];
 #pragma unroll
   for (int j = 0; j < FN; ++j) {
     const int c = (wn * FN + j) * 16 + 4 * g;
-    if (c >= cols) continue;
-    f32x4 bias = {0.f, 0.f, 0.f, 0.f};
-    if (p.bias != nullptr) {
+    bias[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (p.bias != nullptr && c < cols) {
       const u32x2 raw = gld<u32x2>(static_cast<const uint16_t*>(p.bias) + n0 + c);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const uint16_t h = static_cast<uint16_t>(raw[q >> 1] >> (16 * (q & 1)));
-        bias[q] = F16 ? static_cast<float>(__builtin_bit_cast(_Float16, h)) : bf16_bits_to_f32(h);
+        bias[j][q] = F16 ? static_cast<float>(__builtin_bit_cast(_Float16, h)) : bf16_bits_to_f32(h);
       }
     }
+  }
+  constexpr int RPI = 64 / CPR;  // rows per store
+  const int pr = lane / CPR, pcol = lane % CPR;
+  const int col = wn * 16 * FN + pcol * (16 / ES);
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      if (row_at[i] < 0) continue;
-      OutT* const o = static_cast<OutT*>(p.out) + static_cast<int64_t>(row_at[i]) * n + n0 + c;
-      const f32x4 v = acc[i][j] + bias;
-      if constexpr (ES == 4) {
-        gst<f32x4>(o, v);
-      } else {
-        typedef OutT t4 __attribute__((ext_vector_type(4)));
-        gst<u32x2>(o, __builtin_bit_cast(u32x2, __builtin_convertvector(v, t4)));
+  for (int i0 = 0; i0 < FM; i0 += PB) {
+#pragma unroll
+    for (int i = i0; i < i0 + PB; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const f32x4 v = acc[i][j] + bias[j];
+        uint8_t* const at = reg + ((i - i0) * 16 + r) * RBY;
+        if constexpr (ES == 4) {
+          *reinterpret_cast<f32x4*>(at + ((4 * j + g) ^ (r % CPR)) * 16) = v;
+        } else {
+          typedef OutT t4 __attribute__((ext_vector_type(4)));
+          *reinterpret_cast<t4*>(at + ((2 * j + (g >> 1)) ^ (r % CPR)) * 16 + (g & 1) * 8) =
+              __builtin_convertvector(v, t4);
+        }
       }
+    // LDS operations of one wavefront complete in order
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int q = 0; q < PB * 16; q += RPI) {
+      const int lrow = q + pr;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(reg + lrow * RBY + (pcol ^ (lrow % CPR)) * 16);
+      const int row = s_order[(wm * FM + i0) * 16 + lrow].x;
+      if (row >= 0 && col < cols)
+        __builtin_nontemporal_store(
+            v, (MI_GLOBAL u32x4*)(static_cast<OutT*>(p.out) + static_cast<int64_t>(row) * n + n0 + col));
     }
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
 template <bool F16, bool BT, int WM, int WN, int FM, int FN, int NST, typename OutT>
 __global__ __launch_bounds__(64 * WM * WN)
-    __attribute__((amdgpu_waves_per_eu(2))) void lm_mm_kernel(LmMm p) {
-  constexpr int BM = 16 * FM * WM, BN = 16 * FN * WN;
-  __shared__ __attribute__((aligned(16))) uint8_t smem[NST * (BM + BN) * 128];
+    __attribute__((amdgpu_waves_per_eu(2, 2))) void lm_mm_kernel(LmMm p) {
+  constexpr int BM = 16 * FM * WM, BN = 16 * FN * WN, STAGE = (BM + BN) * 128;
+  __shared__ __attribute__((aligned(16))) uint8_t s0[STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t s1[STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t s2[NST >= 3 ? STAGE : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t s3[NST == 4 ? STAGE : 16];
   __shared__ i32x2 s_order[BM];
-  lm_tile<F16, BT, WM, WN, FM, FN, NST, OutT>(p, smem, s_order);
+  const LmPlace t = lm_place<BM, BN>(p);
+  if (t.rows == 0) return;
+  lm_tile<F16, BT, WM, WN, FM, FN, NST, OutT>(p, t, s0, s1, s2, s3, s_order);
 }
 
 // ---------------------------------------------------------------------------
@@ -925,6 +991,9 @@ mi_status lm_mm_launch(const LmMm& a, hipStream_t st) {
 
 template <bool F16, bool BT, typename OutT>
 mi_status lm_mm(const LmMm& a, hipStream_t st) {
+  auto tiles = [&](int64_t bm, int64_t bn) { return (a.T + bm - 1) / bm * ((a.n + bn - 1) / bn); };
+  if (tiles(64, 64) <= 512) return lm_mm_launch<F16, BT, 2, 2, 2, 2, 4, OutT>(a, st);
+  if (tiles(128, 128) > 512) return lm_mm_launch<F16, BT, 2, 4, 8, 4, 2, OutT>(a, st);
   return lm_mm_launch<F16, BT, 2, 2, 4, 4, 2, OutT>(a, st);
 }
 
