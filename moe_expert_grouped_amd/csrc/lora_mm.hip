@@ -11,7 +11,7 @@
 //
 // Steps, each a launch on the caller's stream:
 //   plan    one workgroup sorts the rows by adapter (stable), cuts every adapter's
-//           rows into items of 16 and its items into chunks
+//           rows into items of 32 and its items into chunks
 //   shrink  v (or u) of an item; kept as three bf16 pieces whose sum has 24 bits,
 //           so that the second product runs on bf16 MFMAs without a rounding of v
 //   mm      the dense product over rows in sorted order, the adapters' part added
@@ -33,8 +33,9 @@ typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int LM_MAX_ADAPTERS = 1024;
 constexpr int LM_MAX_RANK = 256;
-constexpr int LM_ITEM = 16;            // rows of an item
+constexpr int LM_ITEM = 32;            // rows of an item
 constexpr int LM_BK = 64;              // 128 bytes of a row of x: one step
+constexpr int LM_FEW_ROWS = 64;       // up to here the few-row kernels
 constexpr uint32_t LM_OUT = 0x80000000u;  // past every descriptor's range
 
 __device__ __forceinline__ lds_void_ptr lm_lds(void* p) { return (lds_void_ptr)(p); }
@@ -43,38 +44,41 @@ __device__ __forceinline__ lds_void_ptr lm_lds(void* p) { return (lds_void_ptr)(
 struct LmPlan {
   i32x2* order;      // [T] {row, adapter}; rows without one last, adapter L
   int* seg;         // [L + 1] first position of every adapter
-  i32x4* items;      // {adapter, first position, rows, 0}
-  int* slot_row;    // [16 * items] row of every slot of an item, -1: none
+  int* item_id;     // adapter of every item
+  int* slot_row;    // [LM_ITEM * items] row of every slot of an item, -1: none
   i32x4* chunks;     // {adapter, first item, items, place of its partial sums or -1}
   i32x4* spans;      // [L] {first chunk, chunks, first partial place or -1, 0}
-  int* totals;      // items, chunks
-  uint16_t* zeros;  // a row of zeros
+  int* totals;      // items of adapters, chunks, items with those of rows without one
+  uint16_t* zeros;  // 16 bytes of zeros
 };
 
 // ---------------------------------------------------------------------------
 // plan
 // ---------------------------------------------------------------------------
-constexpr int PL_T = 1024, PL_W = PL_T / 64;
+constexpr int PL_T = 1024, PL_W = PL_T / 64, PL_S = PL_W + 1;
 
-// exclusive block sums of v, all of it in `total`
-__device__ __forceinline__ uint64_t pl_scan(uint64_t v, uint64_t* s, uint64_t* total) {
+// exclusive sums over the workgroup of two values at once, all of them in `total`
+struct PlPair { uint64_t a, b; };
+__device__ __forceinline__ PlPair pl_scan(PlPair v, PlPair* s, PlPair* total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  uint64_t incl = v;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const uint64_t up = __shfl_up(incl, o, 64);
-    if (lane >= o) incl += up;
-  }
-  __syncthreads();
+  auto upto = [&](PlPair x, int width) {
+#pragma unroll 1
+    for (int o = 1; o < width; o <<= 1) {
+      const uint64_t a = __shfl_up(x.a, o, 64), b = __shfl_up(x.b, o, 64);
+      if (lane >= o) {
+        x.a += a;
+        x.b += b;
+      }
+    }
+    return x;
+  };
+  const PlPair incl = upto(v, 64);
   if (lane == 63) s[wave] = incl;
   __syncthreads();
-  uint64_t before = 0, all = 0;
-  for (int w = 0; w < PL_W; ++w) {
-    if (w < wave) before += s[w];
-    all += s[w];
-  }
-  *total = all;
-  return before + incl - v;
+  const PlPair all = upto(lane < PL_W ? s[lane] : PlPair{0, 0}, PL_W);
+  *total = {__shfl(all.a, PL_W - 1, 64), __shfl(all.b, PL_W - 1, 64)};
+  const uint64_t a = __shfl(all.a, wave - 1, 64), b = __shfl(all.b, wave - 1, 64);
+  return {incl.a - v.a + (wave ? a : 0), incl.b - v.b + (wave ? b : 0)};
 }
 
 // lanes of the wavefront that hold the same value
@@ -88,99 +92,127 @@ __device__ __forceinline__ uint64_t pl_peers(int v, int bits) {
   return peers;
 }
 
+// One workgroup: a launch of several would need two more for the sums between them.
+// The ids of 16384 rows at a time are held in LDS, which is all of them for most calls:
+// the second pass then reads nothing again.  The loops over them are not unrolled: a kernel
+// that runs once a call waits for its instructions more than for its data.
+constexpr int PL_HELD = 1024;  // ids of a wavefront in LDS
+
 __global__ __launch_bounds__(PL_T) void lm_plan_kernel(const int32_t* __restrict__ ids, int T,
-                                                       int L, int chunk_items, int zero_chunks,
-                                                       LmPlan p) {
-  __shared__ int s_cnt[PL_W * (LM_MAX_ADAPTERS + 1)];  // [PL_W][L + 1]
-  __shared__ int s_item0[LM_MAX_ADAPTERS], s_seg[LM_MAX_ADAPTERS];
-  __shared__ uint64_t s_scan[PL_W];
+                                                       int L, int chunk_items, LmPlan p) {
+  __shared__ int s_cnt[(LM_MAX_ADAPTERS + 1) * PL_S];  // an adapter's counts by wavefront
+  __shared__ uint16_t s_ids[PL_W * PL_HELD];
+  __shared__ int s_item0[LM_MAX_ADAPTERS + 1], s_seg[LM_MAX_ADAPTERS + 1];
+  __shared__ PlPair s_scan[PL_W];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  for (int i = tid; i < PL_W * (L + 1); i += PL_T) s_cnt[i] = 0;
-  for (int i = tid; i < zero_chunks; i += PL_T)
-    gst<u32x4>(p.zeros + i * 8, u32x4{0, 0, 0, 0});
-  __syncthreads();
-  // a wavefront has a run of rows, 64 at a time
   const int per = ((T + PL_W - 1) / PL_W + 63) & ~63;
   const int r0 = min(wave * per, T), r1 = min(r0 + per, T);
-  const int bits = 32 - __builtin_clz(L);  // ids 0 .. L
-  int* const cnt = s_cnt + wave * (L + 1);
-  auto id_of = [&](int r) {
-    const int id = r < r1 ? gld<int32_t>(ids + r) : L;
-    return id < 0 || id > L ? L : id;
+  uint16_t* const held = s_ids + wave * PL_HELD;
+  auto hold = [&](int at) {
+    const int n = min(r1 - at, PL_HELD);
+#pragma unroll 4
+    for (int i = lane; i < n; i += 64) {
+      const int id = gld<int32_t>(ids + at + i);
+      held[i] = static_cast<uint16_t>(id < 0 || id > L ? L : id);
+    }
   };
-  for (int r = r0; r < r1; r += 64) {
-    const int id = id_of(r + lane);
-    const uint64_t live = __ballot(r + lane < r1);
-    const uint64_t peers = pl_peers(id, bits) & live;
-    if (r + lane < r1 && (peers & ((1ull << lane) - 1)) == 0) cnt[id] += __popcll(peers);
-    __builtin_amdgcn_wave_barrier();
+  hold(r0);
+  #pragma unroll 1
+  for (int i = tid; i < (L + 1) * PL_S; i += PL_T) s_cnt[i] = 0;
+  if (tid == 0) gst<u32x4>(p.zeros, u32x4{0, 0, 0, 0});
+  __syncthreads();
+  const int bits = 32 - __builtin_clz(L);  // ids 0 .. L
+  int* const cnt = s_cnt + wave;  // of adapter l at l * PL_S
+  // the lanes of `live` that hold the same id; a run's rows all do
+  auto peers_of = [&](int id, uint64_t live) {
+    const uint64_t same = __ballot(id == __builtin_amdgcn_readfirstlane(id)) & live;
+    return same == live ? live : pl_peers(id, bits) & live;
+  };
+  for (int at = r0; at < r1; at += PL_HELD) {
+    if (at > r0) hold(at);
+#pragma unroll 1
+    for (int i = lane; at + i - lane < min(r1, at + PL_HELD); i += 64) {
+      const bool in = at + i < r1;
+      const int id = in ? held[i] : L;
+      const uint64_t peers = peers_of(id, __ballot(in));
+      if (in && (peers & ((1ull << lane) - 1)) == 0) cnt[id * PL_S] += __popcll(peers);
+      __builtin_amdgcn_wave_barrier();
+    }
   }
   __syncthreads();
   // thread l: adapter l
   int rows = 0;
   if (tid < L)
-    for (int w = 0; w < PL_W; ++w) rows += s_cnt[w * (L + 1) + tid];
+    for (int w = 0; w < PL_W; ++w) rows += s_cnt[tid * PL_S + w];
   const int items = (rows + LM_ITEM - 1) / LM_ITEM;
   const int chunks = tid < L ? max((items + chunk_items - 1) / chunk_items, 1) : 0;
-  uint64_t all_rows, all_chunks;
-  const uint64_t a = pl_scan(static_cast<uint64_t>(rows) | static_cast<uint64_t>(items) << 32,
-                             s_scan, &all_rows);
-  const uint64_t b = pl_scan(static_cast<uint64_t>(chunks) |
-                                 static_cast<uint64_t>(chunks > 1 ? chunks : 0) << 32,
-                             s_scan, &all_chunks);
-  const int seg = static_cast<int>(a), item0 = static_cast<int>(a >> 32);
-  const int chunk0 = static_cast<int>(b), part0 = static_cast<int>(b >> 32);
+  PlPair all;
+  const PlPair before =
+      pl_scan({static_cast<uint64_t>(rows) | static_cast<uint64_t>(items) << 32,
+               static_cast<uint64_t>(chunks) | static_cast<uint64_t>(chunks > 1 ? chunks : 0) << 32},
+              s_scan, &all);
+  const int seg = static_cast<int>(before.a), item0 = static_cast<int>(before.a >> 32);
+  const int chunk0 = static_cast<int>(before.b), part0 = static_cast<int>(before.b >> 32);
+  // this wavefront's first place of an adapter's rows, for every wavefront
+  auto places = [&](int l, int run) {
+    for (int w = 0; w < PL_W; ++w) {
+      const int c = s_cnt[l * PL_S + w];
+      s_cnt[l * PL_S + w] = run;
+      run += c;
+    }
+  };
   if (tid < L) {
     s_seg[tid] = seg;
     s_item0[tid] = item0;
     gst<int>(p.seg + tid, seg);
+#pragma unroll 1
     for (int c = 0; c < chunks; ++c)
       gst<i32x4>(p.chunks + chunk0 + c,
-                i32x4{tid, item0 + c * chunk_items, min(items - c * chunk_items, chunk_items),
-                     chunks > 1 ? part0 + c : -1});
+                 i32x4{tid, item0 + c * chunk_items, min(items - c * chunk_items, chunk_items),
+                       chunks > 1 ? part0 + c : -1});
     gst<i32x4>(p.spans + tid, i32x4{chunk0, chunks, chunks > 1 ? part0 : -1, 0});
+#pragma unroll 1
     for (int i = rows; i < items * LM_ITEM; ++i) gst<int>(p.slot_row + item0 * LM_ITEM + i, -1);
-    int run = seg;
-    for (int w = 0; w < PL_W; ++w) {
-      const int c = s_cnt[w * (L + 1) + tid];
-      s_cnt[w * (L + 1) + tid] = run;
-      run += c;
-    }
+    places(tid, seg);
   }
-  if (tid == 0) {
-    const int in = static_cast<int>(all_rows);
+  if (tid == PL_T - 1) {
+    // the rows without an adapter follow, in items of their own
+    const int in = static_cast<int>(all.a), real = static_cast<int>(all.a >> 32);
+    const int more = (T - in + LM_ITEM - 1) / LM_ITEM;
+    s_seg[L] = in;
+    s_item0[L] = real;
     gst<int>(p.seg + L, in);
-    gst<int>(p.totals, static_cast<int>(all_rows >> 32));
-    gst<int>(p.totals + 1, static_cast<int>(all_chunks));
-    int run = in;
-    for (int w = 0; w < PL_W; ++w) {
-      const int c = s_cnt[w * (L + 1) + L];
-      s_cnt[w * (L + 1) + L] = run;
-      run += c;
-    }
+    gst<i32x4>(p.totals, i32x4{real, static_cast<int>(all.b), real + more, 0});
+#pragma unroll 1
+    for (int i = T - in; i < more * LM_ITEM; ++i) gst<int>(p.slot_row + real * LM_ITEM + i, -1);
+    places(L, in);
   }
   __syncthreads();
-  for (int r = r0; r < r1; r += 64) {
-    const int row = r + lane, id = id_of(row);
-    const uint64_t live = __ballot(row < r1);
-    const uint64_t peers = pl_peers(id, bits) & live;
-    const uint64_t below = peers & ((1ull << lane) - 1);
-    int pos = 0;
-    if (row < r1) {
-      pos = cnt[id] + __popcll(below);
-      // pos < T holds where the ids did not change between the passes
-      if (pos < T) gst<i32x2>(p.order + pos, i32x2{row, id});
-      if (id < L && pos < T) {
-        const int rank = pos - s_seg[id], item = s_item0[id] + rank / LM_ITEM;
-        gst<int>(p.slot_row + item * LM_ITEM + rank % LM_ITEM, row);
-        if (rank % LM_ITEM == 0)
-          gst<i32x4>(p.items + item, i32x4{id, pos, 0, 0});
+  for (int at = r0; at < r1; at += PL_HELD) {
+    if (per > PL_HELD) hold(at);
+#pragma unroll 1
+    for (int i = lane; at + i - lane < min(r1, at + PL_HELD); i += 64) {
+      const int row = at + i;
+      const bool in = row < r1;
+      const int id = in ? held[i] : L;
+      const uint64_t peers = peers_of(id, __ballot(in));
+      const uint64_t below = peers & ((1ull << lane) - 1);
+      int pos = 0;
+      if (in) {
+        pos = cnt[id * PL_S] + __popcll(below);
+        // pos < T holds where the ids did not change between the passes
+        if (pos < T) {
+          gst<i32x2>(p.order + pos, i32x2{row, id});
+          const int rank = pos - s_seg[id], item = s_item0[id] + rank / LM_ITEM;
+          gst<int>(p.slot_row + item * LM_ITEM + rank % LM_ITEM, row);
+          if (rank % LM_ITEM == 0) gst<int>(p.item_id + item, id);
+        }
       }
+      // LDS operations of one wavefront complete in order
+      __builtin_amdgcn_wave_barrier();
+      if (in && below == 0) cnt[id * PL_S] = pos + __popcll(peers);
+      __builtin_amdgcn_wave_barrier();
     }
-    // LDS operations of one wavefront complete in order
-    __builtin_amdgcn_wave_barrier();
-    if (row < r1 && below == 0) cnt[id] = pos + __popcll(peers);
-    __builtin_amdgcn_wave_barrier();
   }
 }
 
@@ -240,7 +272,7 @@ __device__ __forceinline__ u32x4 lm_column(const uint8_t* first, const uint8_t* 
 // shrink: one item's rows times its adapter's matrix.
 //   BT == false: bank [L, R, C], v[t, r] = sum_c x[t, c] bank[l, r, c]
 //   BT == true:  bank [L, C, R], v[t, r] = sum_c x[t, c] bank[l, c, r]
-// A workgroup has 16 rows and 16 NB ranks; its wavefronts take steps of 64 columns
+// A workgroup has the item's rows and 16 NB ranks; its wavefronts take steps of 64 columns
 // in turn, and their sums are added in order in LDS.
 // ---------------------------------------------------------------------------
 struct LmShrink {
@@ -260,88 +292,141 @@ constexpr int SH_W = 8;
 
 template <bool F16, bool BT, int NB>
 __global__ __launch_bounds__(64 * SH_W) void lm_shrink_kernel(LmShrink a) {
+  constexpr int FM = LM_ITEM / 16;
   __shared__ __attribute__((aligned(16))) uint8_t s_buf[SH_W * 64 * NB * 32];
-  static_assert(64 * NB * 32 >= NB * 64 * 16, "the sums fit the stages");
-  const int item = blockIdx.x;
-  if (item >= gld<int>(a.plan.totals)) return;
-  const i32x4 it = gld<i32x4>(a.plan.items + item);
-  const int l = it.x;
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  static_assert(64 * NB * 32 >= FM * NB * 64 * 16, "the sums fit the stages");
+  const int item = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
+  const int* const slots = a.plan.slot_row + item * LM_ITEM;
+  const int R = a.R, rank0 = blockIdx.y * 16 * NB;
+  // all that the plan says of the item at once (past the last item it is not used)
+  const i32x4 totals = gld<i32x4>(a.plan.totals);
+  const int l = gld<int>(a.plan.item_id + item);
   const int r = lane & 15, g = lane >> 4;
-  const int rank0 = blockIdx.y * 16 * NB;
-  const int row = gld<int>(a.plan.slot_row + item * LM_ITEM + r);
-  const int C = a.C, R = a.R, KT = (C + LM_BK - 1) / LM_BK;
+  int row_of[FM];
+#pragma unroll
+  for (int i = 0; i < FM; ++i) row_of[i] = gld<int>(slots + 16 * i + r);
+  if (item >= totals.z) return;
+  if (item >= totals.x) {  // rows without an adapter: zeros for activations
+    if (a.out != nullptr)
+      for (int q = tid; q < LM_ITEM * NB * 4; q += 64 * SH_W) {
+        const int t = gld<int>(slots + q / (NB * 4)), rk = rank0 + q % (NB * 4) * 4;
+        if (t >= 0 && rk < R) gst<f32x4>(a.out + static_cast<int64_t>(t) * R + rk, f32x4{0.f, 0.f, 0.f, 0.f});
+      }
+    return;
+  }
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int C = a.C, KT = (C + LM_BK - 1) / LM_BK;
   const __amdgpu_buffer_rsrc_t xr =
       buf_rsrc(a.x, static_cast<uint32_t>(a.T) * static_cast<uint32_t>(C) * 2u);
   const __amdgpu_buffer_rsrc_t br =
       buf_rsrc(static_cast<const uint16_t*>(a.bank) + static_cast<int64_t>(l) * R * C,
                static_cast<uint32_t>(R) * static_cast<uint32_t>(C) * 2u);
-  const uint32_t vx = row >= 0 ? static_cast<uint32_t>(row) * C * 2 : LM_OUT;
-  f32x4 acc[NB];
+  // lane (r, g) has chunks g and g + 4 of a step of row r
+  uint32_t vx[FM];
 #pragma unroll
-  for (int j = 0; j < NB; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int kt = wave; kt < KT; kt += SH_W) {
-    u32x4 fx[2];
+  for (int i = 0; i < FM; ++i) {
+    vx[i] = row_of[i] >= 0 ? static_cast<uint32_t>(row_of[i]) * C * 2 + g * 16 : LM_OUT;
+  }
+  const bool two = __builtin_amdgcn_readfirstlane(row_of[1]) >= 0;  // any rows in block 1
+  constexpr int CPR = 2 * NB;  // BT: 16-byte pieces of a bank's row
+  uint32_t vb[CPR];
+#pragma unroll
+  for (int i = 0; i < CPR; ++i) {
+    if constexpr (BT) {
+      const int at = i * 64 + lane, rk = rank0 + at % CPR * 8;
+      vb[i] = rk < R ? (static_cast<uint32_t>(at / CPR) * R + rk) * 2 : LM_OUT;
+    } else {
+      const int rk = rank0 + 16 * (i >> 1) + r;
+      vb[i] = rk < R ? static_cast<uint32_t>(rk) * C * 2 + g * 16 + 64 * (i & 1) : LM_OUT;
+    }
+  }
+  struct Step { u32x4 x[FM][2], b[CPR]; };
+  auto load = [&](Step& q, int kt) {  // a step past the last loads zeros
+    const int kb = min(kt, KT - 1);
+    const uint32_t so = __builtin_amdgcn_readfirstlane(kb * (LM_BK * 2));
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int c = kt * LM_BK + 32 * h + 8 * g;
-      fx[h] = buf_ld128(xr, c < C ? vx + c * 2 : LM_OUT, 0);
+      const uint32_t drop = kt < KT && kb * LM_BK + 32 * h + 8 * g < C ? 0u : LM_OUT;
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+        if (i == 0 || two) q.x[i][h] = buf_ld128(xr, (vx[i] + 64 * h) | drop, so);
+      if constexpr (!BT)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) q.b[2 * j + h] = buf_ld128(br, vb[2 * j + h] | drop, so);
     }
-    if constexpr (!BT) {
-#pragma unroll
-      for (int j = 0; j < NB; ++j)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int c = kt * LM_BK + 32 * h + 8 * g, rk = rank0 + 16 * j + r;
-          const u32x4 fb = buf_ld128(
-              br, c < C && rk < R ? (static_cast<uint32_t>(rk) * C + c) * 2 : LM_OUT, 0);
-          acc[j] = lm_mfma<F16>(fb, fx[h], acc[j]);
-        }
-    } else {
-      // this wavefront's stage: 64 rows of 16 NB ranks
-      uint8_t* const st = s_buf + wave * (64 * NB * 32);
-      constexpr int CPR = 2 * NB;  // 16-byte pieces of a row
-      u32x4 q[CPR];
-#pragma unroll
-      for (int i = 0; i < CPR; ++i) {
-        const int at = i * 64 + lane, c = kt * LM_BK + at / CPR, rk = rank0 + at % CPR * 8;
-        q[i] = buf_ld128(br, c < C && rk < R ? (static_cast<uint32_t>(c) * R + rk) * 2 : LM_OUT, 0);
-      }
+    if constexpr (BT) {
+      const uint32_t sob = __builtin_amdgcn_readfirstlane(kb * (LM_BK * 2) * R);
 #pragma unroll
       for (int i = 0; i < CPR; ++i)
-        *reinterpret_cast<u32x4*>(st + (i * 64 + lane) * 16) = q[i];
+        q.b[i] = buf_ld128(br, kt < KT && kb * LM_BK + (i * 64 + lane) / CPR < C ? vb[i] : LM_OUT, sob);
+    }
+  };
+  f32x4 acc[FM][NB];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  uint8_t* const st = s_buf + wave * (64 * NB * 32);  // BT: this wavefront's 64 rows of ranks
+  auto add = [&](const Step& q) {
+    if constexpr (BT) {
       __builtin_amdgcn_wave_barrier();
 #pragma unroll
-      for (int j = 0; j < NB; ++j)
+      for (int i = 0; i < CPR; ++i) *reinterpret_cast<u32x4*>(st + (i * 64 + lane) * 16) = q.b[i];
+      __builtin_amdgcn_wave_barrier();
+    }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        u32x4 fb;
+        if constexpr (BT) {
           const uint8_t* at = st + (32 * h + 8 * g + (r >> 2)) * (NB * 32) + j * 32 + (r & 3) * 8;
-          acc[j] = lm_mfma<F16>(lm_column(at, at + 4 * NB * 32), fx[h], acc[j]);
+          fb = lm_column(at, at + 4 * NB * 32);
+        } else {
+          fb = q.b[2 * j + h];
         }
-      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+          if (i == 0 || two) acc[i][j] = lm_mfma<F16>(fb, q.x[i][h], acc[i][j]);
+      }
+  };
+  constexpr int P = NB == 1 ? 4 : NB == 2 ? 3 : 2;  // steps in flight
+  Step q[P];
+#pragma unroll
+  for (int u = 0; u < P; ++u) {
+    load(q[u], wave + SH_W * u);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  for (int kt = wave; kt < KT; kt += SH_W * P) {
+#pragma unroll
+    for (int u = 0; u < P; ++u) {
+      add(q[u]);
+      load(q[u], kt + SH_W * (u + P));
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
   __syncthreads();
   f32x4* const red = reinterpret_cast<f32x4*>(s_buf);
 #pragma unroll
-  for (int j = 0; j < NB; ++j) red[(wave * NB + j) * 64 + lane] = acc[j];
-  __syncthreads();
-  // quad q: ranks 16 j + 4 g .. of the row at slot q % 16
-  for (int q = tid; q < NB * 64; q += 64 * SH_W) {
-    f32x4 v = red[q];
-    for (int w = 1; w < SH_W; ++w) v += red[w * NB * 64 + q];
-    const int rk = rank0 + 16 * (q >> 6) + 4 * ((q & 63) >> 4);
-    if (rk >= a.RP) continue;
-    const int slot = item * LM_ITEM + (q & 15);
-    const int t = gld<int>(a.plan.slot_row + slot);
-    const float s = a.scale != nullptr ? gld<float>(a.scale + l) : 1.f;
-    auto put = [&](f32x4 w, uint16_t* rows, uint16_t* cols) {
+  for (int i = 0; i < FM; ++i)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = t >= 0 && rk < R ? w[i] * s : 0.f;
+    for (int j = 0; j < NB; ++j) red[((wave * FM + i) * NB + j) * 64 + lane] = acc[i][j];
+  __syncthreads();
+  // quad: ranks 16 j + 4 g .. of slot 16 i + r
+  const float s = a.scale != nullptr ? gld<float>(a.scale + l) : 1.f;
+  for (int at = tid; at < FM * NB * 64; at += 64 * SH_W) {
+    f32x4 v = red[at];
+#pragma unroll
+    for (int w = 1; w < SH_W; ++w) v += red[w * FM * NB * 64 + at];
+    const int j = (at >> 6) % NB, in = at / (64 * NB) * 16 + (at & 15);
+    const int rk = rank0 + 16 * j + 4 * ((at & 63) >> 4);
+    if (rk >= a.RP) continue;
+    const int slot = item * LM_ITEM + in, t = gld<int>(slots + in);
+    const bool here = t >= 0 && rk < R;
+    auto put = [&](f32x4 w, uint16_t* rows, uint16_t* cols) {
       LmPieces p[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) p[i] = lm_pieces(w[i]);
+      for (int i = 0; i < 4; ++i) p[i] = lm_pieces(here ? w[i] * s : 0.f);
 #pragma unroll
       for (int c = 0; c < 3; ++c) {
         if (rows != nullptr && t >= 0)
@@ -355,25 +440,13 @@ __global__ __launch_bounds__(64 * SH_W) void lm_shrink_kernel(LmShrink a) {
                           p[i].p[c]);
       }
     };
-    if (a.out != nullptr && t >= 0 && rk < R)
-      gst<f32x4>(a.out + static_cast<int64_t>(t) * R + rk, v);
+    if (a.out != nullptr && here) gst<f32x4>(a.out + static_cast<int64_t>(t) * R + rk, v);
     if (a.pieces != nullptr || a.pieces_t != nullptr) put(v, a.pieces, a.pieces_t);
     if (a.act != nullptr) {
-      const f32x4 w = t >= 0 && rk < R ? gld<f32x4>(a.act + static_cast<int64_t>(t) * R + rk)
-                                       : f32x4{0.f, 0.f, 0.f, 0.f};
+      f32x4 w = {0.f, 0.f, 0.f, 0.f};
+      if (here) w = gld<f32x4>(a.act + static_cast<int64_t>(t) * R + rk);
       put(w, nullptr, a.pieces_t2);
     }
-  }
-}
-
-// rows without an adapter have zeros for activations
-__global__ __launch_bounds__(256) void lm_zero_act_kernel(const int32_t* __restrict__ ids, int T,
-                                                          int L, int quads, float* act) {
-  const int64_t n = static_cast<int64_t>(T) * quads;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n;
-       i += static_cast<int64_t>(gridDim.x) * 256) {
-    const int id = gld<int32_t>(ids + i / quads);
-    if (id < 0 || id >= L) gst<f32x4>(act + i * 4, f32x4{0.f, 0.f, 0.f, 0.f});
   }
 }
 
@@ -738,6 +811,217 @@ __global__ __launch_bounds__(64 * WM * WN)
 }
 
 // ---------------------------------------------------------------------------
+// Few rows: no plan, two launches.
+//
+// dots: v[t, r] as it stands, a wavefront for RW ranks of a row, fp32 throughout.
+// ---------------------------------------------------------------------------
+struct LmFew {
+  const void* x;          // [T, k]
+  const void* w;          // [n, k]
+  const void* a;          // [L, R, k]
+  const void* b;          // [L, n, R]
+  const int32_t* ids;
+  const float* scale;
+  const void* bias;
+  float* v;               // [T, R] scaled
+  float* act;             // [T, R] or null
+  void* out;
+  int T, k, n, L, R;
+};
+
+template <bool F16>
+__device__ __forceinline__ void lm_unpack(u32x4 q, float (&o)[8]) {
+  if constexpr (F16) {
+    const f16x8 h = __builtin_bit_cast(f16x8, q);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = static_cast<float>(h[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      o[2 * i] = __uint_as_float(q[i] << 16);
+      o[2 * i + 1] = __uint_as_float(q[i] & 0xffff0000u);
+    }
+  }
+}
+
+template <bool F16, int RW>
+__global__ __launch_bounds__(256) void lm_dots_kernel(LmFew p) {
+  const int lane = threadIdx.x & 63, t = blockIdx.x;
+  const int r0 = (blockIdx.y * 4 + (threadIdx.x >> 6)) * RW;
+  if (r0 >= p.R) return;
+  const int l = gld<int32_t>(p.ids + t);
+  const bool none = l < 0 || l >= p.L;
+  float sum[RW];
+#pragma unroll
+  for (int i = 0; i < RW; ++i) sum[i] = 0.f;
+  if (!none) {
+    const uint16_t* const x = static_cast<const uint16_t*>(p.x) + static_cast<int64_t>(t) * p.k;
+    const uint16_t* const a = static_cast<const uint16_t*>(p.a) + (static_cast<int64_t>(l) * p.R + r0) * p.k;
+#pragma unroll 4
+    for (int c = lane * 8; c < p.k; c += 512) {
+      u32x4 qa[RW];
+      const u32x4 qx = gld<u32x4>(x + c);
+#pragma unroll
+      for (int i = 0; i < RW; ++i) qa[i] = gld<u32x4>(a + static_cast<int64_t>(i) * p.k + c);
+      float fx[8];
+      lm_unpack<F16>(qx, fx);
+#pragma unroll
+      for (int i = 0; i < RW; ++i) {
+        float fa[8];
+        lm_unpack<F16>(qa[i], fa);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[i] = __builtin_fmaf(fx[e], fa[e], sum[i]);
+      }
+    }
+  }
+  const float s = none ? 0.f : p.scale != nullptr ? gld<float>(p.scale + l) : 1.f;
+#pragma unroll
+  for (int i = 0; i < RW; ++i) {
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) sum[i] += __shfl_xor(sum[i], o, 64);
+    if (lane == 0) {
+      gst<float>(p.v + static_cast<int64_t>(t) * p.R + r0 + i, sum[i] * s);
+      if (p.act != nullptr) gst<float>(p.act + static_cast<int64_t>(t) * p.R + r0 + i, sum[i]);
+    }
+  }
+}
+
+// few: w streams from memory, so every wavefront loads it straight into MFMA operands
+// (no LDS, no barrier).  A workgroup has 16 FN columns of all rows (16 FM at most); its
+// NW wavefronts take the steps (64 of k) in turn.  Their sums are added in wavefront
+// order in LDS, and with them v B^T, which needs no MFMA: four columns of a row are R
+// fp32 fmas each, the adapter's part of them spread over the threads by 8 ranks.  The
+// first of those operands are loaded before the main loop.
+template <bool F16, int FM, int FN, int NW, typename OutT>
+__global__ __launch_bounds__(64 * NW) void lm_few_kernel(LmFew p) {
+  constexpr int BN = 16 * FN, Q = FM * FN * 64, PARTS = 64 * NW / Q;
+  static_assert(PARTS >= 1 && PARTS * Q == 64 * NW, "threads");
+  __shared__ __attribute__((aligned(16))) f32x4 red[NW * Q];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int k = p.k, n = p.n, R = p.R, KT = (k + LM_BK - 1) / LM_BK;
+  const int n0 = blockIdx.x * BN, cols = min(n - n0, BN);
+  // quad q: block (i, j) = q / 64, row 16 i + q % 16, columns 16 j + 4 ((q % 64) / 16) ..
+  const int quad = tid % Q, part = tid / Q;
+  const int row = quad / (64 * FN) * 16 + (quad & 15);
+  const int col = quad / 64 % FN * 16 + 4 * ((quad & 63) >> 4);
+  const bool in = row < p.T && col < cols;
+  const int l = row < p.T ? gld<int32_t>(p.ids + row) : -1;
+  const bool has = in && l >= 0 && l < p.L;
+  const uint16_t* const bank = static_cast<const uint16_t*>(p.b) + (static_cast<int64_t>(has ? l : 0) * n + n0 + col) * R;
+  const float* const v = p.v + static_cast<int64_t>(row) * R;
+  struct Ranks { u32x4 b[4]; f32x4 v[2]; };
+  auto ranks = [&](Ranks& q, int c) {  // ranks 8 c .. of the quad's four columns
+    if (!has || c * 8 >= R) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q.b[i] = gld<u32x4>(bank + i * R + c * 8);
+    q.v[0] = gld<f32x4>(v + c * 8);
+    q.v[1] = gld<f32x4>(v + c * 8 + 4);
+  };
+  Ranks first;
+  ranks(first, part);
+
+  const __amdgpu_buffer_rsrc_t xr = buf_rsrc(p.x, static_cast<uint32_t>(p.T) * k * 2u);
+  const __amdgpu_buffer_rsrc_t wr =
+      buf_rsrc(static_cast<const uint16_t*>(p.w) + static_cast<int64_t>(n0) * k, static_cast<uint32_t>(cols) * k * 2u);
+  uint32_t vx[FM], vw[FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+    vx[i] = 16 * i + r < p.T ? static_cast<uint32_t>(16 * i + r) * k * 2 + g * 16 : LM_OUT;
+#pragma unroll
+  for (int j = 0; j < FN; ++j)
+    vw[j] = 16 * j + r < cols ? static_cast<uint32_t>(16 * j + r) * k * 2 + g * 16 : LM_OUT;
+  f32x4 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  struct Step { u32x4 x[FM][2], w[FN][2]; };
+  auto load = [&](Step& q, int kt) {
+    const int kb = min(kt, KT - 1);
+    const uint32_t so = __builtin_amdgcn_readfirstlane(kb * (LM_BK * 2));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t drop = kt < KT && kb * LM_BK + 32 * h + 8 * g < k ? 0u : LM_OUT;
+#pragma unroll
+      for (int j = 0; j < FN; ++j) q.w[j][h] = buf_ld128(wr, (vw[j] + 64 * h) | drop, so);
+#pragma unroll
+      for (int i = 0; i < FM; ++i) q.x[i][h] = buf_ld128(xr, (vx[i] + 64 * h) | drop, so);
+    }
+  };
+  constexpr int P = 2;
+  Step q[P];
+#pragma unroll
+  for (int u = 0; u < P; ++u) {
+    load(q[u], wave + NW * u);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  for (int kt = wave; kt < KT; kt += NW * P) {
+#pragma unroll
+    for (int u = 0; u < P; ++u) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j) acc[i][j] = lm_mfma<F16>(q[u].w[j][h], q[u].x[i][h], acc[i][j]);
+      load(q[u], kt + NW * (u + P));
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) red[((wave * FM + i) * FN + j) * 64 + lane] = acc[i][j];
+  __syncthreads();
+  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int w = 0; w < NW / PARTS; ++w) sum += red[(part * (NW / PARTS) + w) * Q + quad];
+  if (has) {
+    auto add = [&](const Ranks& q) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float b[8];
+        lm_unpack<F16>(q.b[i], b);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[i] = __builtin_fmaf(q.v[e >> 2][e & 3], b[e], sum[i]);
+      }
+    };
+    if (part * 8 < R) add(first);
+    for (int c = part + PARTS; c * 8 < R; c += PARTS) {
+      Ranks next;
+      ranks(next, c);
+      add(next);
+    }
+  }
+  if constexpr (PARTS > 1) {
+    __syncthreads();
+    red[part * Q + quad] = sum;
+    __syncthreads();
+    if (part != 0) return;
+#pragma unroll
+    for (int w = 1; w < PARTS; ++w) sum += red[w * Q + quad];
+  }
+  if (!in) return;
+  if (p.bias != nullptr) {
+    const u32x2 raw = gld<u32x2>(static_cast<const uint16_t*>(p.bias) + n0 + col);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint16_t h = static_cast<uint16_t>(raw[c >> 1] >> (16 * (c & 1)));
+      sum[c] += F16 ? static_cast<float>(__builtin_bit_cast(_Float16, h)) : bf16_bits_to_f32(h);
+    }
+  }
+  OutT* const o = static_cast<OutT*>(p.out) + static_cast<int64_t>(row) * n + n0 + col;
+  if constexpr (sizeof(OutT) == 4) {
+    gst<f32x4>(o, sum);
+  } else {
+    typedef OutT t4 __attribute__((ext_vector_type(4)));
+    gst<u32x2>(o, __builtin_bit_cast(u32x2, __builtin_convertvector(sum, t4)));
+  }
+}
+
+// ---------------------------------------------------------------------------
 // grads: for a chunk of an adapter's rows, 128 columns of x (or go) and 16 NB ranks,
 //   ROWS == false: ga[l, r, c] = sum_t u[t, r] x[t, c]
 //   ROWS == true:  gb[l, c, r] = sum_t v[t, r] go[t, c]
@@ -890,11 +1174,11 @@ struct LmSizes {
     const int64_t most = fit < (1LL << 22) ? fit : 1LL << 22;
     return T < most ? T : most;
   }
-  static int64_t items(int64_t t, int64_t l) { return t / LM_ITEM + (l < t ? l : t) + 1; }
+  static int64_t items(int64_t t, int64_t l) { return t / LM_ITEM + (l + 1 < t ? l + 1 : t) + 1; }
   // items of a chunk: 512 rows, and no more than 32 chunks of a call's rows
   int64_t chunk_items() const {
-    const int64_t i = (T + 16 * 32 - 1) / (16 * 32);
-    return i < 32 ? 32 : i;
+    const int64_t i = (T + LM_ITEM * 32 - 1) / (LM_ITEM * 32);
+    return i < 512 / LM_ITEM ? 512 / LM_ITEM : i;
   }
   int64_t chunks() const { return L + items(T, L) / chunk_items() + 1; }
   // those of adapters that have several: each but an adapter's last is full
@@ -922,16 +1206,15 @@ struct LmSpace {
 LmSpace lm_space(const LmSizes& s, bool backward, void* base) {
   LmCarve c{static_cast<uint8_t*>(base)};
   LmSpace o{};
-  const int64_t items = LmSizes::items(s.T, s.L), wide = s.N > s.K ? s.N : s.K;
+  const int64_t items = LmSizes::items(s.T, s.L);
   o.plan.order = c.take<i32x2>(s.T);
   o.plan.seg = c.take<int>(s.L + 1);
-  o.plan.items = c.take<i32x4>(items);
+  o.plan.item_id = c.take<int>(items);
   o.plan.slot_row = c.take<int>(items * LM_ITEM);
   o.plan.chunks = c.take<i32x4>(s.chunks());
   o.plan.spans = c.take<i32x4>(s.L);
-  o.plan.totals = c.take<int>(2);
+  o.plan.totals = c.take<int>(4);
   o.plan.zeros = c.take<uint16_t>(8);
-  (void)wide;
   o.pieces = c.take<uint16_t>(s.T * 3 * s.rp());
   if (backward) {
     o.ut = c.take<uint16_t>(items * LM_ITEM * 3 * s.rp());
@@ -962,7 +1245,7 @@ mi_status lm_check(const char* what, const LmSizes& s, mi_dtype dt) {
 mi_status lm_plan(const LmSizes& s, int64_t rows, const int32_t* ids, const LmPlan& p, hipStream_t st) {
   hipLaunchKernelGGL(lm_plan_kernel, dim3(1), dim3(PL_T),
                      0, st, ids, static_cast<int>(rows),
-                     static_cast<int>(s.L), static_cast<int>(s.chunk_items()), 1, p);
+                     static_cast<int>(s.L), static_cast<int>(s.chunk_items()), p);
   return launch_status("mm_lora (plan)");
 }
 
@@ -995,6 +1278,26 @@ mi_status lm_mm(const LmMm& a, hipStream_t st) {
   if (tiles(64, 64) <= 512) return lm_mm_launch<F16, BT, 2, 2, 2, 2, 4, OutT>(a, st);
   if (tiles(128, 128) > 512) return lm_mm_launch<F16, BT, 2, 4, 8, 4, 2, OutT>(a, st);
   return lm_mm_launch<F16, BT, 2, 2, 4, 4, 2, OutT>(a, st);
+}
+
+template <bool F16, typename OutT>
+mi_status lm_few(const LmFew& p, hipStream_t st) {
+  const unsigned T = static_cast<unsigned>(p.T), R = static_cast<unsigned>(p.R);
+  if (T * R <= 2048)
+    hipLaunchKernelGGL((lm_dots_kernel<F16, 1>), dim3(T, R / 4), dim3(256), 0, st, p);
+  else
+    hipLaunchKernelGGL((lm_dots_kernel<F16, 4>), dim3(T, (R + 15) / 16), dim3(256), 0, st, p);
+  const mi_status one = launch_status("mm_lora (dots)");
+  if (one != MI_OK) return one;
+#define LM_FEW(FM_, FN_)                                                                     \
+  hipLaunchKernelGGL((lm_few_kernel<F16, FM_, FN_, 8, OutT>),                                \
+                     dim3(static_cast<unsigned>((p.n + 16 * FN_ - 1) / (16 * FN_))), dim3(512), 0, st, p)
+  const bool wide = p.n > 16 * 256;
+  if (p.T <= 16) { if (wide) LM_FEW(1, 2); else LM_FEW(1, 1); }
+  else if (p.T <= 32) { if (wide) LM_FEW(2, 2); else LM_FEW(2, 1); }
+  else { if (wide) LM_FEW(4, 2); else LM_FEW(4, 1); }
+#undef LM_FEW
+  return launch_status("mm_lora (few rows)");
 }
 
 }  // namespace
@@ -1046,13 +1349,12 @@ extern "C" mi_status mi_mm_lora(const void* x, int64_t m, int64_t k, mi_dtype dt
              "%s: the workspace needs %zu bytes, aligned to 256 (got %zu)", what, sp.bytes, workspace_bytes);
   hipStream_t hs = static_cast<hipStream_t>(stream);
   const int64_t es = out_dtype == MI_F32 ? 4 : 2;
-  if (act != nullptr) {
-    const int64_t quads = m * (rank / 4), blocks = (quads + 255) / 256;
-    hipLaunchKernelGGL(lm_zero_act_kernel, dim3(static_cast<unsigned>(blocks < 2048 ? blocks : 2048)),
-                       dim3(256), 0, hs, lora_ids, static_cast<int>(m), static_cast<int>(num_adapters),
-                       static_cast<int>(rank / 4), act);
-    st = launch_status("mm_lora (activations)");
-    if (st != MI_OK) return st;
+  if (m <= LM_FEW_ROWS) {
+    LmFew p{x, w, lora_a, lora_b, lora_ids, lora_scale, bias, reinterpret_cast<float*>(sp.pieces), act, out,
+            static_cast<int>(m), static_cast<int>(k), static_cast<int>(n),
+            static_cast<int>(num_adapters), static_cast<int>(rank)};
+    return dtype == MI_F16 ? (es == 4 ? lm_few<true, float>(p, hs) : lm_few<true, _Float16>(p, hs))
+                           : (es == 4 ? lm_few<false, float>(p, hs) : lm_few<false, __bf16>(p, hs));
   }
   for (int64_t t0 = 0; t0 < m; t0 += s.pass()) {
     const int64_t rows = m - t0 < s.pass() ? m - t0 : s.pass();
@@ -1143,7 +1445,7 @@ extern "C" mi_status mi_mm_lora_backward(const void* grad_out, const void* x, in
              "%s: the workspace needs %zu bytes, aligned to 256 (got %zu)", what, sp.bytes, workspace_bytes);
   hipStream_t hs = static_cast<hipStream_t>(stream);
   const bool f16 = dtype == MI_F16, several = s.pass() < m;
-  auto shrink = [&](int64_t t0, int64_t rows) {
+  auto shrink = [&](int64_t rows) {
     LmShrink a{};
     a.scale = lora_scale;
     a.plan = sp.plan;
@@ -1151,7 +1453,6 @@ extern "C" mi_status mi_mm_lora_backward(const void* grad_out, const void* x, in
     a.L = static_cast<int>(num_adapters);
     a.R = static_cast<int>(rank);
     a.RP = static_cast<int>(s.rp());
-    (void)t0;
     return a;
   };
   MI_REQUIRE_SUPPORTED(!several || !banks,
@@ -1168,7 +1469,7 @@ extern "C" mi_status mi_mm_lora_backward(const void* grad_out, const void* x, in
     const int64_t items = LmSizes::items(rows, num_adapters);
     const float* v = act;
     if (banks && act == nullptr) {
-      LmShrink a = shrink(t0, rows);
+      LmShrink a = shrink(rows);
       a.x = x;
       a.bank = lora_a;
       a.C = static_cast<int>(k);
@@ -1177,7 +1478,7 @@ extern "C" mi_status mi_mm_lora_backward(const void* grad_out, const void* x, in
       if (st != MI_OK) return st;
       v = sp.act;
     }
-    LmShrink a = shrink(t0, rows);
+    LmShrink a = shrink(rows);
     a.x = static_cast<const uint16_t*>(grad_out) + t0 * n;
     a.bank = lora_b;
     a.C = static_cast<int>(n);
