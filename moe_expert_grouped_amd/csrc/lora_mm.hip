@@ -488,17 +488,17 @@ __device__ __forceinline__ void lm_wait_barrier() {
 
 // Where a tile lies in the call: m-tiles in groups of GM sweep the n-panels together,
 // and each XCD has a contiguous run of that order (workgroup ids go to the 8 in turn).
-struct LmPlace { int m0, n0, rows, cols; };
+struct LmPlace { int m0, n0, rows, cols, k0, steps; };
 template <int BM, int BN>
 __device__ __forceinline__ LmPlace lm_place(const LmMm& p) {
   const int nt = (p.n + BN - 1) / BN, mt = (p.T + BM - 1) / BM;
   const int total = nt * mt, per = (total + 7) / 8;
   const int slot = blockIdx.x >> 3, tile = (blockIdx.x & 7) * per + slot;
-  if (slot >= per || tile >= total) return {0, 0, 0, 0};
+  if (slot >= per || tile >= total) return {0, 0, 0, 0, 0, 0};
   constexpr int GM = BM >= 256 ? 4 : 8;
   const int grp = tile / (GM * nt), in = tile - grp * GM * nt, gsz = min(mt - grp * GM, GM);
   const int m0 = (grp * GM + in % gsz) * BM, n0 = in / gsz * BN;
-  return {m0, n0, min(p.T - m0, BM), min(p.n - n0, BN)};
+  return {m0, n0, min(p.T - m0, BM), min(p.n - n0, BN), 0, (p.k + LM_BK - 1) / LM_BK};
 }
 
 // One tile of BM = 16 FM WM rows and BN = 16 FN WN columns; WM * WN wavefronts of
@@ -514,7 +514,9 @@ __device__ __forceinline__ LmPlace lm_place(const LmMm& p) {
 // barrier stands before its last two regions, whose operands are in registers by then:
 // behind it the stage is free for the loads of step kt + NST and the next stage is
 // complete, so the last regions read the next step's first fragments.
-template <bool F16, bool BT, int WM, int WN, int FM, int FN, int NST, typename OutT>
+//
+// PART: only the steps [t.k0, t.k0 + t.steps), rows in their own order, no adapters.
+template <bool F16, bool BT, bool PART, int WM, int WN, int FM, int FN, int NST, typename OutT>
 __device__ __forceinline__ void lm_tile(const LmMm& p, const LmPlace& t, uint8_t* s0, uint8_t* s1,
                                         uint8_t* s2, uint8_t* s3, i32x2* s_order) {
   constexpr int NW = WM * WN, BM = 16 * FM * WM, BN = 16 * FN * WN;
@@ -527,11 +529,11 @@ __device__ __forceinline__ void lm_tile(const LmMm& p, const LmPlace& t, uint8_t
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
   const int r = lane & 15, g = lane >> 4;
-  const int k = p.k, n = p.n, KT = (k + LM_BK - 1) / LM_BK;
+  const int k = p.k, n = p.n, k0 = t.k0, KT = t.steps, last = (k + LM_BK - 1) / LM_BK - 1;
   const int m0 = t.m0, n0 = t.n0, rows = t.rows, cols = t.cols;
 
   for (int i = tid; i < BM; i += 64 * NW)
-    s_order[i] = i < rows ? gld<i32x2>(p.plan.order + m0 + i) : i32x2{-1, p.L};
+    s_order[i] = i >= rows ? i32x2{-1, p.L} : PART ? i32x2{m0 + i, p.L} : gld<i32x2>(p.plan.order + m0 + i);
   __syncthreads();
 
   const __amdgpu_buffer_rsrc_t ar =
@@ -558,12 +560,12 @@ __device__ __forceinline__ void lm_tile(const LmMm& p, const LmPlace& t, uint8_t
       vb[i] = col < cols ? (static_cast<uint32_t>(row) * n + n0 + col) * 2 : LM_OUT;
     }
   }
-  const uint32_t tail = (KT - 1) * LM_BK + chunk * 8 < k ? 0u : LM_OUT;
+  const uint32_t tail = last * LM_BK + chunk * 8 < k ? 0u : LM_OUT;
   // Pieces [first, first + count) of the NI loads of a stage.  A step past the last
   // loads zeros: the steps stay free of branches.
   auto dma = [&](uint8_t* st, int kt, int first, int count) {
-    const int kb = min(kt, KT - 1);
-    const uint32_t drop = kt >= KT ? LM_OUT : 0u, dropa = kt == KT - 1 ? tail : drop;
+    const int kb = k0 + min(kt, KT - 1);
+    const uint32_t drop = kt >= KT ? LM_OUT : 0u, dropa = kb == last ? drop | tail : drop;
     const uint32_t so = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(kb) * (LM_BK * 2));
     const uint32_t sob =
         BT ? __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(kb) * (LM_BK * 2) * n) : so;
@@ -682,7 +684,7 @@ __device__ __forceinline__ void lm_tile(const LmMm& p, const LmPlace& t, uint8_t
     row_at[i] = o.x;
     id_at[i] = o.y;
   }
-  for (int at = 0; at < rows;) {
+  for (int at = PART ? rows : 0; at < rows;) {
     const int l = __builtin_amdgcn_readfirstlane(s_order[at].y);
     if (l >= p.L) break;  // the rows without an adapter are last
     const int end = max(min(gld<int>(p.plan.seg + l + 1) - m0, rows), at + 1);
@@ -807,26 +809,36 @@ __global__ __launch_bounds__(64 * WM * WN)
   __shared__ i32x2 s_order[BM];
   const LmPlace t = lm_place<BM, BN>(p);
   if (t.rows == 0) return;
-  lm_tile<F16, BT, WM, WN, FM, FN, NST, OutT>(p, t, s0, s1, s2, s3, s_order);
+  lm_tile<F16, BT, false, WM, WN, FM, FN, NST, OutT>(p, t, s0, s1, s2, s3, s_order);
 }
 
 // ---------------------------------------------------------------------------
-// Few rows: no plan, two launches.
+// Few rows: no plan, and two launches.
 //
-// dots: v[t, r] as it stands, a wavefront for RW ranks of a row, fp32 throughout.
+//   parts   the dense product's 64 x 64 tiles, split along k until they fill the chip,
+//           into fp32 partial sums; beside them, in workgroups of the same launch, v
+//           (or u) in fp32 as it stands, a wavefront for some ranks of a row
+//   finish  four columns of a row: the partial sums in order, the bias, and R fp32
+//           fmas for the adapter; in the backward pass, workgroups of the same
+//           launch sum gA and gB over the rows, which are few
 // ---------------------------------------------------------------------------
-struct LmFew {
-  const void* x;          // [T, k]
-  const void* w;          // [n, k]
-  const void* a;          // [L, R, k]
-  const void* b;          // [L, n, R]
+struct LmSmall {
+  LmMm mm;                // w, x of the dense product; out: the partial sums [S, T, n]
+  const void* x;          // [T, ca] rows that meet a (dots)
+  const void* go;         // [T, cb] rows that meet b (backward)
+  const void* a;          // [L, R, ca]
+  const void* b;          // [L, cb, R]
   const int32_t* ids;
   const float* scale;
+  const float* act_in;    // backward: the forward's act, or null
+  float* v;               // [T, R] x a^T (backward: where act_in is null)
+  float* u;               // [T, R] go b (backward)
+  float* act;             // forward: v goes here too, or null
   const void* bias;
-  float* v;               // [T, R] scaled
-  float* act;             // [T, R] or null
-  void* out;
-  int T, k, n, L, R;
+  void* out;              // [T, mm.n]
+  void *ga, *gb;          // backward, or null
+  int T, ca, cb, L, R;
+  int splits, tiles, gemm, dots, fin;  // workgroups
 };
 
 template <bool F16>
@@ -843,30 +855,35 @@ __device__ __forceinline__ void lm_unpack(u32x4 q, float (&o)[8]) {
     }
   }
 }
-
-template <bool F16, int RW>
-__global__ __launch_bounds__(256) void lm_dots_kernel(LmFew p) {
-  const int lane = threadIdx.x & 63, t = blockIdx.x;
-  const int r0 = (blockIdx.y * 4 + (threadIdx.x >> 6)) * RW;
-  if (r0 >= p.R) return;
-  const int l = gld<int32_t>(p.ids + t);
-  const bool none = l < 0 || l >= p.L;
-  float sum[RW];
+template <bool F16>
+__device__ __forceinline__ float lm_half(uint16_t h) {
+  return F16 ? static_cast<float>(__builtin_bit_cast(_Float16, h)) : bf16_bits_to_f32(h);
+}
+__device__ __forceinline__ float lm_wave_sum(float v) {
 #pragma unroll
-  for (int i = 0; i < RW; ++i) sum[i] = 0.f;
+  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+
+// ranks r0 .. r0 + 3 of x[t] a[l]^T
+template <bool F16>
+__device__ __forceinline__ void lm_dot_a(const LmSmall& p, int t, int r0) {
+  const int lane = threadIdx.x & 63, l = gld<int32_t>(p.ids + t), k = p.ca;
+  const bool none = l < 0 || l >= p.L;
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
   if (!none) {
-    const uint16_t* const x = static_cast<const uint16_t*>(p.x) + static_cast<int64_t>(t) * p.k;
-    const uint16_t* const a = static_cast<const uint16_t*>(p.a) + (static_cast<int64_t>(l) * p.R + r0) * p.k;
+    const uint16_t* const x = static_cast<const uint16_t*>(p.x) + static_cast<int64_t>(t) * k;
+    const uint16_t* const a = static_cast<const uint16_t*>(p.a) + (static_cast<int64_t>(l) * p.R + r0) * k;
 #pragma unroll 4
-    for (int c = lane * 8; c < p.k; c += 512) {
-      u32x4 qa[RW];
+    for (int c = lane * 8; c < k; c += 512) {
+      u32x4 qa[4];
       const u32x4 qx = gld<u32x4>(x + c);
 #pragma unroll
-      for (int i = 0; i < RW; ++i) qa[i] = gld<u32x4>(a + static_cast<int64_t>(i) * p.k + c);
+      for (int i = 0; i < 4; ++i) qa[i] = gld<u32x4>(a + static_cast<int64_t>(i) * k + c);
       float fx[8];
       lm_unpack<F16>(qx, fx);
 #pragma unroll
-      for (int i = 0; i < RW; ++i) {
+      for (int i = 0; i < 4; ++i) {
         float fa[8];
         lm_unpack<F16>(qa[i], fa);
 #pragma unroll
@@ -874,145 +891,180 @@ __global__ __launch_bounds__(256) void lm_dots_kernel(LmFew p) {
       }
     }
   }
-  const float s = none ? 0.f : p.scale != nullptr ? gld<float>(p.scale + l) : 1.f;
 #pragma unroll
-  for (int i = 0; i < RW; ++i) {
+  for (int i = 0; i < 4; ++i) sum[i] = lm_wave_sum(sum[i]);
+  if (lane == 0) {
+    const f32x4 v = {sum[0], sum[1], sum[2], sum[3]};
+    const int64_t at = static_cast<int64_t>(t) * p.R + r0;
+    gst<f32x4>(p.v + at, v);
+    if (p.act != nullptr) gst<f32x4>(p.act + at, v);
+  }
+}
+
+// ranks r0 .. r0 + 7 of go[t] b[l]: a lane has its own rows of b
+template <bool F16>
+__device__ __forceinline__ void lm_dot_b(const LmSmall& p, int t, int r0) {
+  const int lane = threadIdx.x & 63, l = gld<int32_t>(p.ids + t);
+  const bool none = l < 0 || l >= p.L;
+  float sum[8] = {};
+  if (!none) {
+    const uint16_t* const go = static_cast<const uint16_t*>(p.go) + static_cast<int64_t>(t) * p.cb;
+    const uint16_t* const b = static_cast<const uint16_t*>(p.b) + static_cast<int64_t>(l) * p.cb * p.R + r0;
+#pragma unroll 8
+    for (int c = lane; c < p.cb; c += 64) {
+      const uint16_t h = gld<uint16_t>(go + c);
+      float fb[8];
+      lm_unpack<F16>(gld<u32x4>(b + static_cast<int64_t>(c) * p.R), fb);
+      const float f = lm_half<F16>(h);
 #pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) sum[i] += __shfl_xor(sum[i], o, 64);
-    if (lane == 0) {
-      gst<float>(p.v + static_cast<int64_t>(t) * p.R + r0 + i, sum[i] * s);
-      if (p.act != nullptr) gst<float>(p.act + static_cast<int64_t>(t) * p.R + r0 + i, sum[i]);
+      for (int e = 0; e < 8; ++e) sum[e] = __builtin_fmaf(f, fb[e], sum[e]);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sum[e] = lm_wave_sum(sum[e]);
+  if (lane == 0) {
+    float* const at = p.u + static_cast<int64_t>(t) * p.R + r0;
+    gst<f32x4>(at, f32x4{sum[0], sum[1], sum[2], sum[3]});
+    gst<f32x4>(at + 4, f32x4{sum[4], sum[5], sum[6], sum[7]});
+  }
+}
+
+template <bool F16, bool BT>
+__global__ __launch_bounds__(256) void lm_parts_kernel(LmSmall p) {
+  constexpr int STAGE = 128 * 128;
+  __shared__ __attribute__((aligned(16))) uint8_t s0[STAGE], s1[STAGE], s2[STAGE], s3[STAGE];
+  __shared__ i32x2 s_order[64];
+  const int block = blockIdx.x;
+  if (block < p.gemm) {
+    const int split = block / p.tiles, tile = block % p.tiles;
+    const int mt = (p.T + 63) / 64, all = (p.mm.k + LM_BK - 1) / LM_BK;
+    const int k0 = all * split / p.splits, k1 = all * (split + 1) / p.splits;
+    LmMm mm = p.mm;
+    mm.out = static_cast<float*>(p.mm.out) + static_cast<int64_t>(split) * p.T * mm.n;
+    const int m0 = tile % mt * 64, n0 = tile / mt * 64;
+    lm_tile<F16, BT, true, 2, 2, 2, 2, 4, float>(
+        mm, {m0, n0, min(p.T - m0, 64), min(mm.n - n0, 64), k0, k1 - k0}, s0, s1, s2, s3, s_order);
+    return;
+  }
+  const int wave = (block - p.gemm) * 4 + (threadIdx.x >> 6), waves = p.dots * 4;
+  // backward: u first, then v where it is not given
+  const int nu = p.u != nullptr ? p.T * (p.R / 8) : 0, nv = p.v != nullptr ? p.T * (p.R / 4) : 0;
+  for (int i = wave; i < nu + nv; i += waves) {
+    if (i < nu) lm_dot_b<F16>(p, i / (p.R / 8), i % (p.R / 8) * 8);
+    else lm_dot_a<F16>(p, (i - nu) / (p.R / 4), (i - nu) % (p.R / 4) * 4);
+  }
+}
+
+// gA: 8 ranks and 2048 columns of x of an adapter, a thread 8 x 8 of them (OTHER: gB)
+template <bool F16, bool OTHER, typename OutT>
+__device__ __forceinline__ void lm_small_grad(const LmSmall& p, int l, int r0, int c0) {
+  const int C = OTHER ? p.cb : p.ca, at_c = c0 + threadIdx.x * 8, c = min(at_c, C - 8);
+  const uint16_t* const x = static_cast<const uint16_t*>(OTHER ? p.go : p.x) + c;
+  const float* const f = (OTHER ? (p.act_in != nullptr ? p.act_in : p.v) : p.u) + r0;
+  f32x4 acc[8][2];  // [rank][columns], OTHER: [column][ranks]
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // the adapter's rows among 64 at a time
+  uint64_t own = 0;
+  for (int t = 0, t0 = -64;;) {
+    while (own == 0 && (t0 += 64) < p.T) {
+      const int at = t0 + (threadIdx.x & 63);
+      own = __ballot(at < p.T && gld<int32_t>(p.ids + min(at, p.T - 1)) == l);
+    }
+    if (own == 0) break;
+    t = t0 + __builtin_ctzll(own);
+    own &= own - 1;
+    float xs[8];
+    lm_unpack<F16>(gld<u32x4>(x + static_cast<int64_t>(t) * C), xs);
+    const f32x4 f0 = gld<f32x4>(f + static_cast<int64_t>(t) * p.R), f1 = gld<f32x4>(f + static_cast<int64_t>(t) * p.R + 4);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float rank = (OTHER ? e : i) < 4 ? f0[(OTHER ? e : i) & 3] : f1[(OTHER ? e : i) & 3];
+        acc[i][e >> 2][e & 3] = __builtin_fmaf(rank, xs[OTHER ? i : e], acc[i][e >> 2][e & 3]);
+      }
+  }
+  if (at_c >= C) return;
+  const float s = p.scale != nullptr ? gld<float>(p.scale + l) : 1.f;
+  OutT* const out = static_cast<OutT*>(OTHER ? p.gb : p.ga) + static_cast<int64_t>(l) * p.R * C;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    OutT* const at = OTHER ? out + static_cast<int64_t>(c + i) * p.R + r0 : out + static_cast<int64_t>(r0 + i) * C + c;
+    if constexpr (sizeof(OutT) == 4) {
+      gst<f32x4>(at, acc[i][0] * s);
+      gst<f32x4>(at + 4, acc[i][1] * s);
+    } else {
+      typedef OutT t8 __attribute__((ext_vector_type(8)));
+      t8 o;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = static_cast<OutT>(acc[i][e >> 2][e & 3] * s);
+      gst<u32x4>(at, __builtin_bit_cast(u32x4, o));
     }
   }
 }
 
-// few: w streams from memory, so every wavefront loads it straight into MFMA operands
-// (no LDS, no barrier).  A workgroup has 16 FN columns of all rows (16 FM at most); its
-// NW wavefronts take the steps (64 of k) in turn.  Their sums are added in wavefront
-// order in LDS, and with them v B^T, which needs no MFMA: four columns of a row are R
-// fp32 fmas each, the adapter's part of them spread over the threads by 8 ranks.  The
-// first of those operands are loaded before the main loop.
-template <bool F16, int FM, int FN, int NW, typename OutT>
-__global__ __launch_bounds__(64 * NW) void lm_few_kernel(LmFew p) {
-  constexpr int BN = 16 * FN, Q = FM * FN * 64, PARTS = 64 * NW / Q;
-  static_assert(PARTS >= 1 && PARTS * Q == 64 * NW, "threads");
-  __shared__ __attribute__((aligned(16))) f32x4 red[NW * Q];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int r = lane & 15, g = lane >> 4;
-  const int k = p.k, n = p.n, R = p.R, KT = (k + LM_BK - 1) / LM_BK;
-  const int n0 = blockIdx.x * BN, cols = min(n - n0, BN);
-  // quad q: block (i, j) = q / 64, row 16 i + q % 16, columns 16 j + 4 ((q % 64) / 16) ..
-  const int quad = tid % Q, part = tid / Q;
-  const int row = quad / (64 * FN) * 16 + (quad & 15);
-  const int col = quad / 64 % FN * 16 + 4 * ((quad & 63) >> 4);
-  const bool in = row < p.T && col < cols;
-  const int l = row < p.T ? gld<int32_t>(p.ids + row) : -1;
-  const bool has = in && l >= 0 && l < p.L;
-  const uint16_t* const bank = static_cast<const uint16_t*>(p.b) + (static_cast<int64_t>(has ? l : 0) * n + n0 + col) * R;
-  const float* const v = p.v + static_cast<int64_t>(row) * R;
-  struct Ranks { u32x4 b[4]; f32x4 v[2]; };
-  auto ranks = [&](Ranks& q, int c) {  // ranks 8 c .. of the quad's four columns
-    if (!has || c * 8 >= R) return;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) q.b[i] = gld<u32x4>(bank + i * R + c * 8);
-    q.v[0] = gld<f32x4>(v + c * 8);
-    q.v[1] = gld<f32x4>(v + c * 8 + 4);
-  };
-  Ranks first;
-  ranks(first, part);
-
-  const __amdgpu_buffer_rsrc_t xr = buf_rsrc(p.x, static_cast<uint32_t>(p.T) * k * 2u);
-  const __amdgpu_buffer_rsrc_t wr =
-      buf_rsrc(static_cast<const uint16_t*>(p.w) + static_cast<int64_t>(n0) * k, static_cast<uint32_t>(cols) * k * 2u);
-  uint32_t vx[FM], vw[FN];
-#pragma unroll
-  for (int i = 0; i < FM; ++i)
-    vx[i] = 16 * i + r < p.T ? static_cast<uint32_t>(16 * i + r) * k * 2 + g * 16 : LM_OUT;
-#pragma unroll
-  for (int j = 0; j < FN; ++j)
-    vw[j] = 16 * j + r < cols ? static_cast<uint32_t>(16 * j + r) * k * 2 + g * 16 : LM_OUT;
-  f32x4 acc[FM][FN];
-#pragma unroll
-  for (int i = 0; i < FM; ++i)
-#pragma unroll
-    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  struct Step { u32x4 x[FM][2], w[FN][2]; };
-  auto load = [&](Step& q, int kt) {
-    const int kb = min(kt, KT - 1);
-    const uint32_t so = __builtin_amdgcn_readfirstlane(kb * (LM_BK * 2));
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t drop = kt < KT && kb * LM_BK + 32 * h + 8 * g < k ? 0u : LM_OUT;
-#pragma unroll
-      for (int j = 0; j < FN; ++j) q.w[j][h] = buf_ld128(wr, (vw[j] + 64 * h) | drop, so);
-#pragma unroll
-      for (int i = 0; i < FM; ++i) q.x[i][h] = buf_ld128(xr, (vx[i] + 64 * h) | drop, so);
-    }
-  };
-  constexpr int P = 2;
-  Step q[P];
-#pragma unroll
-  for (int u = 0; u < P; ++u) {
-    load(q[u], wave + NW * u);
-    __builtin_amdgcn_sched_barrier(0);
-  }
-  for (int kt = wave; kt < KT; kt += NW * P) {
-#pragma unroll
-    for (int u = 0; u < P; ++u) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < FM; ++i)
-#pragma unroll
-          for (int j = 0; j < FN; ++j) acc[i][j] = lm_mfma<F16>(q[u].w[j][h], q[u].x[i][h], acc[i][j]);
-      load(q[u], kt + NW * (u + P));
-      __builtin_amdgcn_sched_barrier(0);
+// BT (backward): the adapter's part is s u a, else s v b^T
+template <bool F16, bool BT, typename OutT, typename GradT>
+__global__ __launch_bounds__(256) void lm_finish_kernel(LmSmall p) {
+  const int n = p.mm.n, R = p.R;
+  if constexpr (BT) {
+    if (static_cast<int>(blockIdx.x) >= p.fin) {
+      const int pa = (p.ca + 2047) / 2048, pb = (p.cb + 2047) / 2048, r8 = R / 8;
+      int i = blockIdx.x - p.fin;
+      const int panel = i % (pa + pb);
+      i /= pa + pb;
+      if (panel < pa) lm_small_grad<F16, false, GradT>(p, i / r8, i % r8 * 8, panel * 2048);
+      else lm_small_grad<F16, true, GradT>(p, i / r8, i % r8 * 8, (panel - pa) * 2048);
+      return;
     }
   }
-#pragma unroll
-  for (int i = 0; i < FM; ++i)
-#pragma unroll
-    for (int j = 0; j < FN; ++j) red[((wave * FM + i) * FN + j) * 64 + lane] = acc[i][j];
-  __syncthreads();
-  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int w = 0; w < NW / PARTS; ++w) sum += red[(part * (NW / PARTS) + w) * Q + quad];
+  const uint32_t quad = blockIdx.x * 256 + threadIdx.x, per = n / 4;
+  const int t = quad / per, c = quad % per * 4;
+  if (t >= p.T) return;
+  const int l = gld<int32_t>(p.ids + t);
+  const bool has = l >= 0 && l < p.L;
+  const float* const parts = static_cast<const float*>(p.mm.out) + static_cast<int64_t>(t) * n + c;
+  f32x4 sum = gld<f32x4>(parts);
+#pragma unroll 4
+  for (int i = 1; i < p.splits; ++i) sum += gld<f32x4>(parts + static_cast<int64_t>(i) * p.T * n);
   if (has) {
-    auto add = [&](const Ranks& q) {
+    const float* const f = (BT ? p.u : p.v) + static_cast<int64_t>(t) * R;
+    f32x4 d = {0.f, 0.f, 0.f, 0.f};
+    if constexpr (BT) {
+      const uint16_t* const bank = static_cast<const uint16_t*>(p.a) + static_cast<int64_t>(l) * R * n + c;
+#pragma unroll 8
+      for (int r = 0; r < R; ++r) {
+        const u32x2 q = gld<u32x2>(bank + static_cast<int64_t>(r) * n);
+        const float u = gld<float>(f + r);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float b[8];
-        lm_unpack<F16>(q.b[i], b);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum[i] = __builtin_fmaf(q.v[e >> 2][e & 3], b[e], sum[i]);
+        for (int e = 0; e < 4; ++e)
+          d[e] = __builtin_fmaf(u, lm_half<F16>(static_cast<uint16_t>(q[e >> 1] >> (16 * (e & 1)))), d[e]);
       }
-    };
-    if (part * 8 < R) add(first);
-    for (int c = part + PARTS; c * 8 < R; c += PARTS) {
-      Ranks next;
-      ranks(next, c);
-      add(next);
-    }
-  }
-  if constexpr (PARTS > 1) {
-    __syncthreads();
-    red[part * Q + quad] = sum;
-    __syncthreads();
-    if (part != 0) return;
+    } else {
+      const uint16_t* const bank = static_cast<const uint16_t*>(p.b) + (static_cast<int64_t>(l) * n + c) * R;
+#pragma unroll 2
+      for (int r = 0; r < R; r += 8) {
+        const f32x4 f0 = gld<f32x4>(f + r), f1 = gld<f32x4>(f + r + 4);
 #pragma unroll
-    for (int w = 1; w < PARTS; ++w) sum += red[w * Q + quad];
+        for (int e = 0; e < 4; ++e) {
+          float b[8];
+          lm_unpack<F16>(gld<u32x4>(bank + static_cast<int64_t>(e) * R + r), b);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) d[e] = __builtin_fmaf(i < 4 ? f0[i & 3] : f1[i & 3], b[i], d[e]);
+        }
+      }
+    }
+    const float s = p.scale != nullptr ? gld<float>(p.scale + l) : 1.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] = __builtin_fmaf(s, d[e], sum[e]);
   }
-  if (!in) return;
   if (p.bias != nullptr) {
-    const u32x2 raw = gld<u32x2>(static_cast<const uint16_t*>(p.bias) + n0 + col);
+    const u32x2 q = gld<u32x2>(static_cast<const uint16_t*>(p.bias) + c);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const uint16_t h = static_cast<uint16_t>(raw[c >> 1] >> (16 * (c & 1)));
-      sum[c] += F16 ? static_cast<float>(__builtin_bit_cast(_Float16, h)) : bf16_bits_to_f32(h);
-    }
+    for (int e = 0; e < 4; ++e) sum[e] += lm_half<F16>(static_cast<uint16_t>(q[e >> 1] >> (16 * (e & 1))));
   }
-  OutT* const o = static_cast<OutT*>(p.out) + static_cast<int64_t>(row) * n + n0 + col;
+  OutT* const o = static_cast<OutT*>(p.out) + static_cast<int64_t>(t) * n + c;
   if constexpr (sizeof(OutT) == 4) {
     gst<f32x4>(o, sum);
   } else {
@@ -1185,6 +1237,17 @@ struct LmSizes {
   int64_t places() const { return 2 * (items(T, L) / chunk_items()) + 2; }
 };
 
+// Splits of the k axis of few rows' tiles: 64 x 64 tiles on 256 CUs, 8 steps each at least.
+int lm_splits(int64_t T, int64_t n, int64_t k) {
+  const int64_t tiles = (T + 63) / 64 * ((n + 63) / 64), steps = (k + LM_BK - 1) / LM_BK;
+  int64_t s = 256 / tiles;
+  if (s > steps / 8) s = steps / 8;
+  return static_cast<int>(s < 1 ? 1 : s);
+}
+
+// Few rows: where the dots' reads of the banks, from the L2s, stay small beside the rest
+bool lm_small(const LmSizes& s) { return s.T <= LM_FEW_ROWS; }
+
 struct LmCarve {
   uint8_t* at;
   size_t used = 0;
@@ -1200,12 +1263,20 @@ struct LmSpace {
   LmPlan plan;
   uint16_t *pieces, *ut, *vt;
   float *act, *part_a, *part_b;
+  float *v, *u, *parts;  // few rows
   size_t bytes;
 };
 
 LmSpace lm_space(const LmSizes& s, bool backward, void* base) {
   LmCarve c{static_cast<uint8_t*>(base)};
   LmSpace o{};
+  if (s.T > 0 && lm_small(s)) {
+    o.v = c.take<float>(s.T * s.R);
+    o.u = c.take<float>(backward ? s.T * s.R : 0);
+    o.parts = c.take<float>(s.T * (backward ? lm_splits(s.T, s.K, s.N) * s.K : lm_splits(s.T, s.N, s.K) * s.N));
+    o.bytes = c.used;
+    return o;
+  }
   const int64_t items = LmSizes::items(s.T, s.L);
   o.plan.order = c.take<i32x2>(s.T);
   o.plan.seg = c.take<int>(s.L + 1);
@@ -1280,24 +1351,22 @@ mi_status lm_mm(const LmMm& a, hipStream_t st) {
   return lm_mm_launch<F16, BT, 2, 2, 4, 4, 2, OutT>(a, st);
 }
 
-template <bool F16, typename OutT>
-mi_status lm_few(const LmFew& p, hipStream_t st) {
-  const unsigned T = static_cast<unsigned>(p.T), R = static_cast<unsigned>(p.R);
-  if (T * R <= 2048)
-    hipLaunchKernelGGL((lm_dots_kernel<F16, 1>), dim3(T, R / 4), dim3(256), 0, st, p);
-  else
-    hipLaunchKernelGGL((lm_dots_kernel<F16, 4>), dim3(T, (R + 15) / 16), dim3(256), 0, st, p);
-  const mi_status one = launch_status("mm_lora (dots)");
+template <bool F16, bool BT, typename OutT, typename GradT>
+mi_status lm_small_run(LmSmall p, hipStream_t st) {
+  const char* what = BT ? "mm_lora_backward (few rows)" : "mm_lora (few rows)";
+  const bool dense = p.out != nullptr;
+  p.splits = lm_splits(p.T, p.mm.n, p.mm.k);
+  p.tiles = (p.T + 63) / 64 * ((p.mm.n + 63) / 64);
+  p.gemm = dense ? p.tiles * p.splits : 0;
+  const int dots = (p.u != nullptr ? p.T * (p.R / 8) : 0) + (p.v != nullptr ? p.T * (p.R / 4) : 0);
+  p.dots = (dots + 3) / 4 < 1024 ? (dots + 3) / 4 : 1024;
+  p.fin = dense ? static_cast<int>((static_cast<int64_t>(p.T) * (p.mm.n / 4) + 255) / 256) : 0;
+  hipLaunchKernelGGL((lm_parts_kernel<F16, BT>), dim3(p.gemm + p.dots), dim3(256), 0, st, p);
+  const mi_status one = launch_status(what);
   if (one != MI_OK) return one;
-#define LM_FEW(FM_, FN_)                                                                     \
-  hipLaunchKernelGGL((lm_few_kernel<F16, FM_, FN_, 8, OutT>),                                \
-                     dim3(static_cast<unsigned>((p.n + 16 * FN_ - 1) / (16 * FN_))), dim3(512), 0, st, p)
-  const bool wide = p.n > 16 * 256;
-  if (p.T <= 16) { if (wide) LM_FEW(1, 2); else LM_FEW(1, 1); }
-  else if (p.T <= 32) { if (wide) LM_FEW(2, 2); else LM_FEW(2, 1); }
-  else { if (wide) LM_FEW(4, 2); else LM_FEW(4, 1); }
-#undef LM_FEW
-  return launch_status("mm_lora (few rows)");
+  const int grads = p.ga == nullptr ? 0 : p.L * (p.R / 8) * ((p.ca + 2047) / 2048 + (p.cb + 2047) / 2048);
+  hipLaunchKernelGGL((lm_finish_kernel<F16, BT, OutT, GradT>), dim3(p.fin + grads), dim3(256), 0, st, p);
+  return launch_status(what);
 }
 
 }  // namespace
@@ -1349,12 +1418,28 @@ extern "C" mi_status mi_mm_lora(const void* x, int64_t m, int64_t k, mi_dtype dt
              "%s: the workspace needs %zu bytes, aligned to 256 (got %zu)", what, sp.bytes, workspace_bytes);
   hipStream_t hs = static_cast<hipStream_t>(stream);
   const int64_t es = out_dtype == MI_F32 ? 4 : 2;
-  if (m <= LM_FEW_ROWS) {
-    LmFew p{x, w, lora_a, lora_b, lora_ids, lora_scale, bias, reinterpret_cast<float*>(sp.pieces), act, out,
-            static_cast<int>(m), static_cast<int>(k), static_cast<int>(n),
-            static_cast<int>(num_adapters), static_cast<int>(rank)};
-    return dtype == MI_F16 ? (es == 4 ? lm_few<true, float>(p, hs) : lm_few<true, _Float16>(p, hs))
-                           : (es == 4 ? lm_few<false, float>(p, hs) : lm_few<false, __bf16>(p, hs));
+  if (lm_small(s)) {
+    LmSmall p{};
+    p.mm.x = p.x = x;
+    p.mm.w = w;
+    p.mm.T = p.T = static_cast<int>(m);
+    p.mm.k = p.ca = static_cast<int>(k);
+    p.mm.n = p.cb = static_cast<int>(n);
+    p.mm.L = p.L = static_cast<int>(num_adapters);
+    p.R = static_cast<int>(rank);
+    p.mm.out = sp.parts;
+    p.a = lora_a;
+    p.b = lora_b;
+    p.ids = lora_ids;
+    p.scale = lora_scale;
+    p.v = sp.v;
+    p.act = act;
+    p.bias = bias;
+    p.out = out;
+    return dtype == MI_F16 ? (es == 4 ? lm_small_run<true, false, float, float>(p, hs)
+                                      : lm_small_run<true, false, _Float16, float>(p, hs))
+                           : (es == 4 ? lm_small_run<false, false, float, float>(p, hs)
+                                      : lm_small_run<false, false, __bf16, float>(p, hs));
   }
   for (int64_t t0 = 0; t0 < m; t0 += s.pass()) {
     const int64_t rows = m - t0 < s.pass() ? m - t0 : s.pass();
@@ -1445,6 +1530,32 @@ extern "C" mi_status mi_mm_lora_backward(const void* grad_out, const void* x, in
              "%s: the workspace needs %zu bytes, aligned to 256 (got %zu)", what, sp.bytes, workspace_bytes);
   hipStream_t hs = static_cast<hipStream_t>(stream);
   const bool f16 = dtype == MI_F16, several = s.pass() < m;
+  if (m > 0 && lm_small(s)) {
+    LmSmall p{};
+    p.mm.x = p.go = grad_out;
+    p.x = x;
+    p.mm.w = w;
+    p.mm.T = p.T = static_cast<int>(m);
+    p.mm.k = p.cb = static_cast<int>(n);
+    p.mm.n = p.ca = static_cast<int>(k);
+    p.mm.L = p.L = static_cast<int>(num_adapters);
+    p.R = static_cast<int>(rank);
+    p.mm.out = sp.parts;
+    p.a = lora_a;
+    p.b = lora_b;
+    p.ids = lora_ids;
+    p.scale = lora_scale;
+    p.act_in = act;
+    p.v = banks && act == nullptr ? sp.v : nullptr;
+    p.u = sp.u;
+    p.out = grad_x;
+    p.ga = grad_a;
+    p.gb = grad_b;
+    return f16 ? (ges == 4 ? lm_small_run<true, true, _Float16, float>(p, hs)
+                           : lm_small_run<true, true, _Float16, _Float16>(p, hs))
+               : (ges == 4 ? lm_small_run<false, true, __bf16, float>(p, hs)
+                           : lm_small_run<false, true, __bf16, __bf16>(p, hs));
+  }
   auto shrink = [&](int64_t rows) {
     LmShrink a{};
     a.scale = lora_scale;
