@@ -35,7 +35,7 @@ constexpr int LM_MAX_ADAPTERS = 1024;
 constexpr int LM_MAX_RANK = 256;
 constexpr int LM_ITEM = 32;            // rows of an item
 constexpr int LM_BK = 64;              // 128 bytes of a row of x: one step
-constexpr int LM_FEW_ROWS = 64;       // up to here the few-row kernels
+constexpr int LM_FEW_ROWS = 64;         // up to here the few-row kernels
 constexpr uint32_t LM_OUT = 0x80000000u;  // past every descriptor's range
 
 __device__ __forceinline__ lds_void_ptr lm_lds(void* p) { return (lds_void_ptr)(p); }
@@ -670,76 +670,107 @@ __device__ __forceinline__ void lm_tile(const LmMm& p, const LmPlace& t, uint8_t
   // the loads of the steps past the last have written their zeros
   lm_wait_barrier<0>();
 
-  // The adapters, one run of rows after another.  The reduction runs over slots of 16
-  // ranks, all of the first piece, then of the second (fp32 outputs: the third), two
-  // slots an MFMA.  With BT, 64 ranks of the bank at a time go through LDS.
+  // The adapters, one run of rows after another, in steps of the same kind: the reduction
+  // runs over the first NP pieces of v (RP ranks each), 64 at a time, x's place taken by a
+  // row's pieces and w's by the bank's ranks, once for every piece.  A step's loads
+  // go out one step ahead.
   constexpr int NP = sizeof(OutT) == 4 ? 3 : 2;
-  constexpr int RB = 4;
-  static_assert(RB * 16 * BN * 2 <= STAGE, "ranks in a stage");
-  const int nb = p.RP / 16;
-  int row_at[FM], id_at[FM];
+  const int RP = p.RP, R = p.R, E = NP * RP;
+  int id_at[FM];
 #pragma unroll
-  for (int i = 0; i < FM; ++i) {
-    const i32x2 o = s_order[(wm * FM + i) * 16 + r];
-    row_at[i] = o.x;
-    id_at[i] = o.y;
-  }
-  for (int at = PART ? rows : 0; at < rows;) {
-    const int l = __builtin_amdgcn_readfirstlane(s_order[at].y);
-    if (l >= p.L) break;  // the rows without an adapter are last
-    const int end = max(min(gld<int>(p.plan.seg + l + 1) - m0, rows), at + 1);
+  for (int i = 0; i < FM; ++i) id_at[i] = s_order[(wm * FM + i) * 16 + r].y;
+  struct Run { int l, at, end, e; };  // rows [at, end) of adapter l, from reduction index e on
+  auto run_at = [&](int at) {
+    const int l = at < rows ? __builtin_amdgcn_readfirstlane(s_order[at].y) : p.L;
+    // the rows without an adapter are last
+    if (l >= p.L) return Run{p.L, rows, rows, 0};
+    return Run{l, at, max(min(gld<int>(p.plan.seg + l + 1) - m0, rows), at + 1), 0};
+  };
+  auto after = [&](const Run& u) { return u.e + LM_BK < E ? Run{u.l, u.at, u.end, u.e + LM_BK} : run_at(u.end); };
+  const __amdgpu_buffer_rsrc_t pr_ =
+      buf_rsrc(p.pieces, static_cast<uint32_t>(p.T) * static_cast<uint32_t>(RP) * 6u);
+  auto fetch = [&](uint8_t* st, const Run& u) {
+    if (u.l >= p.L) return;
     const __amdgpu_buffer_rsrc_t lr_ =
-        buf_rsrc(static_cast<const uint16_t*>(p.bank) + static_cast<int64_t>(l) * p.R * n,
-                 static_cast<uint32_t>(p.R) * static_cast<uint32_t>(n) * 2u);
-    for (int j0 = 0; j0 < nb; j0 += BT ? RB : nb) {
-      const int part = BT ? min(nb - j0, RB) : nb, ns = NP * part;
-      if constexpr (BT) {
-        __syncthreads();
-        for (int q = tid; q < part * 16 * CPW; q += 64 * NW) {
-          const int row = q / CPW, c = q % CPW, rk = j0 * 16 + row;
-          const int col = (((c >> 1) ^ lm_tswz<BN>(row)) * 2 + (c & 1)) * 8;
-          *reinterpret_cast<u32x4*>(s0 + q * 16) = buf_ld128(
-              lr_, col < cols && rk < p.R ? (static_cast<uint32_t>(rk) * n + n0 + col) * 2 : LM_OUT, 0);
-        }
-        __syncthreads();
+        buf_rsrc(static_cast<const uint16_t*>(p.bank) + static_cast<int64_t>(u.l) * R * n,
+                 static_cast<uint32_t>(R) * static_cast<uint32_t>(n) * 2u);
+    const int e = u.e + chunk * 8;
+#pragma unroll
+    for (int i = 0; i < NIA; ++i) {
+      const int row = 8 * (NW * i + wave) + lr;
+      const bool own = row >= u.at && row < u.end && e < E;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          pr_, lm_lds(st + (NW * i + wave) * 1024), 16,
+          own ? (static_cast<uint32_t>(s_order[row].x) * 3 * RP + e) * 2 : LM_OUT, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < NIB; ++i) {
+      uint32_t at;
+      if constexpr (!BT) {
+        const int row = 8 * (NW * i + wave) + lr, rk = e % RP;
+        at = row < cols && e < E && rk < R ? (static_cast<uint32_t>(n0 + row) * R + rk) * 2 : LM_OUT;
+      } else {
+        const int row = brow(i), c = lane % CPW, rk = (u.e + row) % RP;
+        const int col = (((c >> 1) ^ lm_tswz<BN>(row)) * 2 + (c & 1)) * 8;
+        at = col < cols && u.e + row < E && rk < R ? (static_cast<uint32_t>(rk) * n + n0 + col) * 2 : LM_OUT;
       }
-      for (int s = 0; s < ns; s += 2) {
-        // this lane's slot: piece pc, ranks 16 (j0 + jb) + 8 (g & 1) ..
-        const int mine = min(s + (g >> 1), ns - 1), pc = mine / part, jb = mine % part;
-        const bool live = s + (g >> 1) < ns;
-        u32x4 fv[FM];
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(lr_, lm_lds(st + BM * 128 + (NW * i + wave) * 1024), 16, at, 0, 0, 0);
+    }
+  };
+  // blocks all in the run take the sums as they come; in one that it shares, only its own
+  // rows' lanes do: a NaN in this adapter's bank is not another row's
+  auto adapt = [&](const uint8_t* st, const Run& u) {
+    Frag b[FN], lo[FN];
 #pragma unroll
-        for (int i = 0; i < FM; ++i) {
-          fv[i] = u32x4{0, 0, 0, 0};
-          if (live && id_at[i] == l)
-            fv[i] = gld<u32x4>(p.pieces + (static_cast<int64_t>(row_at[i]) * 3 + pc) * p.RP +
-                               (j0 + jb) * 16 + (g & 1) * 8);
-        }
+    for (int j = 0; j < FN; ++j) b[j] = frag_b(st, j);
+    Frag a0 = frag_a(st, 0), a1 = frag_a(st, 1);
+    if constexpr (F16)
 #pragma unroll
-        for (int j = 0; j < FN; ++j) {
-          u32x4 hi, lo = {0, 0, 0, 0};
-          if constexpr (BT) {
-            hi = column(s0, wn * FN + j, jb * 16 + (g & 1) * 8);
-          } else {
-            const int c = (wn * FN + j) * 16 + r, rk = jb * 16 + (g & 1) * 8;
-            hi = buf_ld128(lr_, c < cols && rk < p.R ? (static_cast<uint32_t>(n0 + c) * p.R + rk) * 2 : LM_OUT, 0);
-          }
-          if constexpr (F16) lm_split(hi, hi, lo);
+      for (int j = 0; j < FN; ++j)
 #pragma unroll
-          for (int i = 0; i < FM; ++i) {
-            const int b0 = (wm * FM + i) * 16;
-            if (b0 + 16 <= at || b0 >= end) continue;
-            f32x4 d = lm_mfma<false>(hi, fv[i], acc[i][j]);
-            if constexpr (F16) d = lm_mfma<false>(lo, fv[i], d);
-            // a NaN in this adapter's bank is not another row's
-            if (id_at[i] == l) acc[i][j] = d;
-          }
-        }
+        for (int h = 0; h < 2; ++h) lm_split(b[j].h[h], b[j].h[h], lo[j].h[h]);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const Frag a = a0;
+      a0 = a1;
+      if (i + 2 < FM) a1 = frag_a(st, i + 2);
+      const int b0 = (wm * FM + i) * 16;
+      if (b0 + 16 <= u.at || b0 >= u.end) continue;
+      f32x4 d[FN];
+#pragma unroll
+      for (int j = 0; j < FN; ++j) d[j] = acc[i][j];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j) d[j] = lm_mfma<false>(b[j].h[h], a.h[h], d[j]);
+        if constexpr (F16)
+#pragma unroll
+          for (int j = 0; j < FN; ++j) d[j] = lm_mfma<false>(lo[j].h[h], a.h[h], d[j]);
+      }
+      if (b0 >= u.at && b0 + 16 <= u.end) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = d[j];
+      } else if (id_at[i] == u.l) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = d[j];
       }
     }
-    at = end;
+  };
+  if constexpr (!PART) {
+    Run u = run_at(0);
+    fetch(s0, u);
+    while (u.l < p.L) {
+      const Run v = after(u);
+      lm_wait_barrier<0>();
+      fetch(s1, v);
+      adapt(s0, u);
+      if (v.l >= p.L) break;
+      u = after(v);
+      lm_wait_barrier<0>();
+      fetch(s0, u);
+      adapt(s1, v);
+    }
   }
-
   // acc[i][j][q]: row 16 i + r, column 16 j + 4 g + q of the wavefront's.  The outputs go
   // through the wavefront's own part of the stages, PB blocks of rows at a time, so that
   // it stores runs of RBY bytes of a row, 16 bytes a lane.  16-byte chunk c of a row sits
@@ -749,7 +780,7 @@ __device__ __forceinline__ void lm_tile(const LmMm& p, const LmPlace& t, uint8_t
   constexpr int PER = STAGE / (PB * 16 * RBY);  // parts in a stage
   static_assert(PB * 16 * RBY <= ROOM && NW <= NST * PER && 64 % CPR == 0, "epilogue");
   uint8_t* const reg = sts[wave / PER] + wave % PER * (PB * 16 * RBY);
-  __syncthreads();  // the ranks of the last run have been read
+  __syncthreads();  // the last stages have been read
   f32x4 bias[FN];
 #pragma unroll
   for (int j = 0; j < FN; ++j) {
@@ -1223,7 +1254,9 @@ struct LmSizes {
   // rows of one pass: a row's place in x or go is a 31-bit byte offset
   int64_t pass() const {
     const int64_t wide = N > K ? N : K, fit = ((1LL << 31) - 1) / (2 * wide) & ~255LL;
-    const int64_t most = fit < (1LL << 22) ? fit : 1LL << 22;
+    const int64_t pieces = ((1LL << 31) - 1) / (6 * rp()) & ~255LL;  // and in the pieces
+    int64_t most = fit < (1LL << 22) ? fit : 1LL << 22;
+    if (pieces < most) most = pieces;
     return T < most ? T : most;
   }
   static int64_t items(int64_t t, int64_t l) { return t / LM_ITEM + (l + 1 < t ? l + 1 : t) + 1; }
