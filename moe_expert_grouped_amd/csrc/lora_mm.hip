@@ -10,7 +10,7 @@
 //   gB[l]  = s[l] sum_{t of l} go[t]^T v[t]                [N, R]
 //
 // Steps, each a launch on the caller's stream:
-//   plan    one workgroup sorts the rows by adapter (stable), cuts every adapter's
+//   plan    (two launches) sorts the rows by adapter (stable), cuts every adapter's
 //           rows into items of 32 and its items into chunks
 //   shrink  v (or u) of an item; kept as three bf16 pieces whose sum has 24 bits,
 //           so that the second product runs on bf16 MFMAs without a rounding of v
@@ -42,7 +42,9 @@ __device__ __forceinline__ lds_void_ptr lm_lds(void* p) { return (lds_void_ptr)(
 
 // the sorted rows and what is cut from them
 struct LmPlan {
-  i32x2* order;      // [T] {row, adapter}; rows without one last, adapter L
+  int* rank;        // [T] of a row among its chunk's rows of its adapter
+  int* counts;      // [chunks, L + 1] of adapters' rows
+  i32x2* order;     // [T] {row, adapter}; rows without one last, adapter L
   int* seg;         // [L + 1] first position of every adapter
   int* item_id;     // adapter of every item
   int* slot_row;    // [LM_ITEM * items] row of every slot of an item, -1: none
@@ -92,58 +94,81 @@ __device__ __forceinline__ uint64_t pl_peers(int v, int bits) {
   return peers;
 }
 
-// One workgroup: a launch of several would need two more for the sums between them.
-// The ids of 16384 rows at a time are held in LDS, which is all of them for most calls:
-// the second pass then reads nothing again.  The loops over them are not unrolled: a kernel
-// that runs once a call waits for its instructions more than for its data.
-constexpr int PL_HELD = 1024;  // ids of a wavefront in LDS
-
-__global__ __launch_bounds__(PL_T) void lm_plan_kernel(const int32_t* __restrict__ ids, int T,
-                                                       int L, int chunk_items, LmPlan p) {
+// Two launches of a workgroup per chunk of rows (1024, or a 64th of them).  count: the
+// chunk's rows of every adapter, and each row's rank among them; a wavefront's rows go in
+// order, and the counts of the wavefronts before it are added.  place: every workgroup adds
+// the chunks' counts itself, which gives all places; the first writes the lists.
+__global__ __launch_bounds__(PL_T) void lm_count_kernel(const int32_t* __restrict__ ids, int T,
+                                                        int L, int chunk, LmPlan p) {
   __shared__ int s_cnt[(LM_MAX_ADAPTERS + 1) * PL_S];  // an adapter's counts by wavefront
-  __shared__ uint16_t s_ids[PL_W * PL_HELD];
-  __shared__ int s_item0[LM_MAX_ADAPTERS + 1], s_seg[LM_MAX_ADAPTERS + 1];
-  __shared__ PlPair s_scan[PL_W];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int per = ((T + PL_W - 1) / PL_W + 63) & ~63;
-  const int r0 = min(wave * per, T), r1 = min(r0 + per, T);
-  uint16_t* const held = s_ids + wave * PL_HELD;
-  auto hold = [&](int at) {
-    const int n = min(r1 - at, PL_HELD);
-#pragma unroll 4
-    for (int i = lane; i < n; i += 64) {
-      const int id = gld<int32_t>(ids + at + i);
-      held[i] = static_cast<uint16_t>(id < 0 || id > L ? L : id);
-    }
+  const int per = chunk / PL_W;
+  const int r0 = min(static_cast<int>(blockIdx.x) * chunk + wave * per, T), r1 = min(r0 + per, T);
+  auto id_at = [&](int row) {
+    const int id = row < r1 ? gld<int32_t>(ids + row) : L;
+    return id < 0 || id > L ? L : id;
   };
-  hold(r0);
-  #pragma unroll 1
+  const int first_id = id_at(r0 + lane);
+#pragma unroll 1
   for (int i = tid; i < (L + 1) * PL_S; i += PL_T) s_cnt[i] = 0;
-  if (tid == 0) gst<u32x4>(p.zeros, u32x4{0, 0, 0, 0});
   __syncthreads();
   const int bits = 32 - __builtin_clz(L);  // ids 0 .. L
-  int* const cnt = s_cnt + wave;  // of adapter l at l * PL_S
-  // the lanes of `live` that hold the same id; a run's rows all do
-  auto peers_of = [&](int id, uint64_t live) {
-    const uint64_t same = __ballot(id == __builtin_amdgcn_readfirstlane(id)) & live;
-    return same == live ? live : pl_peers(id, bits) & live;
-  };
-  for (int at = r0; at < r1; at += PL_HELD) {
-    if (at > r0) hold(at);
+  int* const cnt = s_cnt + wave;           // of adapter l at l * PL_S
 #pragma unroll 1
-    for (int i = lane; at + i - lane < min(r1, at + PL_HELD); i += 64) {
-      const bool in = at + i < r1;
-      const int id = in ? held[i] : L;
-      const uint64_t peers = peers_of(id, __ballot(in));
-      if (in && (peers & ((1ull << lane) - 1)) == 0) cnt[id * PL_S] += __popcll(peers);
-      __builtin_amdgcn_wave_barrier();
+  for (int at = r0; at < r1; at += 64) {
+    const int row = at + lane, id = at == r0 ? first_id : id_at(row);
+    // the lanes that hold the same id; a run's rows all do
+    const uint64_t live = __ballot(row < r1);
+    uint64_t peers = __ballot(id == __builtin_amdgcn_readfirstlane(id)) & live;
+    if (peers != live) peers = pl_peers(id, bits) & live;
+    const uint64_t below = peers & ((1ull << lane) - 1);
+    if (row < r1) {
+      const int before = cnt[id * PL_S];
+      gst<int>(p.rank + row, before + __popcll(below));
+      if (below == 0) cnt[id * PL_S] = before + __popcll(peers);
     }
+    // LDS operations of one wavefront complete in order
+    __builtin_amdgcn_wave_barrier();
   }
   __syncthreads();
+  for (int l = tid; l <= L; l += PL_T) {
+    int run = 0;
+#pragma unroll
+    for (int w = 0; w < PL_W; ++w) {
+      const int c = s_cnt[l * PL_S + w];
+      s_cnt[l * PL_S + w] = run;
+      run += c;
+    }
+    gst<int>(p.counts + static_cast<int64_t>(blockIdx.x) * (L + 1) + l, run);
+  }
+  __syncthreads();
+  if (wave == 0) return;  // nothing before it
+#pragma unroll 2
+  for (int row = r0 + lane; row < r1; row += 64) {
+    const int id = row == r0 + lane ? first_id : id_at(row);
+    const int add = cnt[id * PL_S];
+    if (add) gst<int>(p.rank + row, gld<int>(p.rank + row) + add);
+  }
+}
+
+__global__ __launch_bounds__(PL_T) void lm_place_kernel(const int32_t* __restrict__ ids, int T,
+                                                        int L, int chunk, int chunk_items,
+                                                        LmPlan p) {
+  __shared__ int s_base[LM_MAX_ADAPTERS + 1];  // place of this chunk's first row
+  __shared__ int s_seg[LM_MAX_ADAPTERS + 1], s_item0[LM_MAX_ADAPTERS + 2];
+  __shared__ PlPair s_scan[PL_W];
+  const int tid = threadIdx.x, blocks = gridDim.x, block = blockIdx.x;
+  const bool lists = block == 0;
   // thread l: adapter l
-  int rows = 0;
-  if (tid < L)
-    for (int w = 0; w < PL_W; ++w) rows += s_cnt[tid * PL_S + w];
+  int rows = 0, mine = 0;
+  if (tid < L) {
+#pragma unroll 4
+    for (int c = 0; c < blocks; ++c) {
+      const int v = gld<int>(p.counts + static_cast<int64_t>(c) * (L + 1) + tid);
+      rows += v;
+      mine += c < block ? v : 0;
+    }
+  }
   const int items = (rows + LM_ITEM - 1) / LM_ITEM;
   const int chunks = tid < L ? max((items + chunk_items - 1) / chunk_items, 1) : 0;
   PlPair all;
@@ -153,66 +178,54 @@ __global__ __launch_bounds__(PL_T) void lm_plan_kernel(const int32_t* __restrict
               s_scan, &all);
   const int seg = static_cast<int>(before.a), item0 = static_cast<int>(before.a >> 32);
   const int chunk0 = static_cast<int>(before.b), part0 = static_cast<int>(before.b >> 32);
-  // this wavefront's first place of an adapter's rows, for every wavefront
-  auto places = [&](int l, int run) {
-    for (int w = 0; w < PL_W; ++w) {
-      const int c = s_cnt[l * PL_S + w];
-      s_cnt[l * PL_S + w] = run;
-      run += c;
-    }
-  };
+  // the rows without an adapter follow, in items of their own
+  const int in = static_cast<int>(all.a), real = static_cast<int>(all.a >> 32);
+  const int more = (T - in + LM_ITEM - 1) / LM_ITEM;
   if (tid < L) {
+    s_base[tid] = seg + mine;
     s_seg[tid] = seg;
     s_item0[tid] = item0;
-    gst<int>(p.seg + tid, seg);
+    if (lists) {
+      gst<int>(p.seg + tid, seg);
 #pragma unroll 1
-    for (int c = 0; c < chunks; ++c)
-      gst<i32x4>(p.chunks + chunk0 + c,
-                 i32x4{tid, item0 + c * chunk_items, min(items - c * chunk_items, chunk_items),
-                       chunks > 1 ? part0 + c : -1});
-    gst<i32x4>(p.spans + tid, i32x4{chunk0, chunks, chunks > 1 ? part0 : -1, 0});
+      for (int c = 0; c < chunks; ++c)
+        gst<i32x4>(p.chunks + chunk0 + c,
+                   i32x4{tid, item0 + c * chunk_items, min(items - c * chunk_items, chunk_items),
+                         chunks > 1 ? part0 + c : -1});
+      gst<i32x4>(p.spans + tid, i32x4{chunk0, chunks, chunks > 1 ? part0 : -1, 0});
 #pragma unroll 1
-    for (int i = rows; i < items * LM_ITEM; ++i) gst<int>(p.slot_row + item0 * LM_ITEM + i, -1);
-    places(tid, seg);
+      for (int i = rows; i < items * LM_ITEM; ++i) gst<int>(p.slot_row + item0 * LM_ITEM + i, -1);
+    }
   }
   if (tid == PL_T - 1) {
-    // the rows without an adapter follow, in items of their own
-    const int in = static_cast<int>(all.a), real = static_cast<int>(all.a >> 32);
-    const int more = (T - in + LM_ITEM - 1) / LM_ITEM;
+    int run = in;
+#pragma unroll 4
+    for (int c = 0; c < block; ++c) run += gld<int>(p.counts + static_cast<int64_t>(c) * (L + 1) + L);
+    s_base[L] = run;
     s_seg[L] = in;
     s_item0[L] = real;
-    gst<int>(p.seg + L, in);
-    gst<i32x4>(p.totals, i32x4{real, static_cast<int>(all.b), real + more, 0});
+    s_item0[L + 1] = real + more;
+    if (lists) {
+      gst<int>(p.seg + L, in);
+      gst<i32x4>(p.totals, i32x4{real, static_cast<int>(all.b), real + more, 0});
+      gst<u32x4>(p.zeros, u32x4{0, 0, 0, 0});
 #pragma unroll 1
-    for (int i = T - in; i < more * LM_ITEM; ++i) gst<int>(p.slot_row + real * LM_ITEM + i, -1);
-    places(L, in);
+      for (int i = T - in; i < more * LM_ITEM; ++i) gst<int>(p.slot_row + real * LM_ITEM + i, -1);
+    }
   }
   __syncthreads();
-  for (int at = r0; at < r1; at += PL_HELD) {
-    if (per > PL_HELD) hold(at);
-#pragma unroll 1
-    for (int i = lane; at + i - lane < min(r1, at + PL_HELD); i += 64) {
-      const int row = at + i;
-      const bool in = row < r1;
-      const int id = in ? held[i] : L;
-      const uint64_t peers = peers_of(id, __ballot(in));
-      const uint64_t below = peers & ((1ull << lane) - 1);
-      int pos = 0;
-      if (in) {
-        pos = cnt[id * PL_S] + __popcll(below);
-        // pos < T holds where the ids did not change between the passes
-        if (pos < T) {
-          gst<i32x2>(p.order + pos, i32x2{row, id});
-          const int rank = pos - s_seg[id], item = s_item0[id] + rank / LM_ITEM;
-          gst<int>(p.slot_row + item * LM_ITEM + rank % LM_ITEM, row);
-          if (rank % LM_ITEM == 0) gst<int>(p.item_id + item, id);
-        }
-      }
-      // LDS operations of one wavefront complete in order
-      __builtin_amdgcn_wave_barrier();
-      if (in && below == 0) cnt[id * PL_S] = pos + __popcll(peers);
-      __builtin_amdgcn_wave_barrier();
-    }
+  const int r1 = min((block + 1) * chunk, T);
+#pragma unroll 4
+  for (int row = block * chunk + tid; row < r1; row += PL_T) {
+    int id = gld<int32_t>(ids + row);
+    id = id < 0 || id > L ? L : id;
+    const int pos = s_base[id] + gld<int>(p.rank + row), rank = pos - s_seg[id];
+    const int item = s_item0[id] + rank / LM_ITEM;
+    // all so where the ids did not change between the passes
+    if (rank < 0 || pos >= T || item >= s_item0[id + 1]) continue;
+    gst<i32x2>(p.order + pos, i32x2{row, id});
+    gst<int>(p.slot_row + item * LM_ITEM + rank % LM_ITEM, row);
+    if (rank % LM_ITEM == 0) gst<int>(p.item_id + item, id);
   }
 }
 
@@ -1311,6 +1324,8 @@ LmSpace lm_space(const LmSizes& s, bool backward, void* base) {
     return o;
   }
   const int64_t items = LmSizes::items(s.T, s.L);
+  o.plan.rank = c.take<int>(s.T);
+  o.plan.counts = c.take<int>(64 * (s.L + 1));
   o.plan.order = c.take<i32x2>(s.T);
   o.plan.seg = c.take<int>(s.L + 1);
   o.plan.item_id = c.take<int>(items);
@@ -1347,9 +1362,17 @@ mi_status lm_check(const char* what, const LmSizes& s, mi_dtype dt) {
 }
 
 mi_status lm_plan(const LmSizes& s, int64_t rows, const int32_t* ids, const LmPlan& p, hipStream_t st) {
-  hipLaunchKernelGGL(lm_plan_kernel, dim3(1), dim3(PL_T),
-                     0, st, ids, static_cast<int>(rows),
-                     static_cast<int>(s.L), static_cast<int>(s.chunk_items()), p);
+  // 64 chunks at most, of 1024 rows each at least
+  int64_t chunk = (rows + 63) / 64;
+  chunk = chunk <= PL_T ? PL_T : (chunk + PL_T - 1) / PL_T * PL_T;
+  const int64_t blocks = rows > 0 ? (rows + chunk - 1) / chunk : 1;
+  const dim3 grid(static_cast<unsigned>(blocks));
+  const int T = static_cast<int>(rows), L = static_cast<int>(s.L), c = static_cast<int>(chunk);
+  hipLaunchKernelGGL(lm_count_kernel, grid, dim3(PL_T), 0, st, ids, T, L, c, p);
+  const mi_status one = launch_status("mm_lora (plan)");
+  if (one != MI_OK) return one;
+  hipLaunchKernelGGL(lm_place_kernel, grid, dim3(PL_T), 0, st, ids, T, L, c,
+                     static_cast<int>(s.chunk_items()), p);
   return launch_status("mm_lora (plan)");
 }
 
