@@ -514,6 +514,9 @@ __device__ __forceinline__ LmPlace lm_place(const LmMm& p) {
   return {m0, n0, min(p.T - m0, BM), min(p.n - n0, BN), 0, (p.k + LM_BK - 1) / LM_BK};
 }
 
+// the LDS of one step: w's rows, and x's, of two stages in two halves
+struct LmStage { uint8_t *w, *x0, *x1; };
+
 // One tile of BM = 16 FM WM rows and BN = 16 FN WN columns; WM * WN wavefronts of
 // 16 FM x 16 FN.  w is the MFMA's first operand, so a lane's results are four
 // consecutive columns of one row.
@@ -530,8 +533,8 @@ __device__ __forceinline__ LmPlace lm_place(const LmMm& p) {
 //
 // PART: only the steps [t.k0, t.k0 + t.steps), rows in their own order, no adapters.
 template <bool F16, bool BT, bool PART, int WM, int WN, int FM, int FN, int NST, typename OutT>
-__device__ __forceinline__ void lm_tile(const LmMm& p, const LmPlace& t, uint8_t* s0, uint8_t* s1,
-                                        uint8_t* s2, uint8_t* s3, i32x2* s_order) {
+__device__ __forceinline__ void lm_tile(const LmMm& p, const LmPlace& t, LmStage s0, LmStage s1,
+                                        LmStage s2, LmStage s3, i32x2* s_order) {
   constexpr int NW = WM * WN, BM = 16 * FM * WM, BN = 16 * FN * WN;
   constexpr int NIA = BM / 8 / NW, NIB = BN / 8 / NW, NI = NIA + NIB;
   constexpr int STAGE = (BM + BN) * 128;
@@ -561,6 +564,18 @@ __device__ __forceinline__ void lm_tile(const LmMm& p, const LmPlace& t, uint8_t
     va[i] = row >= 0 ? (static_cast<uint32_t>(row) * k + chunk * 8) * 2 : LM_OUT;
   }
   constexpr int CPW = BN / 8;  // 16-byte pieces of a transposed tile's row
+  // Two stages: w's rows and the even instructions' rows of x first, then the odd ones'
+  auto nth = [](int o) {
+    return NST > 2 ? o : o < NIB ? NIA + o : o < NIB + NIA / 2 ? 2 * (o - NIB) : 2 * (o - NIB - NIA / 2) + 1;
+  };
+  // where instruction i of x's rows goes, and where block i of this wavefront's rows is
+  auto to_x = [&](const LmStage& st, int i) {
+    return NST > 2 ? st.x0 + (NW * i + wave) * 1024 : (i & 1 ? st.x1 : st.x0) + (NW * (i >> 1) + wave) * 1024;
+  };
+  auto block_x = [&](const LmStage& st, int i) {
+    constexpr int H = FM / 2;
+    return NST > 2 ? st.x0 + (wm * FM + i) * 2048 : i < H ? st.x0 + (wm * H + i) * 2048 : st.x1 + (wm * H + i - H) * 2048;
+  };
   auto brow = [&](int i) { return ((NW * i + wave) * 64 + lane) / CPW; };
 #pragma unroll
   for (int i = 0; i < NIB; ++i) {
@@ -574,25 +589,26 @@ __device__ __forceinline__ void lm_tile(const LmMm& p, const LmPlace& t, uint8_t
     }
   }
   const uint32_t tail = last * LM_BK + chunk * 8 < k ? 0u : LM_OUT;
-  // Pieces [first, first + count) of the NI loads of a stage.  A step past the last
-  // loads zeros: the steps stay free of branches.
-  auto dma = [&](uint8_t* st, int kt, int first, int count) {
+  // Loads [first, first + count) of the NI of a stage, in the order of `nth`.  A step past
+  // the last loads zeros: the steps stay free of branches.
+  auto dma = [&](const LmStage& st, int kt, int first, int count) {
     const int kb = k0 + min(kt, KT - 1);
     const uint32_t drop = kt >= KT ? LM_OUT : 0u, dropa = kb == last ? drop | tail : drop;
     const uint32_t so = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(kb) * (LM_BK * 2));
     const uint32_t sob =
         BT ? __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(kb) * (LM_BK * 2) * n) : so;
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      if (i < first || i >= first + count) continue;
+    for (int o = 0; o < NI; ++o) {
+      if (o < first || o >= first + count) continue;
+      const int i = nth(o);
       if (i < NIA) {
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, lm_lds(st + (NW * i + wave) * 1024), 16,
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, lm_lds(to_x(st, i)), 16,
                                                  va[i < NIA ? i : 0] | dropa, so, 0, 0);
       } else {
         const int b = i < NIA ? 0 : i - NIA;
         const uint32_t d = !BT ? dropa : kb * LM_BK + brow(b) < k ? drop : LM_OUT;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            br, lm_lds(st + BM * 128 + (NW * b + wave) * 1024), 16, vb[b] | d, sob, 0, 0);
+            br, lm_lds(st.w + (NW * b + wave) * 1024), 16, vb[b] | d, sob, 0, 0);
       }
     }
   };
@@ -611,9 +627,9 @@ __device__ __forceinline__ void lm_tile(const LmMm& p, const LmPlace& t, uint8_t
   int fo[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) fo[h] = r * 128 + ((ck + 4 * h) ^ lm_swz(r)) * 16;
-  auto frag = [&](const uint8_t* st, int blk) {
-    return Frag{{*reinterpret_cast<const u32x4*>(st + blk * 2048 + fo[0]),
-                 *reinterpret_cast<const u32x4*>(st + blk * 2048 + fo[1])}};
+  auto frag = [&](const uint8_t* blk) {
+    return Frag{{*reinterpret_cast<const u32x4*>(blk + fo[0]),
+                 *reinterpret_cast<const u32x4*>(blk + fo[1])}};
   };
   // a transposed tile's rows c8 .. c8 + 7 (c8 % 8 == 0) of column block blk
   auto column = [&](const uint8_t* st, int blk, int c8) {
@@ -623,28 +639,45 @@ __device__ __forceinline__ void lm_tile(const LmMm& p, const LmPlace& t, uint8_t
     const int row2 = row + 4;
     return lm_column(a, st + row2 * (BN * 2) + (blk ^ lm_tswz<BN>(row2)) * 32 + (r & 3) * 8);
   };
-  auto frag_a = [&](const uint8_t* st, int i) { return frag(st, wm * FM + i); };
-  auto frag_b = [&](const uint8_t* st, int j) {
-    if constexpr (BT) {
-      const uint8_t* b = st + BM * 128;
-      return Frag{{column(b, wn * FN + j, ck * 8), column(b, wn * FN + j, ck * 8 + 32)}};
-    } else {
-      return frag(st + BM * 128, wn * FN + j);
-    }
+  auto frag_a = [&](const LmStage& st, int i) { return frag(block_x(st, i)); };
+  auto frag_b = [&](const LmStage& st, int j) {
+    if constexpr (BT)
+      return Frag{{column(st.w, wn * FN + j, ck * 8), column(st.w, wn * FN + j, ck * 8 + 32)}};
+    else
+      return frag(st.w + (wn * FN + j) * 2048);
   };
   // A stage's loads go out PPR per region from the one behind the barrier on, over half
   // of the regions.
   constexpr int PPR = (2 * NI + FM - 1) / FM, R0 = FM - 2;
+  // Two stages are too few for that: a load would have less than a step to arrive.  They
+  // have a second barrier half a step before the first, in region RY: by then w's rows
+  // and the first half of every wavefront's blocks of x have been read, and the loads of
+  // these for step kt + 2 go out; those of the second half go out behind the barrier in
+  // R0, and are waited for in RY.  Every load has a step and a half.
+  constexpr int RY = FM / 2 - 2, NY = NIB + NIA / 2, NX = NIA / 2;
+  constexpr int PY = (2 * NY + FM - 1) / FM, PX = (2 * NX + FM - 1) / FM;
+  static_assert(NST > 2 || (FM >= 4 && NIA == 2 * WM && NIA % 2 == 0), "halves of x");
   Frag fb[FN], fa0, fa1;
-  auto step = [&](uint8_t* pv, uint8_t* st, uint8_t* nx, int kt) {
+  auto step = [&](const LmStage& pv, const LmStage& st, const LmStage& nx, int kt) {
     Frag fbx[FN];
 #pragma unroll
     for (int j = 0; j < FN; ++j) fbx[j] = fb[j];
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-      if (i == R0) lm_wait_barrier<FLY>();
-      if (i >= R0) dma(st, kt + NST, (i - R0) * PPR, PPR);
-      else if ((i + 2) * PPR < NI) dma(pv, kt + NST - 1, (i + 2) * PPR, PPR);
+      if constexpr (NST > 2) {
+        if (i == R0) lm_wait_barrier<FLY>();
+        if (i >= R0) dma(st, kt + NST, (i - R0) * PPR, PPR);
+        else if ((i + 2) * PPR < NI) dma(pv, kt + NST - 1, (i + 2) * PPR, PPR);
+      } else {
+        if (i == RY || i == R0) lm_wait_barrier<NI>();
+        // (first, count) within the part, no further than its end
+        auto part = [&](const LmStage& to, int at, int base, int size, int first, int count) {
+          if (first < size) dma(to, at, base + first, first + count < size ? count : size - first);
+        };
+        if (i >= R0) part(st, kt + 2, NY, NX, (i - R0) * PX, PX);
+        else if (i >= RY) part(st, kt + 2, 0, NY, (i - RY) * PY, PY);
+        else part(pv, kt + 1, NY, NX, (i + 2) * PX, PX);
+      }
       const Frag fax = fa0;
       fa0 = fa1;
       fa1 = i < R0 ? frag_a(st, i + 2) : frag_a(nx, i - R0);
@@ -658,12 +691,17 @@ __device__ __forceinline__ void lm_tile(const LmMm& p, const LmPlace& t, uint8_t
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  uint8_t* const sts[4] = {s0, s1, s2, s3};
+  const LmStage* const sts[4] = {&s0, &s1, &s2, &s3};
   dma(s0, 0, 0, NI);
-  if constexpr (NST >= 3) dma(s1, 1, 0, NI);
-  if constexpr (NST == 4) dma(s2, 2, 0, NI);
-  lm_wait_barrier<FLY>();
-  dma(sts[NST - 1], NST - 1, 0, 2 * PPR);  // the rest in step 0
+  if constexpr (NST >= 3) {
+    dma(s1, 1, 0, NI);
+    if constexpr (NST == 4) dma(s2, 2, 0, NI);
+    lm_wait_barrier<FLY>();
+    dma(*sts[NST - 1], NST - 1, 0, 2 * PPR);  // the rest in step 0
+  } else {
+    dma(s1, 1, 0, NY + (2 * PX < NX ? 2 * PX : NX));  // the rest in step 0
+    lm_wait_barrier<NI>();
+  }
   fa0 = frag_a(s0, 0);
   fa1 = frag_a(s0, 1);
 #pragma unroll
@@ -671,7 +709,7 @@ __device__ __forceinline__ void lm_tile(const LmMm& p, const LmPlace& t, uint8_t
   for (int kt = 0; kt < KT; kt += NST) {
 #define LM_STEP(S_)                                                                      \
   if constexpr (S_ < NST) {                                                              \
-    step(sts[(S_ + NST - 1) % NST], sts[S_], sts[(S_ + 1) % NST], kt + S_);              \
+    step(*sts[(S_ + NST - 1) % NST], *sts[S_], *sts[(S_ + 1) % NST], kt + S_);             \
     if (kt + S_ + 1 >= KT) break;                                                        \
   }
     LM_STEP(0)
@@ -702,7 +740,7 @@ __device__ __forceinline__ void lm_tile(const LmMm& p, const LmPlace& t, uint8_t
   auto after = [&](const Run& u) { return u.e + LM_BK < E ? Run{u.l, u.at, u.end, u.e + LM_BK} : run_at(u.end); };
   const __amdgpu_buffer_rsrc_t pr_ =
       buf_rsrc(p.pieces, static_cast<uint32_t>(p.T) * static_cast<uint32_t>(RP) * 6u);
-  auto fetch = [&](uint8_t* st, const Run& u) {
+  auto fetch = [&](const LmStage& st, const Run& u) {
     if (u.l >= p.L) return;
     const __amdgpu_buffer_rsrc_t lr_ =
         buf_rsrc(static_cast<const uint16_t*>(p.bank) + static_cast<int64_t>(u.l) * R * n,
@@ -713,7 +751,7 @@ __device__ __forceinline__ void lm_tile(const LmMm& p, const LmPlace& t, uint8_t
       const int row = 8 * (NW * i + wave) + lr;
       const bool own = row >= u.at && row < u.end && e < E;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          pr_, lm_lds(st + (NW * i + wave) * 1024), 16,
+          pr_, lm_lds(to_x(st, i)), 16,
           own ? (static_cast<uint32_t>(s_order[row].x) * 3 * RP + e) * 2 : LM_OUT, 0, 0, 0);
     }
 #pragma unroll
@@ -727,45 +765,46 @@ __device__ __forceinline__ void lm_tile(const LmMm& p, const LmPlace& t, uint8_t
         const int col = (((c >> 1) ^ lm_tswz<BN>(row)) * 2 + (c & 1)) * 8;
         at = col < cols && u.e + row < E && rk < R ? (static_cast<uint32_t>(rk) * n + n0 + col) * 2 : LM_OUT;
       }
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(lr_, lm_lds(st + BM * 128 + (NW * i + wave) * 1024), 16, at, 0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(lr_, lm_lds(st.w + (NW * i + wave) * 1024), 16, at, 0, 0, 0);
     }
   };
   // blocks all in the run take the sums as they come; in one that it shares, only its own
   // rows' lanes do: a NaN in this adapter's bank is not another row's
-  auto adapt = [&](const uint8_t* st, const Run& u) {
-    Frag b[FN], lo[FN];
+  auto adapt = [&](const LmStage& st, const Run& u) {
 #pragma unroll
-    for (int j = 0; j < FN; ++j) b[j] = frag_b(st, j);
-    Frag a0 = frag_a(st, 0), a1 = frag_a(st, 1);
-    if constexpr (F16)
+    for (int h = 0; h < 2; ++h) {
+      if (h == 1 && u.e + 32 >= E) break;
+      auto half_a = [&](int i) { return *reinterpret_cast<const u32x4*>(block_x(st, i) + fo[h]); };
+      u32x4 b[FN], lo[FN];
 #pragma unroll
-      for (int j = 0; j < FN; ++j)
+      for (int j = 0; j < FN; ++j) {
+        if constexpr (BT) b[j] = column(st.w, wn * FN + j, ck * 8 + 32 * h);
+        else b[j] = *reinterpret_cast<const u32x4*>(st.w + (wn * FN + j) * 2048 + fo[h]);
+      }
+      u32x4 a0 = half_a(0), a1 = half_a(1);
+      if constexpr (F16)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) lm_split(b[j].h[h], b[j].h[h], lo[j].h[h]);
+        for (int j = 0; j < FN; ++j) lm_split(b[j], b[j], lo[j]);
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      const Frag a = a0;
-      a0 = a1;
-      if (i + 2 < FM) a1 = frag_a(st, i + 2);
-      const int b0 = (wm * FM + i) * 16;
-      if (b0 + 16 <= u.at || b0 >= u.end) continue;
-      f32x4 d[FN];
+      for (int i = 0; i < FM; ++i) {
+        const u32x4 a = a0;
+        a0 = a1;
+        if (i + 2 < FM) a1 = half_a(i + 2);
+        const int b0 = (wm * FM + i) * 16;
+        if (b0 + 16 <= u.at || b0 >= u.end) continue;
+        f32x4 d[FN];
 #pragma unroll
-      for (int j = 0; j < FN; ++j) d[j] = acc[i][j];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int j = 0; j < FN; ++j) d[j] = lm_mfma<false>(b[j].h[h], a.h[h], d[j]);
+        for (int j = 0; j < FN; ++j) d[j] = lm_mfma<false>(b[j], a, acc[i][j]);
         if constexpr (F16)
 #pragma unroll
-          for (int j = 0; j < FN; ++j) d[j] = lm_mfma<false>(lo[j].h[h], a.h[h], d[j]);
-      }
-      if (b0 >= u.at && b0 + 16 <= u.end) {
+          for (int j = 0; j < FN; ++j) d[j] = lm_mfma<false>(lo[j], a, d[j]);
+        if (b0 >= u.at && b0 + 16 <= u.end) {
 #pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = d[j];
-      } else if (id_at[i] == u.l) {
+          for (int j = 0; j < FN; ++j) acc[i][j] = d[j];
+        } else if (id_at[i] == u.l) {
 #pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = d[j];
+          for (int j = 0; j < FN; ++j) acc[i][j] = d[j];
+        }
       }
     }
   };
@@ -789,10 +828,12 @@ __device__ __forceinline__ void lm_tile(const LmMm& p, const LmPlace& t, uint8_t
   // it stores runs of RBY bytes of a row, 16 bytes a lane.  16-byte chunk c of a row sits
   // at slot c ^ (row % CPR).
   constexpr int ES = sizeof(OutT), RBY = 16 * FN * ES, CPR = RBY / 16;
-  constexpr int ROOM = NST * STAGE / NW, PB = 16 * FM * RBY <= ROOM ? FM : FM / 2;
-  constexpr int PER = STAGE / (PB * 16 * RBY);  // parts in a stage
-  static_assert(PB * 16 * RBY <= ROOM && NW <= NST * PER && 64 % CPR == 0, "epilogue");
-  uint8_t* const reg = sts[wave / PER] + wave % PER * (PB * 16 * RBY);
+  constexpr int ROOM = STAGE / 4, PB = 16 * FM * RBY <= ROOM ? FM : FM / 2;
+  static_assert(PB * 16 * RBY <= ROOM && NW <= 8 && 64 % CPR == 0, "epilogue");
+  const LmStage& own = wave < 4 ? s0 : s1;
+  uint8_t* const reg = (wave & 3) < 2 ? own.w + (wave & 1) * ROOM
+                       : NST > 2      ? own.x0 + (wave & 1) * ROOM
+                                      : (wave & 1 ? own.x1 : own.x0);
   __syncthreads();  // the last stages have been read
   f32x4 bias[FN];
 #pragma unroll
@@ -845,15 +886,20 @@ __device__ __forceinline__ void lm_tile(const LmMm& p, const LmPlace& t, uint8_t
 template <bool F16, bool BT, int WM, int WN, int FM, int FN, int NST, typename OutT>
 __global__ __launch_bounds__(64 * WM * WN)
     __attribute__((amdgpu_waves_per_eu(2, 2))) void lm_mm_kernel(LmMm p) {
-  constexpr int BM = 16 * FM * WM, BN = 16 * FN * WN, STAGE = (BM + BN) * 128;
-  __shared__ __attribute__((aligned(16))) uint8_t s0[STAGE];
-  __shared__ __attribute__((aligned(16))) uint8_t s1[STAGE];
-  __shared__ __attribute__((aligned(16))) uint8_t s2[NST >= 3 ? STAGE : 16];
-  __shared__ __attribute__((aligned(16))) uint8_t s3[NST == 4 ? STAGE : 16];
+  constexpr int BM = 16 * FM * WM, BN = 16 * FN * WN, X = BM * 128, W = BN * 128;
   __shared__ i32x2 s_order[BM];
   const LmPlace t = lm_place<BM, BN>(p);
   if (t.rows == 0) return;
-  lm_tile<F16, BT, false, WM, WN, FM, FN, NST, OutT>(p, t, s0, s1, s2, s3, s_order);
+  if constexpr (NST == 2) {
+    static_assert(BM == BN, "the parts of a stage");
+    __shared__ __attribute__((aligned(16))) uint8_t w0[W], w1[W], e0[X / 2], e1[X / 2], o0[X / 2], o1[X / 2];
+    const LmStage s0{w0, e0, o0}, s1{w1, e1, o1};
+    lm_tile<F16, BT, false, WM, WN, FM, FN, NST, OutT>(p, t, s0, s1, s0, s1, s_order);
+  } else {
+    __shared__ __attribute__((aligned(16))) uint8_t a0[X + W], a1[X + W], a2[X + W], a3[NST == 4 ? X + W : 16];
+    const LmStage s0{a0 + X, a0, a0}, s1{a1 + X, a1, a1}, s2{a2 + X, a2, a2}, s3{a3 + (NST == 4 ? X : 0), a3, a3};
+    lm_tile<F16, BT, false, WM, WN, FM, FN, NST, OutT>(p, t, s0, s1, s2, s3, s_order);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -983,11 +1029,13 @@ __global__ __launch_bounds__(256) void lm_parts_kernel(LmSmall p) {
     const int split = block / p.tiles, tile = block % p.tiles;
     const int mt = (p.T + 63) / 64, all = (p.mm.k + LM_BK - 1) / LM_BK;
     const int k0 = all * split / p.splits, k1 = all * (split + 1) / p.splits;
+    auto stage = [](uint8_t* s) { return LmStage{s + STAGE / 2, s, s}; };
     LmMm mm = p.mm;
     mm.out = static_cast<float*>(p.mm.out) + static_cast<int64_t>(split) * p.T * mm.n;
     const int m0 = tile % mt * 64, n0 = tile / mt * 64;
     lm_tile<F16, BT, true, 2, 2, 2, 2, 4, float>(
-        mm, {m0, n0, min(p.T - m0, 64), min(mm.n - n0, 64), k0, k1 - k0}, s0, s1, s2, s3, s_order);
+        mm, {m0, n0, min(p.T - m0, 64), min(mm.n - n0, 64), k0, k1 - k0}, stage(s0), stage(s1), stage(s2),
+        stage(s3), s_order);
     return;
   }
   const int wave = (block - p.gemm) * 4 + (threadIdx.x >> 6), waves = p.dots * 4;
