@@ -281,6 +281,9 @@ __device__ __forceinline__ u32x4 lm_column(const uint8_t* first, const uint8_t* 
   return u32x4{x[0], x[1], y[0], y[1]};
 }
 
+// chunk c (16 bytes) of LDS row R sits at slot c ^ lm_swz(R)
+__device__ __forceinline__ int lm_swz(int row) { return (row & 7) ^ ((row >> 3) & 1); }
+
 // ---------------------------------------------------------------------------
 // shrink: one item's rows times its adapter's matrix.
 //   BT == false: bank [L, R, C], v[t, r] = sum_c x[t, c] bank[l, r, c]
@@ -301,27 +304,35 @@ struct LmShrink {
   int T, C, L, R, RP, slots;
 };
 
-constexpr int SH_W = 8;
+// Loads go straight into LDS, a line of 128 bytes of each row at a time, and from there
+// into MFMA operands; a wavefront has its own stages, ST steps of them in flight, and no
+// barrier.  (Loads straight into operand registers touch half a line of 16 rows an
+// instruction: 8192 rows, 4096 columns, rank 16: 28 us against 20, rank 64: 34 against 23.)
+template <int NB>
+struct LmShape {
+  static constexpr int W = NB <= 2 ? 8 : 4;                  // wavefronts
+  static constexpr int ST = NB == 2 ? 2 : 3;                 // stages
+  static constexpr int X = LM_ITEM * 128, BYTES = X + NB * 2048;  // of a wavefront's stage
+};
 
 template <bool F16, bool BT, int NB>
-__global__ __launch_bounds__(64 * SH_W) void lm_shrink_kernel(LmShrink a) {
-  constexpr int FM = LM_ITEM / 16;
-  __shared__ __attribute__((aligned(16))) uint8_t s_buf[SH_W * 64 * NB * 32];
-  static_assert(64 * NB * 32 >= FM * NB * 64 * 16, "the sums fit the stages");
+__device__ __forceinline__ void lm_shrink(const LmShrink& a, uint8_t* s0, uint8_t* s1, uint8_t* s2, f32x4* red) {
+  using Shape = LmShape<NB>;
+  constexpr int FM = LM_ITEM / 16, W = Shape::W, ST = Shape::ST, NX = LM_ITEM / 8, CPR = 2 * NB, NI = NX + CPR;
   const int item = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
   const int* const slots = a.plan.slot_row + item * LM_ITEM;
   const int R = a.R, rank0 = blockIdx.y * 16 * NB;
   // all that the plan says of the item at once (past the last item it is not used)
   const i32x4 totals = gld<i32x4>(a.plan.totals);
-  const int l = gld<int>(a.plan.item_id + item);
-  const int r = lane & 15, g = lane >> 4;
-  int row_of[FM];
+  const int l = __builtin_amdgcn_readfirstlane(gld<int>(a.plan.item_id + item));
+  const int r = lane & 15, g = lane >> 4, lr = lane >> 3;
+  int row_of[NX];
 #pragma unroll
-  for (int i = 0; i < FM; ++i) row_of[i] = gld<int>(slots + 16 * i + r);
+  for (int i = 0; i < NX; ++i) row_of[i] = gld<int>(slots + 8 * i + lr);
   if (item >= totals.z) return;
   if (item >= totals.x) {  // rows without an adapter: zeros for activations
     if (a.out != nullptr)
-      for (int q = tid; q < LM_ITEM * NB * 4; q += 64 * SH_W) {
+      for (int q = tid; q < LM_ITEM * NB * 4; q += 64 * W) {
         const int t = gld<int>(slots + q / (NB * 4)), rk = rank0 + q % (NB * 4) * 4;
         if (t >= 0 && rk < R) gst<f32x4>(a.out + static_cast<int64_t>(t) * R + rk, f32x4{0.f, 0.f, 0.f, 0.f});
       }
@@ -334,44 +345,38 @@ __global__ __launch_bounds__(64 * SH_W) void lm_shrink_kernel(LmShrink a) {
   const __amdgpu_buffer_rsrc_t br =
       buf_rsrc(static_cast<const uint16_t*>(a.bank) + static_cast<int64_t>(l) * R * C,
                static_cast<uint32_t>(R) * static_cast<uint32_t>(C) * 2u);
-  // lane (r, g) has chunks g and g + 4 of a step of row r
-  uint32_t vx[FM];
+  // instruction i of x: rows 8 i .. 8 i + 7, lane (row, slot) the chunk that the slot holds
+  uint32_t vx[NX], vb[CPR];
+  uint32_t cx[2];  // byte of a row's step that this lane's chunk starts at, even and odd i
 #pragma unroll
-  for (int i = 0; i < FM; ++i) {
-    vx[i] = row_of[i] >= 0 ? static_cast<uint32_t>(row_of[i]) * C * 2 + g * 16 : LM_OUT;
-  }
-  const bool two = __builtin_amdgcn_readfirstlane(row_of[1]) >= 0;  // any rows in block 1
-  constexpr int CPR = 2 * NB;  // BT: 16-byte pieces of a bank's row
-  uint32_t vb[CPR];
+  for (int i = 0; i < 2; ++i) cx[i] = ((lane & 7) ^ lr ^ i) * 16;
+#pragma unroll
+  for (int i = 0; i < NX; ++i)
+    vx[i] = row_of[i] >= 0 ? static_cast<uint32_t>(row_of[i]) * C * 2 + cx[i & 1] : LM_OUT;
 #pragma unroll
   for (int i = 0; i < CPR; ++i) {
-    if constexpr (BT) {
+    if constexpr (BT) {  // 64 rows of CPR chunks
       const int at = i * 64 + lane, rk = rank0 + at % CPR * 8;
       vb[i] = rk < R ? (static_cast<uint32_t>(at / CPR) * R + rk) * 2 : LM_OUT;
     } else {
-      const int rk = rank0 + 16 * (i >> 1) + r;
-      vb[i] = rk < R ? static_cast<uint32_t>(rk) * C * 2 + g * 16 + 64 * (i & 1) : LM_OUT;
+      const int rk = rank0 + 8 * i + lr;
+      vb[i] = rk < R ? static_cast<uint32_t>(rk) * C * 2 + cx[i & 1] : LM_OUT;
     }
   }
-  struct Step { u32x4 x[FM][2], b[CPR]; };
-  auto load = [&](Step& q, int kt) {  // a step past the last loads zeros
+  auto load = [&](uint8_t* st, int kt) {  // a step past the last loads zeros
     const int kb = min(kt, KT - 1);
     const uint32_t so = __builtin_amdgcn_readfirstlane(kb * (LM_BK * 2));
+    uint32_t drop[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t drop = kt < KT && kb * LM_BK + 32 * h + 8 * g < C ? 0u : LM_OUT;
+    for (int i = 0; i < 2; ++i) drop[i] = kt < KT && so + cx[i] < static_cast<uint32_t>(C) * 2 ? 0u : LM_OUT;
 #pragma unroll
-      for (int i = 0; i < FM; ++i)
-        if (i == 0 || two) q.x[i][h] = buf_ld128(xr, (vx[i] + 64 * h) | drop, so);
-      if constexpr (!BT)
+    for (int i = 0; i < NX; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, lm_lds(st + i * 1024), 16, vx[i] | drop[i & 1], so, 0, 0);
+    const uint32_t sob = BT ? __builtin_amdgcn_readfirstlane(kb * (LM_BK * 2) * R) : so;
 #pragma unroll
-        for (int j = 0; j < NB; ++j) q.b[2 * j + h] = buf_ld128(br, vb[2 * j + h] | drop, so);
-    }
-    if constexpr (BT) {
-      const uint32_t sob = __builtin_amdgcn_readfirstlane(kb * (LM_BK * 2) * R);
-#pragma unroll
-      for (int i = 0; i < CPR; ++i)
-        q.b[i] = buf_ld128(br, kt < KT && kb * LM_BK + (i * 64 + lane) / CPR < C ? vb[i] : LM_OUT, sob);
+    for (int i = 0; i < CPR; ++i) {
+      const uint32_t d = !BT ? drop[i & 1] : kt < KT && kb * LM_BK + (i * 64 + lane) / CPR < C ? 0u : LM_OUT;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(br, lm_lds(st + Shape::X + i * 1024), 16, vb[i] | d, sob, 0, 0);
     }
   };
   f32x4 acc[FM][NB];
@@ -379,47 +384,49 @@ __global__ __launch_bounds__(64 * SH_W) void lm_shrink_kernel(LmShrink a) {
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  uint8_t* const st = s_buf + wave * (64 * NB * 32);  // BT: this wavefront's 64 rows of ranks
-  auto add = [&](const Step& q) {
-    if constexpr (BT) {
-      __builtin_amdgcn_wave_barrier();
+  const int ck = ((g & 1) << 1) | (g >> 1);
+  auto add = [&](uint8_t* st, int next) {
+    __builtin_amdgcn_s_waitcnt((((ST - 1) * NI) & 15) | ((((ST - 1) * NI) >> 4) << 14) | (15 << 8) | (7 << 4));
+    asm volatile("" ::: "memory");
+    u32x4 fx[FM][2], fb[NB][2];
 #pragma unroll
-      for (int i = 0; i < CPR; ++i) *reinterpret_cast<u32x4*>(st + (i * 64 + lane) * 16) = q.b[i];
-      __builtin_amdgcn_wave_barrier();
-    }
+    for (int h = 0; h < 2; ++h) {
+      const int at = r * 128 + ((ck + 4 * h) ^ lm_swz(r)) * 16;
 #pragma unroll
-    for (int j = 0; j < NB; ++j)
+      for (int i = 0; i < FM; ++i) fx[i][h] = *reinterpret_cast<const u32x4*>(st + i * 2048 + at);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        u32x4 fb;
+      for (int j = 0; j < NB; ++j) {
         if constexpr (BT) {
-          const uint8_t* at = st + (32 * h + 8 * g + (r >> 2)) * (NB * 32) + j * 32 + (r & 3) * 8;
-          fb = lm_column(at, at + 4 * NB * 32);
+          const uint8_t* b = st + Shape::X + (8 * ck + 32 * h + (r >> 2)) * (NB * 32) + j * 32 + (r & 3) * 8;
+          fb[j][h] = lm_column(b, b + 4 * NB * 32);
         } else {
-          fb = q.b[2 * j + h];
+          fb[j][h] = *reinterpret_cast<const u32x4*>(st + Shape::X + j * 2048 + at);
         }
-#pragma unroll
-        for (int i = 0; i < FM; ++i)
-          if (i == 0 || two) acc[i][j] = lm_mfma<F16>(fb, q.x[i][h], acc[i][j]);
       }
-  };
-  constexpr int P = NB == 1 ? 4 : NB == 2 ? 3 : 2;  // steps in flight
-  Step q[P];
-#pragma unroll
-  for (int u = 0; u < P; ++u) {
-    load(q[u], wave + SH_W * u);
-    __builtin_amdgcn_sched_barrier(0);
-  }
-  for (int kt = wave; kt < KT; kt += SH_W * P) {
-#pragma unroll
-    for (int u = 0; u < P; ++u) {
-      add(q[u]);
-      load(q[u], kt + SH_W * (u + P));
-      __builtin_amdgcn_sched_barrier(0);
     }
+    // the stage is free once its reads have returned
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    load(st, next);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int i = 0; i < FM; ++i) acc[i][j] = lm_mfma<F16>(fb[j][h], fx[i][h], acc[i][j]);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  uint8_t* const sts[3] = {s0 + wave * Shape::BYTES, s1 + wave * Shape::BYTES, s2 + wave * Shape::BYTES};
+#pragma unroll
+  for (int u = 0; u < ST; ++u) load(sts[u], wave + W * u);
+  for (int kt = wave; kt < KT; kt += W * ST) {
+#pragma unroll
+    for (int u = 0; u < ST; ++u) add(sts[u], kt + W * (u + ST));
   }
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // the steps past the last have written their zeros
   __syncthreads();
-  f32x4* const red = reinterpret_cast<f32x4*>(s_buf);
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -427,10 +434,10 @@ __global__ __launch_bounds__(64 * SH_W) void lm_shrink_kernel(LmShrink a) {
   __syncthreads();
   // quad: ranks 16 j + 4 g .. of slot 16 i + r
   const float s = a.scale != nullptr ? gld<float>(a.scale + l) : 1.f;
-  for (int at = tid; at < FM * NB * 64; at += 64 * SH_W) {
+  for (int at = tid; at < FM * NB * 64; at += 64 * W) {
     f32x4 v = red[at];
 #pragma unroll
-    for (int w = 1; w < SH_W; ++w) v += red[w * FM * NB * 64 + at];
+    for (int w = 1; w < W; ++w) v += red[w * FM * NB * 64 + at];
     const int j = (at >> 6) % NB, in = at / (64 * NB) * 16 + (at & 15);
     const int rk = rank0 + 16 * j + 4 * ((at & 63) >> 4);
     if (rk >= a.RP) continue;
@@ -463,6 +470,15 @@ __global__ __launch_bounds__(64 * SH_W) void lm_shrink_kernel(LmShrink a) {
   }
 }
 
+template <bool F16, bool BT, int NB>
+__global__ __launch_bounds__(64 * LmShape<NB>::W) void lm_shrink_kernel(LmShrink a) {
+  // a stage its own array: the compiler then knows which loads a read waits for
+  constexpr int SIZE = LmShape<NB>::W * LmShape<NB>::BYTES;
+  __shared__ __attribute__((aligned(16))) uint8_t s0[SIZE], s1[SIZE], s2[LmShape<NB>::ST == 3 ? SIZE : 16];
+  static_assert(LmShape<NB>::W * LM_ITEM / 16 * NB * 1024 <= SIZE, "the sums fit a stage");
+  lm_shrink<F16, BT, NB>(a, s0, s1, s2, reinterpret_cast<f32x4*>(s0));
+}
+
 // ---------------------------------------------------------------------------
 // mm: out = x w^T (BT: x w) plus the pieces times the adapters' matrix
 //   BT == false: w [n, k], bank [L, n, R]
@@ -479,8 +495,6 @@ struct LmMm {
   int T, k, n, L, R, RP;
 };
 
-// chunk c (16 bytes) of LDS row R sits at slot c ^ lm_swz(R)
-__device__ __forceinline__ int lm_swz(int row) { return (row & 7) ^ ((row >> 3) & 1); }
 // 32-byte pieces of a transposed tile's row (BN / 16 of them): the 16 rows that a
 // transposed read touches lie in 8 different ones of 256 bytes
 template <int BN>
@@ -735,7 +749,8 @@ __device__ __forceinline__ void lm_tile(const LmMm& p, const LmPlace& t, LmStage
     const int l = at < rows ? __builtin_amdgcn_readfirstlane(s_order[at].y) : p.L;
     // the rows without an adapter are last
     if (l >= p.L) return Run{p.L, rows, rows, 0};
-    return Run{l, at, max(min(gld<int>(p.plan.seg + l + 1) - m0, rows), at + 1), 0};
+    const int end = __builtin_amdgcn_readfirstlane(gld<int>(p.plan.seg + l + 1)) - m0;
+    return Run{l, at, max(min(end, rows), at + 1), 0};
   };
   auto after = [&](const Run& u) { return u.e + LM_BK < E ? Run{u.l, u.at, u.end, u.e + LM_BK} : run_at(u.end); };
   const __amdgpu_buffer_rsrc_t pr_ =
@@ -1274,7 +1289,9 @@ __global__ __launch_bounds__(256) void lm_grad_kernel(LmGrad ga, LmGrad gb) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[2 * GR_STAGE];
   const int chunk = blockIdx.y;
   if (chunk >= gld<int>(ga.plan.totals + 1)) return;
-  const i32x4 ch = gld<i32x4>(ga.plan.chunks + chunk);
+  i32x4 ch = gld<i32x4>(ga.plan.chunks + chunk);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) ch[i] = __builtin_amdgcn_readfirstlane(ch[i]);
   const int pa = (ga.C + GR_BN - 1) / GR_BN;
   const int rank0 = blockIdx.z * 16 * NB;
   if (static_cast<int>(blockIdx.x) < pa)
@@ -1425,12 +1442,12 @@ mi_status lm_plan(const LmSizes& s, int64_t rows, const int32_t* ids, const LmPl
 }
 
 template <bool F16, bool BT>
-mi_status lm_shrink(const LmShrink& a, int64_t items, hipStream_t st) {
+mi_status lm_shrink_run(const LmShrink& a, int64_t items, hipStream_t st) {
   const int nb = a.RP / 16;
 #define LM_SHRINK(NB_)                                                                              \
   hipLaunchKernelGGL((lm_shrink_kernel<F16, BT, NB_>),                                              \
                      dim3(static_cast<unsigned>(items), static_cast<unsigned>((nb + NB_ - 1) / NB_)), \
-                     dim3(64 * SH_W), 0, st, a)
+                     dim3(64 * LmShape<NB_>::W), 0, st, a)
   if (nb == 1) LM_SHRINK(1);
   else if (nb == 2) LM_SHRINK(2);
   else LM_SHRINK(4);
@@ -1562,7 +1579,7 @@ extern "C" mi_status mi_mm_lora(const void* x, int64_t m, int64_t k, mi_dtype dt
     a.R = static_cast<int>(rank);
     a.RP = static_cast<int>(s.rp());
     const int64_t items = LmSizes::items(rows, num_adapters);
-    st = dtype == MI_F16 ? lm_shrink<true, false>(a, items, hs) : lm_shrink<false, false>(a, items, hs);
+    st = dtype == MI_F16 ? lm_shrink_run<true, false>(a, items, hs) : lm_shrink_run<false, false>(a, items, hs);
     if (st != MI_OK) return st;
     LmMm p{};
     p.x = a.x;
@@ -1689,7 +1706,7 @@ extern "C" mi_status mi_mm_lora_backward(const void* grad_out, const void* x, in
       a.bank = lora_a;
       a.C = static_cast<int>(k);
       a.out = sp.act;
-      st = f16 ? lm_shrink<true, false>(a, items, hs) : lm_shrink<false, false>(a, items, hs);
+      st = f16 ? lm_shrink_run<true, false>(a, items, hs) : lm_shrink_run<false, false>(a, items, hs);
       if (st != MI_OK) return st;
       v = sp.act;
     }
@@ -1704,7 +1721,7 @@ extern "C" mi_status mi_mm_lora_backward(const void* grad_out, const void* x, in
       a.pieces_t = sp.ut;
       a.pieces_t2 = sp.vt;
     }
-    st = f16 ? lm_shrink<true, true>(a, items, hs) : lm_shrink<false, true>(a, items, hs);
+    st = f16 ? lm_shrink_run<true, true>(a, items, hs) : lm_shrink_run<false, true>(a, items, hs);
     if (st != MI_OK) return st;
     if (grad_x != nullptr) {
       LmMm p{};
