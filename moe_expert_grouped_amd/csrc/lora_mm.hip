@@ -295,7 +295,7 @@ struct LmShrink {
   const void* x;          // [T, C]
   const void* bank;
   const float* scale;     // [L] or null
-  const float* act;       // [T, R]: also split these into pieces_t2, or null
+  const float* act;       // [T, R]: split into pieces_t2 beside pieces_t
   LmPlan plan;
   float* out;             // [T, R] unscaled, or null
   uint16_t* pieces;       // [T, 3 RP] scaled, or null
@@ -432,6 +432,9 @@ __device__ __forceinline__ void lm_shrink(const LmShrink& a, uint8_t* s0, uint8_
 #pragma unroll
     for (int j = 0; j < NB; ++j) red[((wave * FM + i) * NB + j) * 64 + lane] = acc[i][j];
   __syncthreads();
+  constexpr int LM_COLS = LM_ITEM + 1;
+  static_assert(16 * NB * LM_COLS * 4 * 2 <= W * Shape::BYTES, "columns in a stage");
+  float* const cols[2] = {reinterpret_cast<float*>(s1), reinterpret_cast<float*>(s1) + 16 * NB * LM_COLS};
   // quad: ranks 16 j + 4 g .. of slot 16 i + r
   const float s = a.scale != nullptr ? gld<float>(a.scale + l) : 1.f;
   for (int at = tid; at < FM * NB * 64; at += 64 * W) {
@@ -443,29 +446,47 @@ __device__ __forceinline__ void lm_shrink(const LmShrink& a, uint8_t* s0, uint8_
     if (rk >= a.RP) continue;
     const int slot = item * LM_ITEM + in, t = gld<int>(slots + in);
     const bool here = t >= 0 && rk < R;
-    auto put = [&](f32x4 w, uint16_t* rows, uint16_t* cols) {
+    const f32x4 none = {0.f, 0.f, 0.f, 0.f};
+    if (a.out != nullptr && here) gst<f32x4>(a.out + static_cast<int64_t>(t) * R + rk, v);
+    if (a.pieces != nullptr && t >= 0) {
       LmPieces p[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) p[i] = lm_pieces(here ? w[i] * s : 0.f);
+      for (int i = 0; i < 4; ++i) p[i] = lm_pieces(here ? v[i] * s : 0.f);
 #pragma unroll
-      for (int c = 0; c < 3; ++c) {
-        if (rows != nullptr && t >= 0)
-          gst<u32x2>(rows + (static_cast<int64_t>(t) * 3 + c) * a.RP + rk,
-                     u32x2{p[0].p[c] | static_cast<uint32_t>(p[1].p[c]) << 16,
-                           p[2].p[c] | static_cast<uint32_t>(p[3].p[c]) << 16});
-        if (cols != nullptr)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            gst<uint16_t>(cols + (static_cast<int64_t>(c) * a.RP + rk + i) * a.slots + slot,
-                          p[i].p[c]);
-      }
-    };
-    if (a.out != nullptr && here) gst<f32x4>(a.out + static_cast<int64_t>(t) * R + rk, v);
-    if (a.pieces != nullptr || a.pieces_t != nullptr) put(v, a.pieces, a.pieces_t);
-    if (a.act != nullptr) {
-      f32x4 w = {0.f, 0.f, 0.f, 0.f};
+      for (int c = 0; c < 3; ++c)
+        gst<u32x2>(a.pieces + (static_cast<int64_t>(t) * 3 + c) * a.RP + rk,
+                   u32x2{p[0].p[c] | static_cast<uint32_t>(p[1].p[c]) << 16,
+                         p[2].p[c] | static_cast<uint32_t>(p[3].p[c]) << 16});
+    }
+    if (a.pieces_t != nullptr) {
+      f32x4 w = none;
       if (here) w = gld<f32x4>(a.act + static_cast<int64_t>(t) * R + rk);
-      put(w, nullptr, a.pieces_t2);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        cols[0][(16 * j + 4 * ((at & 63) >> 4) + i) * LM_COLS + in] = here ? v[i] * s : 0.f;
+        cols[1][(16 * j + 4 * ((at & 63) >> 4) + i) * LM_COLS + in] = here ? w[i] * s : 0.f;
+      }
+    }
+  }
+  if (a.pieces_t == nullptr) return;
+  // down the columns: 8 slots of a rank at a time
+  __syncthreads();
+  for (int q = tid; q < 2 * 16 * NB * (LM_ITEM / 8); q += 64 * W) {
+    const int which = q / (16 * NB * (LM_ITEM / 8)), rank = q / (LM_ITEM / 8) % (16 * NB), in = q % (LM_ITEM / 8) * 8;
+    if (rank0 + rank >= a.RP) continue;
+    uint16_t part[3][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const LmPieces p = lm_pieces(cols[which][rank * LM_COLS + in + i]);
+#pragma unroll
+      for (int c = 0; c < 3; ++c) part[c][i] = p.p[c];
+    }
+    uint16_t* const to = which ? a.pieces_t2 : a.pieces_t;
+#pragma unroll
+    for (int c = 0; c < 3; ++c) {
+      u32x4 raw;
+      __builtin_memcpy(&raw, part[c], 16);
+      gst<u32x4>(to + (static_cast<int64_t>(c) * a.RP + rank0 + rank) * a.slots + item * LM_ITEM + in, raw);
     }
   }
 }
@@ -1184,7 +1205,8 @@ __global__ __launch_bounds__(256) void lm_finish_kernel(LmSmall p) {
 // grads: for a chunk of an adapter's rows, 128 columns of x (or go) and 16 NB ranks,
 //   ROWS == false: ga[l, r, c] = sum_t u[t, r] x[t, c]
 //   ROWS == true:  gb[l, c, r] = sum_t v[t, r] go[t, c]
-// from the transposed pieces.  Stages of 64 rows of x; a wavefront has 32 columns.
+// A step is 64 rows: those of x, and 64 slots of the transposed pieces, both by loads
+// straight into LDS; x is read down its columns.  A wavefront has 32 columns.
 // ---------------------------------------------------------------------------
 struct LmGrad {
   const void* x;             // [T, C]
@@ -1195,29 +1217,44 @@ struct LmGrad {
   int C, R, RP, slots;
 };
 
-constexpr int GR_BN = 128, GR_BK = 64, GR_STAGE = GR_BK * GR_BN * 2;
+constexpr int GR_BN = 128, GR_BK = 64, GR_X = GR_BK * GR_BN * 2;
+constexpr int GR_ROWS = 2048;  // rows of a chunk at most
+template <int NB>
+struct LmGradShape {
+  static constexpr int PI = (6 * NB + 3) / 4;   // a wavefront's loads of pieces: 8 rows of 64 slots each
+  static constexpr int BYTES = GR_X + PI * 4096;
+  static constexpr int ST = NB == 2 ? 2 : 3;    // stages; with two a second workgroup fits
+};
 
 template <bool F16, bool ROWS, int NB, typename OutT>
-__device__ __forceinline__ void lm_grad(const LmGrad& a, uint8_t* smem, i32x4 ch, int c0, int rank0) {
+__device__ __forceinline__ void lm_grad(const LmGrad& a, uint8_t* st0, uint8_t* st1, uint8_t* st2,
+                                        const int* s_rows, i32x4 ch, int c0, int rank0) {
+  using Shape = LmGradShape<NB>;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int r = lane & 15, g = lane >> 4;
-  const int C = a.C, R = a.R;
-  const int s0 = ch.y * LM_ITEM, s1 = s0 + ch.z * LM_ITEM;  // slots
-  const int KT = (s1 - s0 + GR_BK - 1) / GR_BK;
-  constexpr int CPW = GR_BN / 8, NI = GR_STAGE / 1024 / 4;  // 4 rows an instruction, 4 instructions
-  auto dma = [&](int st, int kt) {
+  const int r = lane & 15, g = lane >> 4, lr = lane >> 3;
+  const int C = a.C, R = a.R, RP = a.RP;
+  const int s0 = ch.y * LM_ITEM, n = ch.z * LM_ITEM, KT = (n + GR_BK - 1) / GR_BK;  // slots
+  constexpr int CPW = GR_BN / 8, NX = GR_X / 1024 / 4, PI = Shape::PI, ST = Shape::ST;
+  const uint16_t* const x = static_cast<const uint16_t*>(a.x);
+  const int chunk = (lane & 7) ^ lr;
+  auto load = [&](uint8_t* st, int kt) {
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
+    for (int i = 0; i < NX; ++i) {
       const int at = (4 * i + wave) * 64 + lane, row = at / CPW, c = at % CPW;
       const int col = c0 + (((c >> 1) ^ lm_tswz<GR_BN>(row)) * 2 + (c & 1)) * 8;
-      const int slot = s0 + kt * GR_BK + row;
-      const int t = slot < s1 ? gld<int>(a.plan.slot_row + slot) : -1;
-      const uint16_t* src = t >= 0 && col < C
-                                ? static_cast<const uint16_t*>(a.x) + static_cast<int64_t>(t) * C + col
-                                : a.plan.zeros;
-      __builtin_amdgcn_global_load_lds((const MI_GLOBAL void*)(src),
-                                       lm_lds(smem + st * GR_STAGE + (4 * i + wave) * 1024), 16, 0, 0);
+      const int t = kt * GR_BK + row < n ? s_rows[kt * GR_BK + row] : -1;
+      const uint16_t* src = t >= 0 && col < C ? x + static_cast<int64_t>(t) * C + col : a.plan.zeros;
+      __builtin_amdgcn_global_load_lds((const MI_GLOBAL void*)(src), lm_lds(st + (4 * i + wave) * 1024), 16, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < PI; ++i) {
+      // rows 8 (PI wave + i) .. of [rank block][piece][16 ranks]
+      const int row = 8 * (PI * wave + i) + lr, b = row / 48, c = row / 16 % 3, rk = rank0 + 16 * b + (row & 15);
+      const int slot = kt * GR_BK + (chunk ^ ((row >> 3) & 1)) * 8;
+      const uint16_t* src = b < NB && rk < RP && slot < n
+                                ? a.pieces_t + (static_cast<int64_t>(c) * RP + rk) * a.slots + s0 + slot : a.plan.zeros;
+      __builtin_amdgcn_global_load_lds((const MI_GLOBAL void*)(src), lm_lds(st + GR_X + (PI * wave + i) * 1024), 16, 0, 0);
     }
   };
   f32x4 acc[NB][2];
@@ -1225,31 +1262,23 @@ __device__ __forceinline__ void lm_grad(const LmGrad& a, uint8_t* smem, i32x4 ch
   for (int b = 0; b < NB; ++b)
 #pragma unroll
     for (int j = 0; j < 2; ++j) acc[b][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  if (KT > 0) dma(0, 0);
-  for (int kt = 0; kt < KT; ++kt) {
-    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
-    __syncthreads();
-    if (kt + 1 < KT) dma((kt + 1) & 1, kt + 1);
-    const uint8_t* st = smem + (kt & 1) * GR_STAGE;
+  auto add = [&](const uint8_t* st) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
+      const int ck = (((g & 1) << 1) | (g >> 1)) + 4 * h;  // this lane's 8 slots
       u32x4 fx[2], fl[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int pc = wave * 2 + j, row = 32 * h + 8 * g + (r >> 2), row2 = row + 4;
-        fx[j] = lm_column(st + row * (GR_BN * 2) + (pc ^ lm_tswz<GR_BN>(row)) * 32 + (r & 3) * 8,
-                          st + row2 * (GR_BN * 2) + (pc ^ lm_tswz<GR_BN>(row2)) * 32 + (r & 3) * 8);
+        const int row = 8 * ck + (r >> 2);
+        const uint8_t* at = st + row * (GR_BN * 2) + ((wave * 2 + j) ^ lm_tswz<GR_BN>(row)) * 32 + (r & 3) * 8;
+        fx[j] = lm_column(at, at + 4 * GR_BN * 2);
         if constexpr (F16) lm_split(fx[j], fx[j], fl[j]);
       }
-      const int slot = s0 + kt * GR_BK + 32 * h + 8 * g;
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const int rk = rank0 + 16 * b + r;
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int c = 0; c < 3; ++c) {
-          u32x4 fp = {0, 0, 0, 0};
-          if (slot < s1 && rk < a.RP)
-            fp = gld<u32x4>(a.pieces_t + (static_cast<int64_t>(c) * a.RP + rk) * a.slots + slot);
+          const u32x4 fp = *reinterpret_cast<const u32x4*>(st + GR_X + (b * 3 + c) * 2048 + r * 128 + (ck ^ lm_swz(r)) * 16);
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             acc[b][j] = ROWS ? lm_mfma<false>(fp, fx[j], acc[b][j]) : lm_mfma<false>(fx[j], fp, acc[b][j]);
@@ -1259,9 +1288,31 @@ __device__ __forceinline__ void lm_grad(const LmGrad& a, uint8_t* smem, i32x4 ch
             }
           }
         }
-      }
     }
+  };
+  // a step past the last loads zeros
+  constexpr int NI = NX + PI;
+  load(st0, 0);
+  if constexpr (ST == 3) load(st1, 1);
+  for (int kt = 0; kt < KT; kt += ST) {
+#define LM_STEP(S_, ST_, TO_)                        \
+  if constexpr (S_ < ST) {                           \
+    lm_wait_barrier<(ST - 2) * NI>();                \
+    load(TO_, kt + S_ + ST - 1);                     \
+    add(ST_);                                        \
+    if (kt + S_ + 1 >= KT) break;                    \
   }
+    if constexpr (ST == 3) {
+      LM_STEP(0, st0, st2)
+      LM_STEP(1, st1, st0)
+      LM_STEP(2, st2, st1)
+    } else {
+      LM_STEP(0, st0, st1)
+      LM_STEP(1, st1, st0)
+    }
+#undef LM_STEP
+  }
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): no load writes to LDS after the end
   // four ranks of column r (ROWS), or four columns of rank r
 #pragma unroll
   for (int b = 0; b < NB; ++b)
@@ -1286,18 +1337,22 @@ __device__ __forceinline__ void lm_grad(const LmGrad& a, uint8_t* smem, i32x4 ch
 
 template <bool F16, int NB, typename OutT>
 __global__ __launch_bounds__(256) void lm_grad_kernel(LmGrad ga, LmGrad gb) {
-  __shared__ __attribute__((aligned(16))) uint8_t smem[2 * GR_STAGE];
+  constexpr int SIZE = LmGradShape<NB>::BYTES;
+  __shared__ __attribute__((aligned(16))) uint8_t st0[SIZE], st1[SIZE], st2[LmGradShape<NB>::ST == 3 ? SIZE : 16];
+  __shared__ int s_rows[GR_ROWS];
   const int chunk = blockIdx.y;
   if (chunk >= gld<int>(ga.plan.totals + 1)) return;
   i32x4 ch = gld<i32x4>(ga.plan.chunks + chunk);
 #pragma unroll
   for (int i = 0; i < 4; ++i) ch[i] = __builtin_amdgcn_readfirstlane(ch[i]);
+  for (int i = threadIdx.x; i < ch.z * LM_ITEM; i += 256) s_rows[i] = gld<int>(ga.plan.slot_row + ch.y * LM_ITEM + i);
+  __syncthreads();
   const int pa = (ga.C + GR_BN - 1) / GR_BN;
   const int rank0 = blockIdx.z * 16 * NB;
   if (static_cast<int>(blockIdx.x) < pa)
-    lm_grad<F16, false, NB, OutT>(ga, smem, ch, blockIdx.x * GR_BN, rank0);
+    lm_grad<F16, false, NB, OutT>(ga, st0, st1, st2, s_rows, ch, blockIdx.x * GR_BN, rank0);
   else
-    lm_grad<F16, true, NB, OutT>(gb, smem, ch, (blockIdx.x - pa) * GR_BN, rank0);
+    lm_grad<F16, true, NB, OutT>(gb, st0, st1, st2, s_rows, ch, (blockIdx.x - pa) * GR_BN, rank0);
 }
 
 template <typename OutT>
@@ -1338,10 +1393,15 @@ struct LmSizes {
     return T < most ? T : most;
   }
   static int64_t items(int64_t t, int64_t l) { return t / LM_ITEM + (l + 1 < t ? l + 1 : t) + 1; }
-  // items of a chunk: 512 rows, and no more than 32 chunks of a call's rows
+  // Items of a chunk: as many as leave 512 workgroups of the gradients' kernel, but 128 rows
+  // at least and 512 at most; of very many rows a 32nd of them up to GR_ROWS, which keeps the
+  // partial sums few
   int64_t chunk_items() const {
-    const int64_t i = (T + LM_ITEM * 32 - 1) / (LM_ITEM * 32);
-    return i < 512 / LM_ITEM ? 512 / LM_ITEM : i;
+    const int64_t panels = (K + GR_BN - 1) / GR_BN + (N + GR_BN - 1) / GR_BN;
+    int64_t rows = T * panels / 512;
+    if (rows > 512) rows = T / 32 < 512 ? 512 : T / 32;
+    rows = rows < 128 ? 128 : rows > GR_ROWS ? GR_ROWS : rows;
+    return rows / LM_ITEM;
   }
   int64_t chunks() const { return L + items(T, L) / chunk_items() + 1; }
   // those of adapters that have several: each but an adapter's last is full
