@@ -94,29 +94,31 @@ __device__ __forceinline__ uint64_t pl_peers(int v, int bits) {
   return peers;
 }
 
-// Two launches of a workgroup per chunk of rows (1024, or a 64th of them).  count: the
-// chunk's rows of every adapter, and each row's rank among them; a wavefront's rows go in
-// order, and the counts of the wavefronts before it are added.  place: every workgroup adds
-// the chunks' counts itself, which gives all places; the first writes the lists.
-__global__ __launch_bounds__(PL_T) void lm_count_kernel(const int32_t* __restrict__ ids, int T,
-                                                        int L, int chunk, LmPlan p) {
-  __shared__ int s_cnt[(LM_MAX_ADAPTERS + 1) * PL_S];  // an adapter's counts by wavefront
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int per = chunk / PL_W;
-  const int r0 = min(static_cast<int>(blockIdx.x) * chunk + wave * per, T), r1 = min(r0 + per, T);
+// Up to PL_ONE rows one workgroup does it all; beyond, two launches of a workgroup per
+// chunk of rows (1024, or a 64th of them).  count: the chunk's rows of every adapter, and
+// each row's rank among its wavefront's; a wavefront's rows go in order.  place: every
+// workgroup adds the chunks' counts itself, which gives all places; the first writes the
+// lists.  (us, one workgroup and two launches: 1111 rows 5.9 and 9.3, 8192 rows 13.4 and 10.5.)
+constexpr int PL_ONE = 4096;
+
+// Counts of the rows [r0, r1) of a wavefront, 64 at a time, into its column of s_cnt; f
+// gets every row's id and its rank among the wavefront's rows of that adapter.
+template <typename F>
+__device__ __forceinline__ void pl_count(const int32_t* ids, int r0, int r1, int L, int* s_cnt, F f) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   auto id_at = [&](int row) {
     const int id = row < r1 ? gld<int32_t>(ids + row) : L;
     return id < 0 || id > L ? L : id;
   };
-  const int first_id = id_at(r0 + lane);
+  int id = id_at(r0 + lane);
 #pragma unroll 1
-  for (int i = tid; i < (L + 1) * PL_S; i += PL_T) s_cnt[i] = 0;
+  for (int i = threadIdx.x; i < (L + 1) * PL_S; i += PL_T) s_cnt[i] = 0;
   __syncthreads();
   const int bits = 32 - __builtin_clz(L);  // ids 0 .. L
   int* const cnt = s_cnt + wave;           // of adapter l at l * PL_S
 #pragma unroll 1
   for (int at = r0; at < r1; at += 64) {
-    const int row = at + lane, id = at == r0 ? first_id : id_at(row);
+    const int row = at + lane, next = id_at(row + 64);
     // the lanes that hold the same id; a run's rows all do
     const uint64_t live = __ballot(row < r1);
     uint64_t peers = __ballot(id == __builtin_amdgcn_readfirstlane(id)) & live;
@@ -124,14 +126,16 @@ __global__ __launch_bounds__(PL_T) void lm_count_kernel(const int32_t* __restric
     const uint64_t below = peers & ((1ull << lane) - 1);
     if (row < r1) {
       const int before = cnt[id * PL_S];
-      gst<int>(p.rank + row, before + __popcll(below));
+      f(row, id, before + __popcll(below));
       if (below == 0) cnt[id * PL_S] = before + __popcll(peers);
     }
     // LDS operations of one wavefront complete in order
     __builtin_amdgcn_wave_barrier();
+    id = next;
   }
   __syncthreads();
-  for (int l = tid; l <= L; l += PL_T) {
+  // the wavefronts' counts become the counts before them; the sum behind them
+  for (int l = threadIdx.x; l <= L; l += PL_T) {
     int run = 0;
 #pragma unroll
     for (int w = 0; w < PL_W; ++w) {
@@ -139,34 +143,62 @@ __global__ __launch_bounds__(PL_T) void lm_count_kernel(const int32_t* __restric
       s_cnt[l * PL_S + w] = run;
       run += c;
     }
-    gst<int>(p.counts + static_cast<int64_t>(blockIdx.x) * (L + 1) + l, run);
+    s_cnt[l * PL_S + PL_W] = run;
   }
   __syncthreads();
-  if (wave == 0) return;  // nothing before it
+}
+
+__global__ __launch_bounds__(PL_T) void lm_count_kernel(const int32_t* __restrict__ ids, int T,
+                                                        int L, int chunk, LmPlan p) {
+  __shared__ int s_cnt[(LM_MAX_ADAPTERS + 1) * PL_S];
+  const int per = chunk / PL_W, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int r0 = min(static_cast<int>(blockIdx.x) * chunk + wave * per, T), r1 = min(r0 + per, T);
+  pl_count(ids, r0, r1, L, s_cnt, [&](int row, int, int rank) { gst<int>(p.rank + row, rank); });
+  for (int l = threadIdx.x; l <= L; l += PL_T)
+    gst<int>(p.counts + static_cast<int64_t>(blockIdx.x) * (L + 1) + l, s_cnt[l * PL_S + PL_W]);
 #pragma unroll 2
   for (int row = r0 + lane; row < r1; row += 64) {
-    const int id = row == r0 + lane ? first_id : id_at(row);
-    const int add = cnt[id * PL_S];
+    const int id = gld<int32_t>(ids + row), l = id < 0 || id > L ? L : id;
+    const int add = s_cnt[l * PL_S + wave];
     if (add) gst<int>(p.rank + row, gld<int>(p.rank + row) + add);
   }
 }
 
+template <bool ONE>
 __global__ __launch_bounds__(PL_T) void lm_place_kernel(const int32_t* __restrict__ ids, int T,
                                                         int L, int chunk, int chunk_items,
                                                         LmPlan p) {
+  __shared__ int s_cnt[ONE ? (LM_MAX_ADAPTERS + 1) * PL_S : 1];
   __shared__ int s_base[LM_MAX_ADAPTERS + 1];  // place of this chunk's first row
   __shared__ int s_seg[LM_MAX_ADAPTERS + 1], s_item0[LM_MAX_ADAPTERS + 2];
   __shared__ PlPair s_scan[PL_W];
-  const int tid = threadIdx.x, blocks = gridDim.x, block = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int blocks = ONE ? 1 : gridDim.x, block = ONE ? 0 : blockIdx.x;
   const bool lists = block == 0;
+  const int per = ((T + PL_W - 1) / PL_W + 63) & ~63;  // ONE: rows of a wavefront
+  const int w0 = min(wave * per, T), w1 = min(w0 + per, T);
+  int rank_of[PL_ONE / PL_T], id_of[PL_ONE / PL_T];
+  if constexpr (ONE)
+    pl_count(ids, w0, w1, L, s_cnt, [&](int row, int id, int rank) {
+#pragma unroll
+      for (int i = 0; i < PL_ONE / PL_T; ++i)
+        if (row == w0 + 64 * i + lane) {
+          rank_of[i] = rank;
+          id_of[i] = id;
+        }
+    });
   // thread l: adapter l
   int rows = 0, mine = 0;
   if (tid < L) {
+    if constexpr (ONE) {
+      rows = s_cnt[tid * PL_S + PL_W];
+    } else {
 #pragma unroll 4
-    for (int c = 0; c < blocks; ++c) {
-      const int v = gld<int>(p.counts + static_cast<int64_t>(c) * (L + 1) + tid);
-      rows += v;
-      mine += c < block ? v : 0;
+      for (int c = 0; c < blocks; ++c) {
+        const int v = gld<int>(p.counts + static_cast<int64_t>(c) * (L + 1) + tid);
+        rows += v;
+        mine += c < block ? v : 0;
+      }
     }
   }
   const int items = (rows + LM_ITEM - 1) / LM_ITEM;
@@ -214,18 +246,28 @@ __global__ __launch_bounds__(PL_T) void lm_place_kernel(const int32_t* __restric
     }
   }
   __syncthreads();
-  const int r1 = min((block + 1) * chunk, T);
-#pragma unroll 4
-  for (int row = block * chunk + tid; row < r1; row += PL_T) {
-    int id = gld<int32_t>(ids + row);
-    id = id < 0 || id > L ? L : id;
-    const int pos = s_base[id] + gld<int>(p.rank + row), rank = pos - s_seg[id];
+  auto put = [&](int row, int id, int rank_in) {
+    const int pos = s_base[id] + rank_in, rank = pos - s_seg[id];
     const int item = s_item0[id] + rank / LM_ITEM;
     // all so where the ids did not change between the passes
-    if (rank < 0 || pos >= T || item >= s_item0[id + 1]) continue;
+    if (rank < 0 || pos >= T || item >= s_item0[id + 1]) return;
     gst<i32x2>(p.order + pos, i32x2{row, id});
     gst<int>(p.slot_row + item * LM_ITEM + rank % LM_ITEM, row);
     if (rank % LM_ITEM == 0) gst<int>(p.item_id + item, id);
+  };
+  if constexpr (ONE) {
+#pragma unroll
+    for (int i = 0; i < PL_ONE / PL_T; ++i) {
+      const int row = w0 + 64 * i + lane;
+      if (row < w1) put(row, id_of[i], rank_of[i] + s_cnt[id_of[i] * PL_S + wave]);
+    }
+  } else {
+    const int r1 = min((block + 1) * chunk, T);
+#pragma unroll 4
+    for (int row = block * chunk + tid; row < r1; row += PL_T) {
+      const int id = gld<int32_t>(ids + row);
+      put(row, id < 0 || id > L ? L : id, gld<int>(p.rank + row));
+    }
   }
 }
 
@@ -1092,26 +1134,39 @@ __device__ __forceinline__ void lm_small_grad(const LmSmall& p, int l, int r0, i
   f32x4 acc[8][2];  // [rank][columns], OTHER: [column][ranks]
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-  // the adapter's rows among 64 at a time
-  uint64_t own = 0;
-  for (int t = 0, t0 = -64;;) {
-    while (own == 0 && (t0 += 64) < p.T) {
-      const int at = t0 + (threadIdx.x & 63);
-      own = __ballot(at < p.T && gld<int32_t>(p.ids + min(at, p.T - 1)) == l);
-    }
-    if (own == 0) break;
-    t = t0 + __builtin_ctzll(own);
-    own &= own - 1;
-    float xs[8];
-    lm_unpack<F16>(gld<u32x4>(x + static_cast<int64_t>(t) * C), xs);
-    const f32x4 f0 = gld<f32x4>(f + static_cast<int64_t>(t) * p.R), f1 = gld<f32x4>(f + static_cast<int64_t>(t) * p.R + 4);
+  // the adapter's rows among 64 at a time, four rows' loads in flight
+  for (int t0 = 0; t0 < p.T; t0 += 64) {
+    const int at = t0 + (threadIdx.x & 63);
+    uint64_t own = __ballot(at < p.T && gld<int32_t>(p.ids + min(at, p.T - 1)) == l);
+    while (own != 0) {
+      u32x4 qx[4];
+      f32x4 f0[4], f1[4];
+      int n = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float rank = (OTHER ? e : i) < 4 ? f0[(OTHER ? e : i) & 3] : f1[(OTHER ? e : i) & 3];
-        acc[i][e >> 2][e & 3] = __builtin_fmaf(rank, xs[OTHER ? i : e], acc[i][e >> 2][e & 3]);
+      for (int q = 0; q < 4; ++q) {
+        if (own == 0) break;
+        const int64_t t = t0 + __builtin_ctzll(own);
+        own &= own - 1;
+        qx[q] = gld<u32x4>(x + t * C);
+        f0[q] = gld<f32x4>(f + t * p.R);
+        f1[q] = gld<f32x4>(f + t * p.R + 4);
+        ++n;
       }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (q >= n) break;
+        float xs[8];
+        lm_unpack<F16>(qx[q], xs);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int r = OTHER ? e : i;
+            const float rank = r < 4 ? f0[q][r & 3] : f1[q][r & 3];
+            acc[i][e >> 2][e & 3] = __builtin_fmaf(rank, xs[OTHER ? i : e], acc[i][e >> 2][e & 3]);
+          }
+      }
+    }
   }
   if (at_c >= C) return;
   const float s = p.scale != nullptr ? gld<float>(p.scale + l) : 1.f;
@@ -1493,11 +1548,15 @@ mi_status lm_plan(const LmSizes& s, int64_t rows, const int32_t* ids, const LmPl
   const int64_t blocks = rows > 0 ? (rows + chunk - 1) / chunk : 1;
   const dim3 grid(static_cast<unsigned>(blocks));
   const int T = static_cast<int>(rows), L = static_cast<int>(s.L), c = static_cast<int>(chunk);
+  const int ci = static_cast<int>(s.chunk_items());
+  if (rows <= PL_ONE) {
+    hipLaunchKernelGGL(lm_place_kernel<true>, dim3(1), dim3(PL_T), 0, st, ids, T, L, c, ci, p);
+    return launch_status("mm_lora (plan)");
+  }
   hipLaunchKernelGGL(lm_count_kernel, grid, dim3(PL_T), 0, st, ids, T, L, c, p);
   const mi_status one = launch_status("mm_lora (plan)");
   if (one != MI_OK) return one;
-  hipLaunchKernelGGL(lm_place_kernel, grid, dim3(PL_T), 0, st, ids, T, L, c,
-                     static_cast<int>(s.chunk_items()), p);
+  hipLaunchKernelGGL(lm_place_kernel<false>, grid, dim3(PL_T), 0, st, ids, T, L, c, ci, p);
   return launch_status("mm_lora (plan)");
 }
 

@@ -137,3 +137,25 @@ def test_against_oracle(gpu, T, N, K, L, R, kind, dtype):
         _near(got[0], gx, ((N + R + 8) * U + 2.0 ** -16) * mx, dtype, "grad_x")
         _near(got[1], rga, ((N + T + 8) * U + U) * ma, gd, "grad_a")
         _near(got[2], rgb, ((K + T + 8) * U + U) * mb, gd, "grad_b")
+
+
+@pytest.mark.parametrize("T,N,K,L,R,kind", [(4096, 64, 64, 5, 16, "runs"), (4097, 72, 72, 1024, 8, "mixed"),
+                                            (9000, 64, 136, 7, 8, "mixed"), (70001, 64, 64, 3, 16, "runs"),
+                                            (5000, 1024, 64, 1, 24, "few")])
+def test_exact_many_rows(gpu, T, N, K, L, R, kind):
+    """Rows past what one workgroup sorts, and past the rows of a chunk."""
+    print(f"mm_lora many rows T={T} N={N} K={K} L={L} R={R} {kind}", flush=True)
+    dtype = torch.bfloat16
+    x, w, a, b, ids, scale, bias, go = _case(T, N, K, L, R, dtype, kind, True, T)
+    x, b = x.clamp(-1, 1), torch.where(torch.rand(b.shape, generator=synth.gen(T)) < 8.0 / N, b.float(), 0.0).to(dtype)
+    go = torch.where(torch.rand(go.shape, generator=synth.gen(T + 1)) < 0.1, go.float(), 0.0).to(dtype)
+    ref, mag, act, _ = O.mm_lora(x.double(), w.double(), a.double(), b.double(), ids, scale, bias.double())
+    refs = O.mm_lora_backward(go.double(), x.double(), w.double(), a.double(), b.double(), ids, scale)
+    assert mag.max() < 2 ** 24 and all(m.max() < 2 ** 24 for _, m in refs)
+    dev = [t.to(gpu) for t in (x, w, a, b, ids, scale)]
+    out, ga = mi.mm_lora(*dev, bias=bias.to(gpu), out_dtype=torch.float32, with_act=True)
+    torch.cuda.synchronize()
+    assert np.array_equal(_np(out), ref) and np.array_equal(_np(ga), act)
+    got = mi.mm_lora_backward(go.to(gpu), *dev, act=ga, grad_dtype=torch.float32)
+    for what, t, (want, _) in zip(("grad_x", "grad_a", "grad_b"), got, refs):
+        assert torch.equal(t.cpu(), torch.from_numpy(want).to(t.dtype)), what
