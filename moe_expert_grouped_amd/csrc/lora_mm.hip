@@ -35,7 +35,6 @@ constexpr int LM_MAX_ADAPTERS = 1024;
 constexpr int LM_MAX_RANK = 256;
 constexpr int LM_ITEM = 32;            // rows of an item
 constexpr int LM_BK = 64;              // 128 bytes of a row of x: one step
-constexpr int LM_FEW_ROWS = 64;         // up to here the few-row kernels
 constexpr uint32_t LM_OUT = 0x80000000u;  // past every descriptor's range
 
 __device__ __forceinline__ lds_void_ptr lm_lds(void* p) { return (lds_void_ptr)(p); }
@@ -1125,10 +1124,13 @@ __global__ __launch_bounds__(256) void lm_parts_kernel(LmSmall p) {
   }
 }
 
-// gA: 8 ranks and 2048 columns of x of an adapter, a thread 8 x 8 of them (OTHER: gB)
+// gA: 8 ranks and 512 columns of x of an adapter, a lane 8 x 8 of them (OTHER: gB).  The
+// wavefronts take every fourth row each and add their sums in order.
+constexpr int SG_COLS = 512;
 template <bool F16, bool OTHER, typename OutT>
-__device__ __forceinline__ void lm_small_grad(const LmSmall& p, int l, int r0, int c0) {
-  const int C = OTHER ? p.cb : p.ca, at_c = c0 + threadIdx.x * 8, c = min(at_c, C - 8);
+__device__ __forceinline__ void lm_small_grad(const LmSmall& p, int l, int r0, int c0, f32x4* red) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int C = OTHER ? p.cb : p.ca, at_c = c0 + lane * 8, c = min(at_c, C - 8);
   const uint16_t* const x = static_cast<const uint16_t*>(OTHER ? p.go : p.x) + c;
   const float* const f = (OTHER ? (p.act_in != nullptr ? p.act_in : p.v) : p.u) + r0;
   f32x4 acc[8][2];  // [rank][columns], OTHER: [column][ranks]
@@ -1136,8 +1138,8 @@ __device__ __forceinline__ void lm_small_grad(const LmSmall& p, int l, int r0, i
   for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = f32x4{0.f, 0.f, 0.f, 0.f};
   // the adapter's rows among 64 at a time, four rows' loads in flight
   for (int t0 = 0; t0 < p.T; t0 += 64) {
-    const int at = t0 + (threadIdx.x & 63);
-    uint64_t own = __ballot(at < p.T && gld<int32_t>(p.ids + min(at, p.T - 1)) == l);
+    const int at = t0 + lane;
+    uint64_t own = __ballot(at < p.T && gld<int32_t>(p.ids + min(at, p.T - 1)) == l) & (0x1111111111111111ull << wave);
     while (own != 0) {
       u32x4 qx[4];
       f32x4 f0[4], f1[4];
@@ -1168,20 +1170,36 @@ __device__ __forceinline__ void lm_small_grad(const LmSmall& p, int l, int r0, i
       }
     }
   }
-  if (at_c >= C) return;
   const float s = p.scale != nullptr ? gld<float>(p.scale + l) : 1.f;
   OutT* const out = static_cast<OutT*>(OTHER ? p.gb : p.ga) + static_cast<int64_t>(l) * p.R * C;
+  // half of the sums at a time; wavefront w then has those of index 4 half + w
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int half = 0; half < 2; ++half) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) red[((wave * 4 + i) * 2 + e) * 64 + lane] = acc[4 * half + i][e];
+    __syncthreads();
+    f32x4 v[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      v[e] = red[(wave * 2 + e) * 64 + lane];
+#pragma unroll
+      for (int w = 1; w < 4; ++w) v[e] += red[((w * 4 + wave) * 2 + e) * 64 + lane];
+      v[e] *= s;
+    }
+    if (at_c >= C) continue;
+    const int i = 4 * half + wave;
     OutT* const at = OTHER ? out + static_cast<int64_t>(c + i) * p.R + r0 : out + static_cast<int64_t>(r0 + i) * C + c;
     if constexpr (sizeof(OutT) == 4) {
-      gst<f32x4>(at, acc[i][0] * s);
-      gst<f32x4>(at + 4, acc[i][1] * s);
+      gst<f32x4>(at, v[0]);
+      gst<f32x4>(at + 4, v[1]);
     } else {
       typedef OutT t8 __attribute__((ext_vector_type(8)));
       t8 o;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = static_cast<OutT>(acc[i][e >> 2][e & 3] * s);
+      for (int e = 0; e < 8; ++e) o[e] = static_cast<OutT>(v[e >> 2][e & 3]);
       gst<u32x4>(at, __builtin_bit_cast(u32x4, o));
     }
   }
@@ -1193,12 +1211,13 @@ __global__ __launch_bounds__(256) void lm_finish_kernel(LmSmall p) {
   const int n = p.mm.n, R = p.R;
   if constexpr (BT) {
     if (static_cast<int>(blockIdx.x) >= p.fin) {
-      const int pa = (p.ca + 2047) / 2048, pb = (p.cb + 2047) / 2048, r8 = R / 8;
+      __shared__ __attribute__((aligned(16))) f32x4 red[4 * 4 * 2 * 64];
+      const int pa = (p.ca + SG_COLS - 1) / SG_COLS, pb = (p.cb + SG_COLS - 1) / SG_COLS, r8 = R / 8;
       int i = blockIdx.x - p.fin;
       const int panel = i % (pa + pb);
       i /= pa + pb;
-      if (panel < pa) lm_small_grad<F16, false, GradT>(p, i / r8, i % r8 * 8, panel * 2048);
-      else lm_small_grad<F16, true, GradT>(p, i / r8, i % r8 * 8, (panel - pa) * 2048);
+      if (panel < pa) lm_small_grad<F16, false, GradT>(p, i / r8, i % r8 * 8, panel * SG_COLS, red);
+      else lm_small_grad<F16, true, GradT>(p, i / r8, i % r8 * 8, (panel - pa) * SG_COLS, red);
       return;
     }
   }
@@ -1471,8 +1490,18 @@ int lm_splits(int64_t T, int64_t n, int64_t k) {
   return static_cast<int>(s < 1 ? 1 : s);
 }
 
-// Few rows: where the dots' reads of the banks, from the L2s, stay small beside the rest
-bool lm_small(const LmSizes& s) { return s.T <= LM_FEW_ROWS; }
+// Few rows: as long as the fmas of the finish, and in the backward pass of the adapters'
+// gradients, cost less than the plan and the launches that the MFMAs need.  us, few rows and
+// many, forward: n = k = 4096, rank 16, 256 rows 32 and 34, 384 rows 55 and 39; rank 64, 128
+// rows 32 and 40, 192 rows 45 and 39; n 1024, k 2048, rank 16, 1024 rows 23 and 25; n 2048,
+// k 1024, rank 128, 128 rows 25 and 24.  With the backward pass: n = k = 4096, rank 16, 256
+// rows 74 and 82; rank 64, 128 rows 74 and 97, 192 rows 106 and 95; n 1024, k 2048, 256 rows
+// 45 and 51, 384 rows 58 and 52.
+bool lm_small(const LmSizes& s, bool backward) {
+  if (s.T <= 32) return true;
+  if (backward) return s.T <= 256 && s.T * (s.N + s.K) * (s.R + 16) <= 64000000;
+  return s.T <= 1024 && s.T * s.N * (s.R + 16) <= 36000000 && s.T * s.K * s.R <= 128000000;
+}
 
 struct LmCarve {
   uint8_t* at;
@@ -1496,7 +1525,7 @@ struct LmSpace {
 LmSpace lm_space(const LmSizes& s, bool backward, void* base) {
   LmCarve c{static_cast<uint8_t*>(base)};
   LmSpace o{};
-  if (s.T > 0 && lm_small(s)) {
+  if (s.T > 0 && lm_small(s, backward)) {
     o.v = c.take<float>(s.T * s.R);
     o.u = c.take<float>(backward ? s.T * s.R : 0);
     o.parts = c.take<float>(s.T * (backward ? lm_splits(s.T, s.K, s.N) * s.K : lm_splits(s.T, s.N, s.K) * s.N));
@@ -1604,7 +1633,7 @@ mi_status lm_small_run(LmSmall p, hipStream_t st) {
   hipLaunchKernelGGL((lm_parts_kernel<F16, BT>), dim3(p.gemm + p.dots), dim3(256), 0, st, p);
   const mi_status one = launch_status(what);
   if (one != MI_OK) return one;
-  const int grads = p.ga == nullptr ? 0 : p.L * (p.R / 8) * ((p.ca + 2047) / 2048 + (p.cb + 2047) / 2048);
+  const int grads = p.ga == nullptr ? 0 : p.L * (p.R / 8) * ((p.ca + SG_COLS - 1) / SG_COLS + (p.cb + SG_COLS - 1) / SG_COLS);
   hipLaunchKernelGGL((lm_finish_kernel<F16, BT, OutT, GradT>), dim3(p.fin + grads), dim3(256), 0, st, p);
   return launch_status(what);
 }
@@ -1658,7 +1687,7 @@ extern "C" mi_status mi_mm_lora(const void* x, int64_t m, int64_t k, mi_dtype dt
              "%s: the workspace needs %zu bytes, aligned to 256 (got %zu)", what, sp.bytes, workspace_bytes);
   hipStream_t hs = static_cast<hipStream_t>(stream);
   const int64_t es = out_dtype == MI_F32 ? 4 : 2;
-  if (lm_small(s)) {
+  if (lm_small(s, false)) {
     LmSmall p{};
     p.mm.x = p.x = x;
     p.mm.w = w;
@@ -1770,7 +1799,7 @@ extern "C" mi_status mi_mm_lora_backward(const void* grad_out, const void* x, in
              "%s: the workspace needs %zu bytes, aligned to 256 (got %zu)", what, sp.bytes, workspace_bytes);
   hipStream_t hs = static_cast<hipStream_t>(stream);
   const bool f16 = dtype == MI_F16, several = s.pass() < m;
-  if (m > 0 && lm_small(s)) {
+  if (m > 0 && lm_small(s, true)) {
     LmSmall p{};
     p.mm.x = p.go = grad_out;
     p.x = x;
