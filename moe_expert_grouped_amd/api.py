@@ -12,6 +12,8 @@ memory and the current stream.  Inputs must already live on the GPU.
 """
 from __future__ import annotations
 
+import functools
+
 import numpy as np
 import torch
 
@@ -940,9 +942,25 @@ def moe_combine_rows_backward(grad_out: torch.Tensor, rows: torch.Tensor,
 _HALF = (torch.bfloat16, torch.float16)
 
 
+class _Devices(dict):
+    """Device objects by index (making one costs as much as a check)."""
+
+    def __missing__(self, i):
+        self[i] = d = torch.device("cuda", i)
+        return d
+
+
+_CUDA = _Devices()
+
+
+@functools.lru_cache(maxsize=1024)
+def _lora_mm_bytes(m, n, k, num_adapters, rank, backward):
+    return int(_lib.lib().mi_mm_lora_workspace_size(m, n, k, num_adapters, rank, backward))
+
+
 def lora_mm_workspace_bytes(m, n, k, num_adapters, rank, *, backward: bool = False) -> int:
-    """Workspace of :func:`mm_lora` (or of :func:`mm_lora_backward`)."""
-    return int(_lib.lib().mi_mm_lora_workspace_size(m, n, k, num_adapters, rank, int(backward)))
+    """Workspace of :func:`mm_lora` (or of :func:`mm_lora_backward`); 0 for sizes they refuse."""
+    return _lora_mm_bytes(m, n, k, num_adapters, rank, int(backward))
 
 
 def _lora_operands(name, rows, cols, w, lora_a, lora_b, lora_ids, lora_scale):
@@ -965,9 +983,18 @@ def _lora_operands(name, rows, cols, w, lora_a, lora_b, lora_ids, lora_scale):
     return M, K, N, L, R
 
 
-def _workspace(name, workspace, need, device):
+def _given(name, what, t, shape, dtype, gpu):
+    """A caller's output tensor, or a new one on GPU `gpu`."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=_CUDA[gpu])
+    if not (t.shape == shape and t.dtype == dtype and t.is_contiguous()):
+        raise ValueError(f"{name}: {what} must be contiguous {dtype} of shape {tuple(shape)}")
+    return t
+
+
+def _workspace(name, workspace, need, gpu):
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
+        return torch.empty(need, dtype=torch.uint8, device=_CUDA[gpu])
     if not (workspace.dtype == torch.uint8 and workspace.is_contiguous()):
         raise ValueError(f"{name}: workspace must be a contiguous uint8 tensor")
     return workspace
@@ -1002,18 +1029,11 @@ def mm_lora(x: torch.Tensor, w: torch.Tensor, lora_a: torch.Tensor, lora_b: torc
                                       lora_b.contiguous(), lora_ids.contiguous())
     lora_scale = None if lora_scale is None else lora_scale.contiguous()
     bias = None if bias is None else bias.contiguous()
-    if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=x.device)
-    else:
-        _own_out(name, "[M, N]", out, (M, N), out_dtype)
-    if act is None and with_act:
-        act = torch.empty((M, R), dtype=torch.float32, device=x.device)
-    _need(act is None or (act.shape == (M, R) and act.dtype == torch.float32 and
-                          act.is_contiguous()), "mm_lora: act must be contiguous float32 [M, R]")
-    L_ = _lib.lib()
-    workspace = _workspace(name, workspace, L_.mi_mm_lora_workspace_size(M, N, K, L, R, 0),
-                           x.device)
-    _launch(gpu, L_.mi_mm_lora, x.data_ptr(), M, K, _DT[x.dtype], w.data_ptr(), N,
+    out = _given(name, "out", out, (M, N), out_dtype, gpu)
+    if with_act or act is not None:
+        act = _given(name, "act", act, (M, R), torch.float32, gpu)
+    workspace = _workspace(name, workspace, _lora_mm_bytes(M, N, K, L, R, 0), gpu)
+    _launch(gpu, _lib.lib().mi_mm_lora, x.data_ptr(), M, K, _DT[x.dtype], w.data_ptr(), N,
             lora_a.data_ptr(), lora_b.data_ptr(), L, R, lora_ids.data_ptr(), _ptr(lora_scale),
             _ptr(bias), out.data_ptr(), _DT[out_dtype], _ptr(act), workspace.data_ptr(),
             workspace.numel())
@@ -1060,22 +1080,13 @@ def mm_lora_backward(grad_out: torch.Tensor, x: torch.Tensor, w: torch.Tensor,
     lora_scale = None if lora_scale is None else lora_scale.contiguous()
     act = None if act is None else act.contiguous()
 
-    def own(t, what, shape, dtype):
-        if t is None:
-            return torch.empty(shape, dtype=dtype, device=x.device)
-        _need(t.shape == shape and t.dtype == dtype and t.is_contiguous(),
-              f"mm_lora_backward: {what} must be contiguous {tuple(shape)} of its type")
-        return t
-
     if with_x:
-        grad_x = own(grad_x, "grad_x", (M, K), x.dtype)
+        grad_x = _given(name, "grad_x", grad_x, (M, K), x.dtype, gpu)
     if with_adapters:
-        grad_a = own(grad_a, "grad_a", (L, R, K), grad_dtype)
-        grad_b = own(grad_b, "grad_b", (L, N, R), grad_dtype)
-    L_ = _lib.lib()
-    workspace = _workspace(name, workspace, L_.mi_mm_lora_workspace_size(M, N, K, L, R, 1),
-                           x.device)
-    _launch(gpu, L_.mi_mm_lora_backward, grad_out.data_ptr(), x.data_ptr(), M, K, _DT[x.dtype],
+        grad_a = _given(name, "grad_a", grad_a, (L, R, K), grad_dtype, gpu)
+        grad_b = _given(name, "grad_b", grad_b, (L, N, R), grad_dtype, gpu)
+    workspace = _workspace(name, workspace, _lora_mm_bytes(M, N, K, L, R, 1), gpu)
+    _launch(gpu, _lib.lib().mi_mm_lora_backward, grad_out.data_ptr(), x.data_ptr(), M, K, _DT[x.dtype],
             w.data_ptr(), N, lora_a.data_ptr(), lora_b.data_ptr(), L, R, lora_ids.data_ptr(),
             _ptr(lora_scale), _ptr(act), _ptr(grad_x), _ptr(grad_a), _ptr(grad_b),
             _DT[grad_dtype], workspace.data_ptr(), workspace.numel())
@@ -1116,22 +1127,21 @@ def moe_route_topk(logits: torch.Tensor, top_k: int, *, renormalize: bool = True
     logits = logits.contiguous()
     token_mask = None if token_mask is None else token_mask.contiguous()
     _need(1 <= top_k <= min(E, 64), "moe_route_topk: top_k must be in [1, min(E, 64)]")
-    if topk_weights is None:
-        topk_weights = torch.empty((T, top_k), dtype=torch.float32, device=logits.device)
-    if topk_ids is None:
-        topk_ids = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
-    for t, dt in ((topk_weights, torch.float32), (topk_ids, torch.int32)):
-        _need(t.shape == (T, top_k) and t.dtype == dt and t.is_contiguous(),
-              "moe_route_topk: topk_weights and topk_ids must be contiguous float32 and int32 "
-              "[T, top_k]")
+    topk_weights = _given(name, "topk_weights", topk_weights, (T, top_k), torch.float32, gpu)
+    topk_ids = _given(name, "topk_ids", topk_ids, (T, top_k), torch.int32, gpu)
     _launch(gpu, _lib.lib().mi_moe_route_topk, logits.data_ptr(), _DT[logits.dtype], T, E, top_k,
             int(renormalize), _ptr(token_mask), topk_weights.data_ptr(), topk_ids.data_ptr())
     return topk_weights, topk_ids
 
 
+@functools.lru_cache(maxsize=1024)
+def _balance_bytes(num_tokens, num_experts):
+    return int(_lib.lib().mi_moe_balance_loss_workspace_size(num_tokens, num_experts))
+
+
 def balance_workspace_bytes(num_tokens, num_experts) -> int:
     """Workspace of :func:`moe_balance_loss`."""
-    return int(_lib.lib().mi_moe_balance_loss_workspace_size(num_tokens, num_experts))
+    return _balance_bytes(num_tokens, num_experts)
 
 
 def moe_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, *, coef: float = 1.0,
@@ -1161,20 +1171,11 @@ def moe_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, *, coef: floa
     logits, topk_ids = logits.contiguous(), topk_ids.contiguous()
     token_mask = None if token_mask is None else token_mask.contiguous()
     given_counts = None if given_counts is None else given_counts.contiguous()
-    if loss is None:
-        loss = torch.empty((), dtype=torch.float32, device=logits.device)
-    if counts is None:
-        counts = torch.empty(E, dtype=torch.int32, device=logits.device)
-    if slopes is None:
-        slopes = torch.empty(E, dtype=torch.float32, device=logits.device)
-    _need(loss.numel() == 1 and loss.dtype == torch.float32 and
-          counts.shape == (E,) and counts.dtype == torch.int32 and counts.is_contiguous() and
-          slopes.shape == (E,) and slopes.dtype == torch.float32 and slopes.is_contiguous(),
-          "moe_balance_loss: loss must be one float32, counts int32 [E], slopes float32 [E]")
-    L_ = _lib.lib()
-    workspace = _workspace(name, workspace, L_.mi_moe_balance_loss_workspace_size(T, E),
-                           logits.device)
-    _launch(gpu, L_.mi_moe_balance_loss, logits.data_ptr(), _DT[logits.dtype], T, E,
+    loss = _given(name, "loss", loss, (), torch.float32, gpu)
+    counts = _given(name, "counts", counts, (E,), torch.int32, gpu)
+    slopes = _given(name, "slopes", slopes, (E,), torch.float32, gpu)
+    workspace = _workspace(name, workspace, _balance_bytes(T, E), gpu)
+    _launch(gpu, _lib.lib().mi_moe_balance_loss, logits.data_ptr(), _DT[logits.dtype], T, E,
             topk_ids.data_ptr(), topk_ids.shape[1], _ptr(token_mask), _ptr(given_counts),
             float(coef), loss.data_ptr(), counts.data_ptr(), slopes.data_ptr(),
             workspace.data_ptr(), workspace.numel())
@@ -1227,14 +1228,12 @@ def moe_route_backward(logits: torch.Tensor, *, topk_ids: torch.Tensor | None = 
     topk_ids, topk_weights, grad_weights, slopes, token_mask = (
         None if t is None else t.contiguous()
         for t in (topk_ids, topk_weights, grad_weights, slopes, token_mask))
-    if grad_logits is None:
-        grad_logits = torch.empty((T, E), dtype=grad_dtype or logits.dtype, device=logits.device)
-    _need(grad_logits.shape == (T, E) and grad_logits.dtype in _DT and
-          grad_dtype in (None, grad_logits.dtype) and grad_logits.is_contiguous(),
-          "moe_route_backward: grad_logits must be contiguous [T, E] of grad_dtype (bf16, fp16 or "
-          "fp32)")
+    if grad_dtype is None:
+        grad_dtype = logits.dtype if grad_logits is None else grad_logits.dtype
+    _need(grad_dtype in _DT, "moe_route_backward: grad_dtype must be bfloat16, float16 or float32")
+    grad_logits = _given(name, "grad_logits", grad_logits, (T, E), grad_dtype, gpu)
     _launch(gpu, _lib.lib().mi_moe_route_backward, logits.data_ptr(), _DT[logits.dtype], T, E,
             _ptr(topk_ids), _ptr(topk_weights), _ptr(grad_weights), top_k, int(renormalize),
             _ptr(slopes), _ptr(grad_loss), _ptr(token_mask), grad_logits.data_ptr(),
-            _DT[grad_logits.dtype])
+            _DT[grad_dtype])
     return grad_logits
