@@ -553,8 +553,9 @@ struct LmMm {
   const void* bias;       // [n] or null
   const uint16_t* pieces; // [T, 3 RP]
   LmPlan plan;
-  void* out;              // [T, n]
+  void* out;              // [T, n]; of several splits fp32 [splits, T, n]
   int T, k, n, L, R, RP;
+  int splits, blocks;     // of the k axis, and workgroups of each
 };
 
 // 32-byte pieces of a transposed tile's row (BN / 16 of them): the 16 rows that a
@@ -579,10 +580,10 @@ __device__ __forceinline__ void lm_wait_barrier() {
 // and each XCD has a contiguous run of that order (workgroup ids go to the 8 in turn).
 struct LmPlace { int m0, n0, rows, cols, k0, steps; };
 template <int BM, int BN>
-__device__ __forceinline__ LmPlace lm_place(const LmMm& p) {
+__device__ __forceinline__ LmPlace lm_place(const LmMm& p, int block) {
   const int nt = (p.n + BN - 1) / BN, mt = (p.T + BM - 1) / BM;
   const int total = nt * mt, per = (total + 7) / 8;
-  const int slot = blockIdx.x >> 3, tile = (blockIdx.x & 7) * per + slot;
+  const int slot = block >> 3, tile = (block & 7) * per + slot;
   if (slot >= per || tile >= total) return {0, 0, 0, 0, 0, 0};
   constexpr int GM = BM >= 256 ? 4 : 8;
   const int grp = tile / (GM * nt), in = tile - grp * GM * nt, gsz = min(mt - grp * GM, GM);
@@ -885,7 +886,8 @@ __device__ __forceinline__ void lm_tile(const LmMm& p, const LmPlace& t, LmStage
       }
     }
   };
-  if constexpr (!PART) {
+  // of a k axis in splits, the last one has the adapters
+  if (!PART && k0 + KT == last + 1) {
     Run u = run_at(0);
     fetch(s0, u);
     while (u.l < p.L) {
@@ -965,8 +967,14 @@ __global__ __launch_bounds__(64 * WM * WN)
     __attribute__((amdgpu_waves_per_eu(2, 2))) void lm_mm_kernel(LmMm p) {
   constexpr int BM = 16 * FM * WM, BN = 16 * FN * WN, X = BM * 128, W = BN * 128;
   __shared__ i32x2 s_order[BM];
-  const LmPlace t = lm_place<BM, BN>(p);
+  LmPlace t = lm_place<BM, BN>(p, p.splits > 1 ? blockIdx.x % p.blocks : blockIdx.x);
   if (t.rows == 0) return;
+  if (p.splits > 1) {
+    const int split = blockIdx.x / p.blocks, all = t.steps;
+    t.k0 = all * split / p.splits;
+    t.steps = all * (split + 1) / p.splits - t.k0;
+    p.out = static_cast<OutT*>(p.out) + static_cast<int64_t>(split) * p.T * p.n;
+  }
   if constexpr (NST == 2) {
     static_assert(BM == BN, "the parts of a stage");
     __shared__ __attribute__((aligned(16))) uint8_t w0[W], w1[W], e0[X / 2], e1[X / 2], o0[X / 2], o1[X / 2];
@@ -1429,26 +1437,28 @@ __global__ __launch_bounds__(256) void lm_grad_kernel(LmGrad ga, LmGrad gb) {
     lm_grad<F16, true, NB, OutT>(gb, st0, st1, st2, s_rows, ch, (blockIdx.x - pa) * GR_BN, rank0);
 }
 
+// four values a thread, gA's and then gB's, of an adapter with partial sums
 template <typename OutT>
 __global__ __launch_bounds__(256) void lm_reduce_kernel(LmGrad ga, LmGrad gb) {
   const i32x4 span = gld<i32x4>(ga.plan.spans + blockIdx.y);
   if (span.z < 0) return;
-#pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    const LmGrad& a = which ? gb : ga;
-    const int64_t size = static_cast<int64_t>(a.R) * a.C;
-    for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4; i < size;
-         i += static_cast<int64_t>(gridDim.x) * 1024) {
-      f32x4 v = gld<f32x4>(a.part + span.z * size + i);
-      for (int c = 1; c < span.y; ++c) v += gld<f32x4>(a.part + (span.z + c) * size + i);
-      if constexpr (sizeof(OutT) == 4) {
-        gst<f32x4>(static_cast<float*>(a.out) + blockIdx.y * size + i, v);
-      } else {
-        typedef OutT t4 __attribute__((ext_vector_type(4)));
-        gst<u32x2>(static_cast<OutT*>(a.out) + blockIdx.y * size + i,
-                   __builtin_bit_cast(u32x2, __builtin_convertvector(v, t4)));
-      }
-    }
+  const int64_t na = static_cast<int64_t>(ga.R) * ga.C, nb = static_cast<int64_t>(gb.R) * gb.C;
+  int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+  if (i >= na + nb) return;
+  const bool second = i >= na;
+  const int64_t size = second ? nb : na;
+  if (second) i -= na;
+  const float* const part = (second ? gb.part : ga.part) + span.z * size + i;
+  f32x4 v = gld<f32x4>(part);
+#pragma unroll 8
+  for (int c = 1; c < span.y; ++c) v += gld<f32x4>(part + c * size);
+  void* const out = second ? gb.out : ga.out;
+  if constexpr (sizeof(OutT) == 4) {
+    gst<f32x4>(static_cast<float*>(out) + blockIdx.y * size + i, v);
+  } else {
+    typedef OutT t4 __attribute__((ext_vector_type(4)));
+    gst<u32x2>(static_cast<OutT*>(out) + blockIdx.y * size + i,
+               __builtin_bit_cast(u32x2, __builtin_convertvector(v, t4)));
   }
 }
 
@@ -1490,6 +1500,16 @@ int lm_splits(int64_t T, int64_t n, int64_t k) {
   return static_cast<int>(s < 1 ? 1 : s);
 }
 
+// The same of many rows and a narrow result, 16 steps at least (3817 rows, n 96, k 4760: the
+// product 25.8 us unsplit)
+int lm_wide_splits(int64_t T, int64_t n, int64_t k) {
+  const int64_t tiles = (T + 63) / 64 * ((n + 63) / 64), steps = (k + LM_BK - 1) / LM_BK;
+  if (tiles > 256) return 1;
+  int64_t s = 512 / tiles;
+  if (s > steps / 16) s = steps / 16;
+  return static_cast<int>(s < 1 ? 1 : s);
+}
+
 // Few rows: as long as the fmas of the finish, and in the backward pass of the adapters'
 // gradients, cost less than the plan and the launches that the MFMAs need.  us, few rows and
 // many, forward: n = k = 4096, rank 16, 256 rows 32 and 34, 384 rows 55 and 39; rank 64, 128
@@ -1500,7 +1520,7 @@ int lm_splits(int64_t T, int64_t n, int64_t k) {
 bool lm_small(const LmSizes& s, bool backward) {
   if (s.T <= 32) return true;
   if (backward) return s.T <= 256 && s.T * (s.N + s.K) * (s.R + 16) <= 64000000;
-  return s.T <= 1024 && s.T * s.N * (s.R + 16) <= 36000000 && s.T * s.K * s.R <= 128000000;
+  return s.T <= 1024 && s.T * s.N * (s.R + 16) <= 36000000 && s.T * s.K * s.R <= 64000000;
 }
 
 struct LmCarve {
@@ -1544,6 +1564,14 @@ LmSpace lm_space(const LmSizes& s, bool backward, void* base) {
   o.plan.totals = c.take<int>(4);
   o.plan.zeros = c.take<uint16_t>(8);
   o.pieces = c.take<uint16_t>(s.T * 3 * s.rp());
+  // the passes over the rows: all of one size but the last, which may have more splits
+  const int64_t pass = s.T > 0 ? s.pass() : 1, rest = s.T % pass, on = backward ? s.K : s.N, in = backward ? s.N : s.K;
+  int64_t parts = 0;
+  for (const int64_t rows : {pass, rest}) {
+    const int64_t sp = rows > 0 ? lm_wide_splits(rows, on, in) : 1;
+    if (sp > 1 && sp * rows * on > parts) parts = sp * rows * on;
+  }
+  o.parts = c.take<float>(parts);
   if (backward) {
     o.ut = c.take<uint16_t>(items * LM_ITEM * 3 * s.rp());
     o.vt = c.take<uint16_t>(items * LM_ITEM * 3 * s.rp());
@@ -1596,28 +1624,58 @@ mi_status lm_shrink_run(const LmShrink& a, int64_t items, hipStream_t st) {
   hipLaunchKernelGGL((lm_shrink_kernel<F16, BT, NB_>),                                              \
                      dim3(static_cast<unsigned>(items), static_cast<unsigned>((nb + NB_ - 1) / NB_)), \
                      dim3(64 * LmShape<NB_>::W), 0, st, a)
-  if (nb == 1) LM_SHRINK(1);
-  else if (nb == 2) LM_SHRINK(2);
+  // All ranks a workgroup, up to 64, where the rows fill the chip; else the ranks go to
+  // several, which read the rows again, from the L2 (493 rows, 7640 columns, rank 48: 37 us
+  // in one workgroup of 4 wavefronts, whose 119 steps are then 30 one after another)
+  const int64_t full = a.T / LM_ITEM;
+  if (nb == 1 || full < 64) LM_SHRINK(1);
+  else if (nb == 2 || full < 128) LM_SHRINK(2);
   else LM_SHRINK(4);
 #undef LM_SHRINK
   return launch_status("mm_lora (shrink)");
 }
 
 template <bool F16, bool BT, int WM, int WN, int FM, int FN, int NST, typename OutT>
-mi_status lm_mm_launch(const LmMm& a, hipStream_t st) {
+mi_status lm_mm_launch(LmMm a, int splits, hipStream_t st) {
   constexpr int BM = 16 * FM * WM, BN = 16 * FN * WN;
   const int64_t tiles = static_cast<int64_t>((a.T + BM - 1) / BM) * ((a.n + BN - 1) / BN);
+  a.splits = splits;
+  a.blocks = static_cast<int>((tiles + 7) / 8 * 8);
   hipLaunchKernelGGL((lm_mm_kernel<F16, BT, WM, WN, FM, FN, NST, OutT>),
-                     dim3(static_cast<unsigned>((tiles + 7) / 8 * 8)), dim3(64 * WM * WN), 0, st, a);
+                     dim3(static_cast<unsigned>(a.blocks) * splits), dim3(64 * WM * WN), 0, st, a);
   return launch_status("mm_lora (product)");
 }
 
+// Which tiles: us a call, plan and first product among them, n = k = 4096: 512 rows 64 x 64
+// 34, 128 x 128 41; 768 rows 48 and 42; 2048 rows 128 x 128 67, 256 x 256 83; 3000 rows 97 and
+// 91; n = k = 8192: 320 rows 64 x 64 78, 128 x 128 66; 1024 rows 128 x 128 121, 256 x 256 149;
+// 1280 rows 168 and 152: each as long as the tiles run in one round of two workgroups per CU.
+// Where the 64 x 64 tiles leave CUs idle, the k axis is split and the parts are added
+// (parts: fp32 [splits, T, n]).
 template <bool F16, bool BT, typename OutT>
-mi_status lm_mm(const LmMm& a, hipStream_t st) {
+mi_status lm_mm(const LmMm& a, float* parts, const int32_t* ids, hipStream_t st) {
   auto tiles = [&](int64_t bm, int64_t bn) { return (a.T + bm - 1) / bm * ((a.n + bn - 1) / bn); };
-  if (tiles(64, 64) <= 512) return lm_mm_launch<F16, BT, 2, 2, 2, 2, 4, OutT>(a, st);
-  if (tiles(128, 128) > 512) return lm_mm_launch<F16, BT, 2, 4, 8, 4, 2, OutT>(a, st);
-  return lm_mm_launch<F16, BT, 2, 2, 4, 4, 2, OutT>(a, st);
+  const int splits = lm_wide_splits(a.T, a.n, a.k);
+  if (splits > 1) {
+    LmMm p = a;
+    p.out = parts;
+    p.bias = nullptr;
+    const mi_status one = lm_mm_launch<F16, BT, 2, 2, 2, 2, 4, float>(p, splits, st);
+    if (one != MI_OK) return one;
+    LmSmall f{};  // no adapter is left to add
+    f.mm = p;
+    f.splits = splits;
+    f.ids = ids;
+    f.bias = a.bias;
+    f.out = a.out;
+    f.T = a.T;
+    f.fin = static_cast<int>((static_cast<int64_t>(a.T) * (a.n / 4) + 255) / 256);
+    hipLaunchKernelGGL((lm_finish_kernel<F16, false, OutT, float>), dim3(f.fin), dim3(256), 0, st, f);
+    return launch_status("mm_lora (sums)");
+  }
+  if (tiles(64, 64) <= 512) return lm_mm_launch<F16, BT, 2, 2, 2, 2, 4, OutT>(a, 1, st);
+  if (tiles(128, 128) > 512) return lm_mm_launch<F16, BT, 2, 4, 8, 4, 2, OutT>(a, 1, st);
+  return lm_mm_launch<F16, BT, 2, 2, 4, 4, 2, OutT>(a, 1, st);
 }
 
 template <bool F16, bool BT, typename OutT, typename GradT>
@@ -1743,9 +1801,10 @@ extern "C" mi_status mi_mm_lora(const void* x, int64_t m, int64_t k, mi_dtype dt
     p.L = a.L;
     p.R = a.R;
     p.RP = a.RP;
+    const int32_t* const at = lora_ids + t0;
     st = dtype == MI_F16
-             ? (es == 4 ? lm_mm<true, false, float>(p, hs) : lm_mm<true, false, _Float16>(p, hs))
-             : (es == 4 ? lm_mm<false, false, float>(p, hs) : lm_mm<false, false, __bf16>(p, hs));
+             ? (es == 4 ? lm_mm<true, false, float>(p, sp.parts, at, hs) : lm_mm<true, false, _Float16>(p, sp.parts, at, hs))
+             : (es == 4 ? lm_mm<false, false, float>(p, sp.parts, at, hs) : lm_mm<false, false, __bf16>(p, sp.parts, at, hs));
     if (st != MI_OK) return st;
   }
   return MI_OK;
@@ -1885,7 +1944,8 @@ extern "C" mi_status mi_mm_lora_backward(const void* grad_out, const void* x, in
       p.L = a.L;
       p.R = a.R;
       p.RP = a.RP;
-      st = f16 ? lm_mm<true, true, _Float16>(p, hs) : lm_mm<false, true, __bf16>(p, hs);
+      const int32_t* const at = lora_ids + t0;
+      st = f16 ? lm_mm<true, true, _Float16>(p, sp.parts, at, hs) : lm_mm<false, true, __bf16>(p, sp.parts, at, hs);
       if (st != MI_OK) return st;
     }
   }
@@ -1917,8 +1977,9 @@ extern "C" mi_status mi_mm_lora_backward(const void* grad_out, const void* x, in
     else hipLaunchKernelGGL((lm_grad_kernel<F16, 4, OutT>), grid, dim3(256), 0, hs, ga, gb);
     const mi_status one = launch_status("mm_lora_backward (adapters)");
     if (one != MI_OK || LmSizes::items(m, num_adapters) <= s.chunk_items()) return one;
-    hipLaunchKernelGGL((lm_reduce_kernel<OutT>), dim3(64, static_cast<unsigned>(num_adapters)), dim3(256), 0,
-                       hs, ga, gb);
+    hipLaunchKernelGGL((lm_reduce_kernel<OutT>),
+                       dim3(static_cast<unsigned>((rank * (n + k) / 4 + 255) / 256), static_cast<unsigned>(num_adapters)),
+                       dim3(256), 0, hs, ga, gb);
     return launch_status("mm_lora_backward (sums)");
   };
   if (f16) return ges == 4 ? launch(std::true_type{}, float{}) : launch(std::true_type{}, _Float16{});

@@ -141,9 +141,11 @@ def test_against_oracle(gpu, T, N, K, L, R, kind, dtype):
 
 @pytest.mark.parametrize("T,N,K,L,R,kind", [(4096, 64, 64, 5, 16, "runs"), (4097, 72, 72, 1024, 8, "mixed"),
                                             (9000, 64, 136, 7, 8, "mixed"), (70001, 64, 64, 3, 16, "runs"),
-                                            (5000, 1024, 64, 1, 24, "few")])
+                                            (5000, 1024, 64, 1, 24, "few"), (2100, 72, 2056, 3, 16, "runs"),
+                                            (1500, 2056, 72, 9, 40, "mixed"), (4500, 128, 4104, 4, 8, "few")])
 def test_exact_many_rows(gpu, T, N, K, L, R, kind):
-    """Rows past what one workgroup sorts, and past the rows of a chunk."""
+    """Rows past what one workgroup sorts, past the rows of a chunk, and narrow results, whose
+    product is split."""
     print(f"mm_lora many rows T={T} N={N} K={K} L={L} R={R} {kind}", flush=True)
     dtype = torch.bfloat16
     x, w, a, b, ids, scale, bias, go = _case(T, N, K, L, R, dtype, kind, True, T)
