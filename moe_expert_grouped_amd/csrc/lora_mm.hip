@@ -774,7 +774,8 @@ __device__ __forceinline__ void lm_tile(const LmMm& p, const LmPlace& t, LmStage
     dma(s1, 1, 0, NI);
     if constexpr (NST == 4) dma(s2, 2, 0, NI);
     lm_wait_barrier<FLY>();
-    dma(*sts[NST - 1], NST - 1, 0, 2 * PPR);  // the rest in step 0
+    if constexpr (NST == 4) dma(s3, 3, 0, 2 * PPR);  // the rest in step 0
+    else dma(s2, 2, 0, 2 * PPR);
   } else {
     dma(s1, 1, 0, NY + (2 * PX < NX ? 2 * PX : NX));  // the rest in step 0
     lm_wait_barrier<NI>();
@@ -783,18 +784,29 @@ __device__ __forceinline__ void lm_tile(const LmMm& p, const LmPlace& t, LmStage
   fa1 = frag_a(s0, 1);
 #pragma unroll
   for (int j = 0; j < FN; ++j) fb[j] = frag_b(s0, j);
-  for (int kt = 0; kt < KT; kt += NST) {
-#define LM_STEP(S_)                                                                      \
-  if constexpr (S_ < NST) {                                                              \
-    step(*sts[(S_ + NST - 1) % NST], *sts[S_], *sts[(S_ + 1) % NST], kt + S_);             \
-    if (kt + S_ + 1 >= KT) break;                                                        \
+  // Whole rounds of the stages, then the rest: a loop that may end inside a round would
+  // make the compiler, which follows the loads into each stage, wait at its head for loads
+  // of later steps.
+  const int rounds = KT / NST * NST;
+#define LM_STEP(S_, KT_) step(*sts[(S_ + NST - 1) % NST], *sts[S_ % NST], *sts[(S_ + 1) % NST], KT_)
+  for (int kt = 0; kt < rounds; kt += NST) {
+    LM_STEP(0, kt);
+    LM_STEP(1, kt + 1);
+    if constexpr (NST >= 3) LM_STEP(2, kt + 2);
+    if constexpr (NST == 4) LM_STEP(3, kt + 3);
   }
-    LM_STEP(0)
-    LM_STEP(1)
-    LM_STEP(2)
-    LM_STEP(3)
+  if (KT - rounds >= 1) {
+    LM_STEP(0, rounds);
+    if constexpr (NST >= 3) {
+      if (KT - rounds >= 2) {
+        LM_STEP(1, rounds + 1);
+        if constexpr (NST == 4) {
+          if (KT - rounds == 3) LM_STEP(2, rounds + 2);
+        }
+      }
+    }
+  }
 #undef LM_STEP
-  }
   // the loads of the steps past the last have written their zeros
   lm_wait_barrier<0>();
 
@@ -1376,23 +1388,29 @@ __device__ __forceinline__ void lm_grad(const LmGrad& a, uint8_t* st0, uint8_t* 
   constexpr int NI = NX + PI;
   load(st0, 0);
   if constexpr (ST == 3) load(st1, 1);
-  for (int kt = 0; kt < KT; kt += ST) {
-#define LM_STEP(S_, ST_, TO_)                        \
-  if constexpr (S_ < ST) {                           \
-    lm_wait_barrier<(ST - 2) * NI>();                \
-    load(TO_, kt + S_ + ST - 1);                     \
-    add(ST_);                                        \
-    if (kt + S_ + 1 >= KT) break;                    \
-  }
-    if constexpr (ST == 3) {
-      LM_STEP(0, st0, st2)
-      LM_STEP(1, st1, st0)
-      LM_STEP(2, st2, st1)
-    } else {
-      LM_STEP(0, st0, st1)
-      LM_STEP(1, st1, st0)
+  auto step = [&](const uint8_t* st, uint8_t* to, int kt) {
+    lm_wait_barrier<(ST - 2) * NI>();
+    load(to, kt + ST - 1);
+    add(st);
+  };
+  // whole rounds of the stages, then the rest
+  const int rounds = KT / ST * ST;
+  if constexpr (ST == 3) {
+    for (int kt = 0; kt < rounds; kt += ST) {
+      step(st0, st2, kt);
+      step(st1, st0, kt + 1);
+      step(st2, st1, kt + 2);
     }
-#undef LM_STEP
+    if (KT - rounds >= 1) {
+      step(st0, st2, rounds);
+      if (KT - rounds == 2) step(st1, st0, rounds + 1);
+    }
+  } else {
+    for (int kt = 0; kt < rounds; kt += ST) {
+      step(st0, st1, kt);
+      step(st1, st0, kt + 1);
+    }
+    if (KT - rounds == 1) step(st0, st1, rounds);
   }
   __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): no load writes to LDS after the end
   // four ranks of column r (ROWS), or four columns of rank r
@@ -1520,7 +1538,7 @@ int lm_wide_splits(int64_t T, int64_t n, int64_t k) {
 bool lm_small(const LmSizes& s, bool backward) {
   if (s.T <= 32) return true;
   if (backward) return s.T <= 256 && s.T * (s.N + s.K) * (s.R + 16) <= 64000000;
-  return s.T <= 1024 && s.T * s.N * (s.R + 16) <= 36000000 && s.T * s.K * s.R <= 64000000;
+  return s.T <= 1024 && s.T * s.N * (s.R + 16) <= 36000000 && s.T * s.K * s.R <= 110000000;
 }
 
 struct LmCarve {
