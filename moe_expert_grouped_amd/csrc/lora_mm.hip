@@ -1538,7 +1538,7 @@ int lm_wide_splits(int64_t T, int64_t n, int64_t k) {
 bool lm_small(const LmSizes& s, bool backward) {
   if (s.T <= 32) return true;
   if (backward) return s.T <= 256 && s.T * (s.N + s.K) * (s.R + 16) <= 64000000;
-  return s.T <= 1024 && s.T * s.N * (s.R + 16) <= 36000000 && s.T * s.K * s.R <= 110000000;
+  return s.T <= 1024 && s.T * s.N * (s.R + 16) <= 36000000 && s.T * s.K * s.R <= 64000000;
 }
 
 struct LmCarve {
