@@ -1296,6 +1296,79 @@ __global__ __launch_bounds__(256) void lm_finish_kernel(LmSmall p) {
 }
 
 // ---------------------------------------------------------------------------
+// One row, rank 32 at most: one launch, bound by the reads of w.  A wavefront has ONE_C rows
+// of w and streams them whole lines at a time (four rows instead of two: n = k = 4096, rank
+// 16: 14.1 us for 11.3); every workgroup computes v again beside them, its wavefronts RW ranks
+// each (their loads hit in the L2: 128 KB a workgroup at rank 16, k 4096).  Taken where that
+// costs less than a second launch; us in one launch and two: n = k = 4096, rank 16, 11.3 and
+// 14.1; n 1024, rank 32, k 4096 11.6 and 13.1, k 8192 17.8 and 16.6; n 64, rank 32, k 16384 28
+// and 18; n 4096, rank 32, k 6144 16.8 and 20.9, k 28672 61 and 62.
+// ---------------------------------------------------------------------------
+constexpr int ONE_W = 8, ONE_C = 2;  // wavefronts, rows of w for each
+template <bool F16, int RW, typename OutT>
+__global__ __launch_bounds__(64 * ONE_W) void lm_one_kernel(LmSmall p) {
+  __shared__ float s_v[ONE_W * RW];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int k = p.ca, n = p.cb, R = p.R;
+  const int n0 = (blockIdx.x * ONE_W + wave) * ONE_C, r0 = wave * RW;
+  const int l = __builtin_amdgcn_readfirstlane(gld<int32_t>(p.ids));
+  const bool has = l >= 0 && l < p.L;
+  const uint16_t* const x = static_cast<const uint16_t*>(p.x);
+  const uint16_t* const w = static_cast<const uint16_t*>(p.mm.w);
+  const uint16_t* const a = static_cast<const uint16_t*>(p.a) + static_cast<int64_t>(has ? l : 0) * R * k;
+  float sum[ONE_C] = {}, v[RW] = {};
+#pragma unroll 4
+  for (int c = lane * 8; c < k; c += 512) {
+    u32x4 qw[ONE_C], qa[RW];
+    const u32x4 qx = gld<u32x4>(x + c);
+#pragma unroll
+    for (int i = 0; i < ONE_C; ++i) qw[i] = gld_nt<u32x4>(w + static_cast<int64_t>(min(n0 + i, n - 1)) * k + c);
+    // rows past the ranks are read again, and not used
+    if (has)
+#pragma unroll
+      for (int i = 0; i < RW; ++i) qa[i] = gld<u32x4>(a + static_cast<int64_t>(min(r0 + i, R - 1)) * k + c);
+    float fx[8], f[8];
+    lm_unpack<F16>(qx, fx);
+#pragma unroll
+    for (int i = 0; i < ONE_C; ++i) {
+      lm_unpack<F16>(qw[i], f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[i] = __builtin_fmaf(fx[e], f[e], sum[i]);
+    }
+    if (has)
+#pragma unroll
+      for (int i = 0; i < RW; ++i) {
+        lm_unpack<F16>(qa[i], f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[i] = __builtin_fmaf(fx[e], f[e], v[i]);
+      }
+  }
+  // lane r has rank r of the wavefront's rows of b
+  float b[ONE_C];
+  const uint16_t* const bank = static_cast<const uint16_t*>(p.b) + static_cast<int64_t>(has ? l : 0) * n * R;
+#pragma unroll
+  for (int i = 0; i < ONE_C; ++i)
+    b[i] = has && lane < R ? lm_half<F16>(gld<uint16_t>(bank + static_cast<int64_t>(min(n0 + i, n - 1)) * R + lane)) : 0.f;
+#pragma unroll
+  for (int i = 0; i < RW; ++i) {
+    const float all = lm_wave_sum(v[i]);
+    if (lane == 0) s_v[r0 + i] = has ? all : 0.f;
+    if (p.act != nullptr && blockIdx.x == 0 && lane == 0 && r0 + i < R) gst<float>(p.act + r0 + i, has ? all : 0.f);
+  }
+  __syncthreads();
+  const float s = has && p.scale != nullptr ? gld<float>(p.scale + l) : 1.f;
+  const float vr = lane < R ? s_v[lane] * s : 0.f;
+#pragma unroll
+  for (int i = 0; i < ONE_C; ++i) {
+    // a rank's product is a term of the wavefront's sum, as the columns' are
+    float all = lm_wave_sum(has ? __builtin_fmaf(vr, b[i], sum[i]) : sum[i]);
+    if (lane != 0 || n0 + i >= n) continue;
+    if (p.bias != nullptr) all += lm_half<F16>(gld<uint16_t>(static_cast<const uint16_t*>(p.bias) + n0 + i));
+    gst<OutT>(static_cast<OutT*>(p.out) + n0 + i, static_cast<OutT>(all));
+  }
+}
+
+// ---------------------------------------------------------------------------
 // grads: for a chunk of an adapter's rows, 128 columns of x (or go) and 16 NB ranks,
 //   ROWS == false: ga[l, r, c] = sum_t u[t, r] x[t, c]
 //   ROWS == true:  gb[l, c, r] = sum_t v[t, r] go[t, c]
@@ -1530,15 +1603,17 @@ int lm_wide_splits(int64_t T, int64_t n, int64_t k) {
 
 // Few rows: as long as the fmas of the finish, and in the backward pass of the adapters'
 // gradients, cost less than the plan and the launches that the MFMAs need.  us, few rows and
-// many, forward: n = k = 4096, rank 16, 256 rows 32 and 34, 384 rows 55 and 39; rank 64, 128
-// rows 32 and 40, 192 rows 45 and 39; n 1024, k 2048, rank 16, 1024 rows 23 and 25; n 2048,
-// k 1024, rank 128, 128 rows 25 and 24.  With the backward pass: n = k = 4096, rank 16, 256
-// rows 74 and 82; rank 64, 128 rows 74 and 97, 192 rows 106 and 95; n 1024, k 2048, 256 rows
-// 45 and 51, 384 rows 58 and 52.
+// many, forward: n = k = 4096, rank 16, 256 rows 31 and 35, 320 rows 46 and 39; rank 64, 96 rows
+// 31 and 33, 192 rows 44 and 36; n 1024, k 2048, rank 16, 1024 rows 22 and 29; n 512, k 4096,
+// rank 32, 768 rows (rows * k * rank: 100M) 29 and 31; n 256, k 4096, rank 64, 400 rows (104M)
+// 30 and 29; n 1024, k 8192, rank 32, 400 rows 43 and 40; past the balance n 2048, k 8192, rank
+// 16, 480 rows 52 and 49, and n 8192, k 4096, 128 rows 44 and 36.  With the backward pass: n = k
+// = 4096, rank 16, 256 rows 69 and 80; rank 64, 128 rows (84M) 71 and 84, 192 rows (126M) 96
+// and 87; n 1024, k 2048, rank 16, 256 rows 31 and 52.
 bool lm_small(const LmSizes& s, bool backward) {
   if (s.T <= 32) return true;
-  if (backward) return s.T <= 256 && s.T * (s.N + s.K) * (s.R + 16) <= 64000000;
-  return s.T <= 1024 && s.T * s.N * (s.R + 16) <= 36000000 && s.T * s.K * s.R <= 64000000;
+  if (backward) return s.T <= 256 && s.T * (s.N + s.K) * (s.R + 16) <= 100000000;
+  return s.T <= 1024 && s.T * s.N * (s.R + 16) <= 36000000 && s.T * s.K * s.R <= 100000000;
 }
 
 struct LmCarve {
@@ -1699,6 +1774,18 @@ mi_status lm_mm(const LmMm& a, float* parts, const int32_t* ids, hipStream_t st)
 template <bool F16, bool BT, typename OutT, typename GradT>
 mi_status lm_small_run(LmSmall p, hipStream_t st) {
   const char* what = BT ? "mm_lora_backward (few rows)" : "mm_lora (few rows)";
+  if constexpr (!BT) {
+    if (p.T == 1 && p.R <= 4 * ONE_W && (p.ca <= 6144 || p.cb >= 4096)) {
+      auto one = [&](auto rw) {
+        constexpr int RW = decltype(rw)::value;
+        hipLaunchKernelGGL((lm_one_kernel<F16, RW, OutT>),
+                           dim3(static_cast<unsigned>((p.cb + ONE_W * ONE_C - 1) / (ONE_W * ONE_C))),
+                           dim3(64 * ONE_W), 0, st, p);
+        return launch_status("mm_lora (one row)");
+      };
+      return p.R <= 2 * ONE_W ? one(std::integral_constant<int, 2>{}) : one(std::integral_constant<int, 4>{});
+    }
+  }
   const bool dense = p.out != nullptr;
   p.splits = lm_splits(p.T, p.mm.n, p.mm.k);
   p.tiles = (p.T + 63) / 64 * ((p.mm.n + 63) / 64);
