@@ -641,9 +641,10 @@ MI_API mi_status mi_mm_lora(const void* x, int64_t m, int64_t k, mi_dtype dtype,
  *   grad_a      grad_dtype [num_adapters, rank, k] (dtype or MI_F32), and
  *   grad_b      grad_dtype [num_adapters, n, rank]; both or neither (x is then not read)
  *   workspace   at least mi_mm_lora_workspace_size(..., 1) bytes
- * Requirements: as above; the gradients overlap nothing.  grad_a and grad_b of more
- * rows than a 31-bit byte offset reaches (m * max(n, k) of 2^30 or more) return
- * MI_EUNSUPPORTED.  m == 0 writes zeros to grad_a and grad_b.
+ * Requirements: as above; the gradients overlap nothing.  With grad_a and grad_b,
+ * MI_EUNSUPPORTED for more rows than one pass takes (2^22, or m * 2 * max(n, k) or
+ * m * 6 * rank, rank to the next 16, of 2^31 bytes or more, rows in whole 256s) and for
+ * num_adapters * rank * (n + k) of 2^35 or more.  m == 0 writes zeros to grad_a and grad_b.
  */
 MI_API mi_status mi_mm_lora_backward(const void* grad_out, const void* x, int64_t m, int64_t k,
                                   mi_dtype dtype, const void* w, int64_t n, const void* lora_a,

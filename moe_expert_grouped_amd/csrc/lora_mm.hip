@@ -1942,6 +1942,9 @@ extern "C" mi_status mi_mm_lora_backward(const void* grad_out, const void* x, in
                  aligned16(lora_b) && aligned16(act) && aligned16(grad_x) && aligned16(grad_a) &&
                  aligned16(grad_b),
              "%s: the tensors must be 16-byte aligned", what);
+  // a grid has at most 2^32 - 1 threads along x: those of few rows' gradients are 1 / 16 of the banks
+  MI_REQUIRE_SUPPORTED(!banks || num_adapters * rank * (n + k) < (1LL << 35),
+                       "%s: num_adapters * rank * (n + k) below 2^35 required for the adapters' gradients", what);
   if (m == 0 && !banks) return MI_OK;
   const int64_t bank = num_adapters * rank, ges = grad_dtype == MI_F32 ? 4 : 2;
   const struct { const void* p; int64_t n; } outs[3] = {

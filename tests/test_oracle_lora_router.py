@@ -152,6 +152,8 @@ def test_lora_refusals():
     assert "workspace needs" in c(wsb=100)
     assert "take at most" in c(m=1 << 20, n=1 << 14, go=1 << 40, x=1 << 44, gx=1 << 45, act=1 << 46, ids=1 << 47,
                                ws=1 << 50, wsb=1 << 48)
+    for m in (20, 0):  # banks whose gradients a launch could not cover
+        assert "below 2^35" in c(m=m, n=(1 << 20) - 8, k=1016, L=1024, R=256)
     assert _call("mi_mm_lora_backward", BACK, m=0, ga=None, gb=None) == _lib.MI_OK
     L = _lib.lib()
     assert L.mi_mm_lora_workspace_size(40, 72, 64, 3, 12, 0) == 0
