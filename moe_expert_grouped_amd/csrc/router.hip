@@ -237,8 +237,8 @@ struct RtRoute {
 // top_k.  A lane sorts its own values; then k times the largest of the lanes' heads is
 // taken and its lane moves on.  Keys are unique, so no choice depends on the layout.
 // Lane j keeps choice j and computes its weight from the logit that the key holds.
-// Bound by the VALU: 32768 tokens, 128 experts, top 8, bf16: 13.3 us with the values left
-// unsorted and three butterflies a choice.
+// Bound by the VALU: 32768 tokens, 128 experts, top 8, bf16: 8.8 us (10.5 MB), 13.3 with the
+// values left unsorted and three butterflies a choice.
 // ---------------------------------------------------------------------------
 template <typename T, int G, int VPL>
 __global__ __launch_bounds__(256) void rt_route_kernel(RtRoute a) {
@@ -291,7 +291,9 @@ __global__ __launch_bounds__(256) void rt_route_kernel(RtRoute a) {
 // stay in its registers over all of a workgroup's rows; then they are added in a
 // fixed order, over the workgroup in LDS and over the workgroups by a second
 // launch, whose workgroups have 64 experts each and leave the loss's terms to the last
-// of them to end.  One workgroup does it all for a small batch.  No atomic adds floats.
+// of them to end.  One workgroup does it all for a small batch.  No atomic adds floats.  Bound by
+// latency, of a few rows' loads for every wavefront, then of the second launch's: 16411 tokens
+// of 256 experts in fp32: 9.6 and 7.5 us (17 MB); 512 tokens of 64 in one launch 9.8.
 // ---------------------------------------------------------------------------
 struct RtBalance {
   const void* logits;
@@ -493,7 +495,9 @@ __global__ __launch_bounds__(RT_BT) void rt_balance_finish_kernel(RtBalance a) {
 }
 
 // ---------------------------------------------------------------------------
-// backward
+// backward.  A row is read and written once: 16411 tokens of 256 experts in fp32, of the
+// loss: 12.7 us (34 MB: 2.6 TB/s, the grid's start and end among it); through the weights of
+// 6 choices as well, 16384 tokens of 64: 6.4 us.
 // ---------------------------------------------------------------------------
 struct RtBackward {
   const void* logits;

@@ -30,6 +30,10 @@ passage of the source pages it follows (cited by page title and section):
   -> :mod:`oracle.fp4_quantize`
 - FC1 (gate/up) LoRA delta, the ``gemm1_lora_delta`` the delta page's
   description names -> :mod:`oracle.fc1_lora_delta`
+- the projection with low-rank adapters and its gradients (the formulas of
+  ``mi_moe.h``) -> :mod:`oracle.lora_mm`
+- the router's top_k, counts, balance loss and gradients (the formulas of
+  ``mi_moe.h``) -> :mod:`oracle.router`
 
 Inputs are numpy arrays; bf16 tensors are passed as their uint16 bit patterns.
 
