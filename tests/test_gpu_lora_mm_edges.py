@@ -12,6 +12,7 @@ from oracle import lora_mm as O
 pytestmark = pytest.mark.gpu
 
 BF, F16 = torch.bfloat16, torch.float16
+ONE = (1, 136, 264, 3, 32)  # a single row (one launch)
 # few rows (two launches) and many (the plan and the MFMA tiles)
 SIZES = [(20, 136, 264, 3, 16), (400, 520, 264, 5, 40), (1500, 264, 136, 4, 24)]
 
@@ -34,7 +35,7 @@ def _same(p, q):
 
 
 @pytest.mark.parametrize("dtype", [BF, F16], ids=str)
-@pytest.mark.parametrize("T,N,K,L,R", SIZES)
+@pytest.mark.parametrize("T,N,K,L,R", [ONE, *SIZES])
 def test_no_row_has_an_adapter(gpu, T, N, K, L, R, dtype):
     print(f"mm_lora without adapters T={T} {dtype}", flush=True)
     (x, w, a, b, ids, scale), go = _case(T, N, K, L, R, dtype, gpu)
@@ -46,6 +47,25 @@ def test_no_row_has_an_adapter(gpu, T, N, K, L, R, dtype):
         assert not act.any() and not ga.any() and not gb.any()
         assert torch.allclose(out.float(), x.float() @ w.float().t(), rtol=0.02, atol=0.02)
         assert torch.allclose(gx.float(), go.float() @ w.float(), rtol=0.02, atol=0.05 * N ** 0.5 * K ** -0.5)
+
+
+@pytest.mark.parametrize("R", [8, 16, 24, 32])
+def test_one_rows_own_adapter(gpu, R):
+    """Small whole numbers, so that every sum is exact; the other adapters hold NaN."""
+    print(f"mm_lora of one row R={R}", flush=True)
+    g = synth.gen(R)
+    whole = lambda *s: torch.randint(-2, 3, s, generator=g).to(BF).to(gpu)
+    for N, K in ((8, 8), (24, 520), (136, 1032)):
+        for l in (0, 2):
+            x, w, a, b = whole(1, K), whole(N, K), whole(3, R, K), whole(3, N, R)
+            others = [i for i in range(3) if i != l]
+            a[others], b[others] = float("nan"), float("nan")
+            ids = torch.tensor([l], dtype=torch.int32, device=gpu)
+            out, act = mi.mm_lora(x, w, a, b, ids, out_dtype=torch.float32, with_act=True)
+            torch.cuda.synchronize()
+            v = x.double().cpu() @ a[l].double().cpu().t()
+            assert torch.equal(act.double().cpu(), v)
+            assert torch.equal(out.double().cpu(), x.double().cpu() @ w.double().cpu().t() + v @ b[l].double().cpu().t())
 
 
 @pytest.mark.parametrize("dtype", [BF, F16], ids=str)
@@ -191,7 +211,7 @@ def test_rows_past_a_31_bit_offset(gpu):
         mi.mm_lora_backward(x, out[:, :N].to(BF), w2, a2, b2, ids)
 
 
-@pytest.mark.parametrize("T,N,K,L,R", SIZES)
+@pytest.mark.parametrize("T,N,K,L,R", [ONE, *SIZES])
 def test_in_a_graph(gpu, T, N, K, L, R):
     print(f"mm_lora in a graph T={T}", flush=True)
     args, go = _case(T, N, K, L, R, BF, gpu)
