@@ -583,17 +583,17 @@ __device__ __forceinline__ void lm_wait_barrier() {
 
 // Where a tile lies in the call: m-tiles in groups of GM sweep the n-panels together,
 // and each XCD has a contiguous run of that order (workgroup ids go to the 8 in turn).
-struct LmPlace { int m0, n0, rows, cols, k0, steps; };
+struct LmPlace { int m0, n0, rows, cols, k0, steps, first; };  // first: PART's
 template <int BM, int BN>
 __device__ __forceinline__ LmPlace lm_place(const LmMm& p, int block) {
   const int nt = (p.n + BN - 1) / BN, mt = (p.T + BM - 1) / BM;
   const int total = nt * mt, per = (total + 7) / 8;
   const int slot = block >> 3, tile = (block & 7) * per + slot;
-  if (slot >= per || tile >= total) return {0, 0, 0, 0, 0, 0};
+  if (slot >= per || tile >= total) return {0, 0, 0, 0, 0, 0, 0};
   constexpr int GM = BM >= 256 ? 4 : 8;
   const int grp = tile / (GM * nt), in = tile - grp * GM * nt, gsz = min(mt - grp * GM, GM);
   const int m0 = (grp * GM + in % gsz) * BM, n0 = in / gsz * BN;
-  return {m0, n0, min(p.T - m0, BM), min(p.n - n0, BN), 0, (p.k + LM_BK - 1) / LM_BK};
+  return {m0, n0, min(p.T - m0, BM), min(p.n - n0, BN), 0, (p.k + LM_BK - 1) / LM_BK, 0};
 }
 
 // the LDS of one step: w's rows, and x's, of two stages in two halves
@@ -613,7 +613,8 @@ struct LmStage { uint8_t *w, *x0, *x1; };
 // behind it the stage is free for the loads of step kt + NST and the next stage is
 // complete, so the last regions read the next step's first fragments.
 //
-// PART: only the steps [t.k0, t.k0 + t.steps), rows in their own order, no adapters.
+// PART: only the steps [t.k0, t.k0 + t.steps), from the t.first-th of them on and round, rows
+// in their own order, no adapters.
 template <bool F16, bool BT, bool PART, int WM, int WN, int FM, int FN, int NST, typename OutT>
 __device__ __forceinline__ void lm_tile(const LmMm& p, const LmPlace& t, LmStage s0, LmStage s1,
                                         LmStage s2, LmStage s3, i32x2* s_order) {
@@ -674,7 +675,12 @@ __device__ __forceinline__ void lm_tile(const LmMm& p, const LmPlace& t, LmStage
   // Loads [first, first + count) of the NI of a stage, in the order of `nth`.  A step past
   // the last loads zeros: the steps stay free of branches.
   auto dma = [&](const LmStage& st, int kt, int first, int count) {
-    const int kb = k0 + min(kt, KT - 1);
+    int in = min(kt, KT - 1);
+    if constexpr (PART) {
+      in += t.first;
+      if (in >= KT) in -= KT;
+    }
+    const int kb = k0 + in;
     const uint32_t drop = kt >= KT ? LM_OUT : 0u, dropa = kb == last ? drop | tail : drop;
     const uint32_t so = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(kb) * (LM_BK * 2));
     const uint32_t sob =
@@ -1139,9 +1145,16 @@ __global__ __launch_bounds__(256) void lm_parts_kernel(LmSmall p) {
     LmMm mm = p.mm;
     mm.out = static_cast<float*>(p.mm.out) + static_cast<int64_t>(split) * p.T * mm.n;
     const int m0 = tile % mt * 64, n0 = tile / mt * 64;
+    // Long parts of few row blocks start at their panel's own step: where k is a multiple of a
+    // large power of two, tiles at the same step ask for lines that lie in a few memory
+    // channels.  us, without and with it: n 8192, k 4096, 128 rows 44 and 30; n 2048, k 8192,
+    // 256 rows 45 and 36; n = k = 4096, 192 rows 26 and 27, 256 rows 31 and 31; with six row
+    // blocks and more (n 2048, k 8192, 384 rows) 45 and 47, with 32 steps (128 rows, n = k =
+    // 4096) 21 and 21.
+    const int first = mt <= 4 && k1 - k0 >= 40 ? tile / mt % (k1 - k0) : 0;
     lm_tile<F16, BT, true, 2, 2, 2, 2, 4, float>(
-        mm, {m0, n0, min(p.T - m0, 64), min(mm.n - n0, 64), k0, k1 - k0}, stage(s0), stage(s1), stage(s2),
-        stage(s3), s_order);
+        mm, {m0, n0, min(p.T - m0, 64), min(mm.n - n0, 64), k0, k1 - k0, first}, stage(s0), stage(s1),
+        stage(s2), stage(s3), s_order);
     return;
   }
   const int wave = (block - p.gemm) * 4 + (threadIdx.x >> 6), waves = p.dots * 4;
@@ -1617,8 +1630,8 @@ int lm_wide_splits(int64_t T, int64_t n, int64_t k) {
 // many, forward: n = k = 4096, rank 16, 256 rows 31 and 35, 320 rows 46 and 39; rank 64, 96 rows
 // 31 and 33, 192 rows 44 and 36; n 1024, k 2048, rank 16, 1024 rows 22 and 29; n 512, k 4096,
 // rank 32, 768 rows (rows * k * rank: 100M) 29 and 31; n 256, k 4096, rank 64, 400 rows (104M)
-// 30 and 29; n 1024, k 8192, rank 32, 400 rows 43 and 40; past the balance n 2048, k 8192, rank
-// 16, 480 rows 52 and 49, and n 8192, k 4096, 128 rows 44 and 36.  With the backward pass: n = k
+// 30 and 29; n 1024, k 8192, rank 32, 400 rows 43 and 40; n 8192, k 4096, rank 16, 128
+// rows 30 and 36; past the balance n 2048, k 8192, rank 16, 480 rows 52 and 49.  With the backward pass: n = k
 // = 4096, rank 16, 256 rows 69 and 80; rank 64, 128 rows (84M) 71 and 84, 192 rows (126M) 96
 // and 87; n 1024, k 2048, rank 16, 256 rows 31 and 52.
 bool lm_small(const LmSizes& s, bool backward) {

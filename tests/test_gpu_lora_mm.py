@@ -65,7 +65,9 @@ def _case(T, N, K, L, R, dtype, kind, exact, seed):
 
 # rows from one to several tiles, sizes that end inside a step, a tile and an item
 SHAPES = [(1, 8, 8, 1, 8, "mixed"), (1, 520, 1032, 4, 16, "mixed"), (1, 4104, 72, 2, 24, "mixed"), (1, 64, 4096, 3, 32, "few"),
-          (1, 136, 520, 1, 40, "few"), (2, 4104, 264, 3, 32, "mixed"), (3, 136, 72, 5, 8, "mixed"),
+          (1, 136, 520, 1, 40, "few"), (2, 4104, 264, 3, 32, "mixed"),
+          # tiles of few rows that start at their own step, the last of them short
+          (150, 4104, 2600, 3, 16, "mixed"), (150, 2600, 4104, 3, 16, "mixed"), (3, 136, 72, 5, 8, "mixed"),
           (15, 64, 264, 2, 24, "few"), (16, 256, 512, 16, 16, "mixed"), (17, 264, 640, 9, 40, "mixed"),
           (33, 1024, 136, 64, 64, "mixed"), (64, 512, 256, 64, 16, "mixed"), (65, 128, 96, 3, 72, "few"),
           (100, 392, 328, 7, 32, "runs"), (130, 264, 200, 2, 128, "runs"), (257, 200, 456, 1, 16, "few"),
