@@ -610,9 +610,8 @@ MI_API mi_status mi_moe_combine_rows_backward(
  *               mi_mm_lora_backward takes
  *   workspace   at least mi_mm_lora_workspace_size(..., 0) bytes, 256-byte aligned, no
  *               initialisation needed
- * v is kept to 16 bits at least (24 for fp32 outputs) for the second product, and all
- * sums are fp32.  What one request's rows or adapter hold, NaN among it, changes no
- * other request's rows.
+ * v is kept to 24 bits for the second product, and all sums are fp32.  What one
+ * request's rows or adapter hold, NaN among it, changes no other request's rows.
  * Requirements: n % 8 == 0, k % 8 == 0, rank a multiple of 8 in [8, 256],
  * num_adapters in [1, 1024], everything but lora_ids and lora_scale 16-byte aligned,
  * out and act overlap nothing.  n or k of 2^20 or more, or n * k of 2^30 or more,

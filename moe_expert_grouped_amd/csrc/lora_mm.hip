@@ -822,11 +822,11 @@ __device__ __forceinline__ void lm_tile(const LmMm& p, const LmPlace& t, LmStage
   lm_wait_barrier<0>();
 
   // The adapters, one run of rows after another, in steps of the same kind: the reduction
-  // runs over the first NP pieces of v (RP ranks each), 64 at a time, x's place taken by a
+  // runs over the NP pieces of v (RP ranks each), 64 at a time, x's place taken by a
   // row's pieces and w's by the bank's ranks, once for every piece.  A step's loads
-  // go out one step ahead.  Two pieces hold v to 2^-17, where the output's own half step is
-  // 2^-8 or 2^-11; three, 24 bits, for fp32 outputs.
-  constexpr int NP = sizeof(OutT) == 4 ? 3 : 2;
+  // go out one step ahead.  All three pieces, for 16-bit outputs too: where the two parts
+  // cancel, what two leave, 2^-17 of the adapters' part, may be more than the sum's half step.
+  constexpr int NP = 3;
   const int RP = p.RP, R = p.R, E = NP * RP;
   int id_at[FM];
 #pragma unroll
