@@ -611,7 +611,8 @@ MI_API mi_status mi_moe_combine_rows_backward(
  *   workspace   at least mi_mm_lora_workspace_size(..., 0) bytes, 256-byte aligned, no
  *               initialisation needed
  * v is kept to 24 bits for the second product, and all sums are fp32.  What one
- * request's rows or adapter hold, NaN among it, changes no other request's rows.
+ * request's rows or adapter hold, NaN and infinities among it, changes no other request's
+ * rows, and gives in its own what the formula gives.
  * Requirements: n % 8 == 0, k % 8 == 0, rank a multiple of 8 in [8, 256],
  * num_adapters in [1, 1024], everything but lora_ids and lora_scale 16-byte aligned,
  * out and act overlap nothing.  n or k of 2^20 or more, or n * k of 2^30 or more,

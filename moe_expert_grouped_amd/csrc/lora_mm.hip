@@ -283,17 +283,58 @@ __device__ __forceinline__ f32x4 lm_mfma(u32x4 a, u32x4 b, f32x4 c) {
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-// bf16 pieces of v: each the rounding of what the ones before leave, 24 bits together;
-// where the first is not finite the others are 0
+template <bool F16>
+__device__ __forceinline__ float lm_half(uint16_t h) {
+  return F16 ? static_cast<float>(__builtin_bit_cast(_Float16, h)) : bf16_bits_to_f32(h);
+}
+
+// bf16 pieces of v: each the rounding of what the ones before leave, 24 bits together.  A finite
+// v past the largest bf16 has that one as its first.  An infinity or NaN is the last piece,
+// behind 1 with its sign: the products with the first two stay finite.
 struct LmPieces { uint16_t p[3]; };
 __device__ __forceinline__ LmPieces lm_pieces(float v) {
+  const uint32_t bits = __float_as_uint(v);
   LmPieces o;
+  if ((bits & 0x7f800000u) == 0x7f800000u) {
+    o.p[0] = static_cast<uint16_t>((bits >> 16 & 0x8000u) | 0x3f80u);
+    o.p[1] = 0;
+    o.p[2] = static_cast<uint16_t>(bits >> 16 | (bits & 0xffffu ? 1u : 0u));
+    return o;
+  }
   float rest = v;
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
-    const __bf16 h = static_cast<__bf16>(rest);
-    o.p[i] = __builtin_bit_cast(uint16_t, h);
-    rest = (o.p[i] & 0x7f80) == 0x7f80 ? 0.f : rest - static_cast<float>(h);
+    uint16_t h = __builtin_bit_cast(uint16_t, static_cast<__bf16>(rest));
+    if (i == 0 && (h & 0x7f80) == 0x7f80) --h;
+    o.p[i] = h;
+    rest -= bf16_bits_to_f32(h);
+  }
+  return o;
+}
+
+// A sum over pieces takes an infinity or NaN of its other factor once, with the first piece and
+// on its own: the later pieces are 0 or of the other sign, and would make NaN of an infinity.
+// In the sum itself 1 with its sign stands in its place.
+//
+// The largest magnitudes of bf16 values, two a word and each doubled, and whether one of
+// them is not finite
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ u16x2 lm_top(u32x4 q, u16x2 top) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, q[i] << 1));
+  return top;
+}
+__device__ __forceinline__ bool lm_odd(u16x2 top) { return max(top.x, top.y) >= 0xff00; }
+// the values that are not finite (else 0), and those that are (else 1 with the sign)
+struct LmOdd { u32x4 odd, rest; };
+__device__ __forceinline__ LmOdd lm_part(u32x4 q) {
+  LmOdd o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t hit = ((q[i] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+    const uint32_t low = hit - (hit >> 15);  // all bits but the sign
+    o.odd[i] = q[i] & (hit | low);
+    o.rest[i] = (q[i] & ~low) | (0x3f803f80u & low);
   }
   return o;
 }
@@ -828,9 +869,6 @@ __device__ __forceinline__ void lm_tile(const LmMm& p, const LmPlace& t, LmStage
   // cancel, what two leave, 2^-17 of the adapters' part, may be more than the sum's half step.
   constexpr int NP = 3;
   const int RP = p.RP, R = p.R, E = NP * RP;
-  int id_at[FM];
-#pragma unroll
-  for (int i = 0; i < FM; ++i) id_at[i] = s_order[(wm * FM + i) * 16 + r].y;
   struct Run { int l, at, end, e; };  // rows [at, end) of adapter l, from reduction index e on
   auto run_at = [&](int at) {
     const int l = at < rows ? __builtin_amdgcn_readfirstlane(s_order[at].y) : p.L;
@@ -870,9 +908,12 @@ __device__ __forceinline__ void lm_tile(const LmMm& p, const LmPlace& t, LmStage
       __builtin_amdgcn_raw_ptr_buffer_load_lds(lr_, lm_lds(st.w + (NW * i + wave) * 1024), 16, at, 0, 0, 0);
     }
   };
-  // blocks all in the run take the sums as they come; in one that it shares, only its own
-  // rows' lanes do: a NaN in this adapter's bank is not another row's
+  // Rows of other adapters in a block have zeros for their pieces.  What is not finite in the
+  // bank is left for the end.
+  const int w0 = wm * FM * 16;
+  bool odd = false;
   auto adapt = [&](const LmStage& st, const Run& u) {
+    if (u.at >= w0 + FM * 16 || u.end <= w0) return;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (h == 1 && u.e + 32 >= E) break;
@@ -884,29 +925,30 @@ __device__ __forceinline__ void lm_tile(const LmMm& p, const LmPlace& t, LmStage
         else b[j] = *reinterpret_cast<const u32x4*>(st.w + (wn * FN + j) * 2048 + fo[h]);
       }
       u32x4 a0 = half_a(0), a1 = half_a(1);
-      if constexpr (F16)
+      u16x2 top = {0, 0};
 #pragma unroll
-        for (int j = 0; j < FN; ++j) lm_split(b[j], b[j], lo[j]);
+      for (int j = 0; j < FN; ++j) {
+        if constexpr (F16) lm_split(b[j], b[j], lo[j]);
+        top = lm_top(b[j], top);
+      }
+      if (__builtin_expect(__any(lm_odd(top)), 0)) {
+        odd = true;
+#pragma unroll
+        for (int j = 0; j < FN; ++j) b[j] = lm_part(b[j]).rest;
+      }
+      // fp16's second piece with the first two of v; the halves do not mix the second and the last
+      const bool two = F16 && u.e + 32 * h < 2 * RP;
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
         const u32x4 a = a0;
         a0 = a1;
         if (i + 2 < FM) a1 = half_a(i + 2);
-        const int b0 = (wm * FM + i) * 16;
-        if (b0 + 16 <= u.at || b0 >= u.end) continue;
-        f32x4 d[FN];
+        if (w0 + 16 * i + 16 <= u.at || w0 + 16 * i >= u.end) continue;
 #pragma unroll
-        for (int j = 0; j < FN; ++j) d[j] = lm_mfma<false>(b[j], a, acc[i][j]);
-        if constexpr (F16)
+        for (int j = 0; j < FN; ++j) acc[i][j] = lm_mfma<false>(b[j], a, acc[i][j]);
+        if (two)
 #pragma unroll
-          for (int j = 0; j < FN; ++j) d[j] = lm_mfma<false>(lo[j], a, d[j]);
-        if (b0 >= u.at && b0 + 16 <= u.end) {
-#pragma unroll
-          for (int j = 0; j < FN; ++j) acc[i][j] = d[j];
-        } else if (id_at[i] == u.l) {
-#pragma unroll
-          for (int j = 0; j < FN; ++j) acc[i][j] = d[j];
-        }
+          for (int j = 0; j < FN; ++j) acc[i][j] = lm_mfma<false>(lo[j], a, acc[i][j]);
       }
     }
   };
@@ -958,19 +1000,53 @@ __device__ __forceinline__ void lm_tile(const LmMm& p, const LmPlace& t, LmStage
 #pragma unroll
   for (int i0 = 0; i0 < FM; i0 += PB) {
 #pragma unroll
-    for (int i = i0; i < i0 + PB; ++i)
+    for (int i = i0; i < i0 + PB; ++i) {
+      uint8_t* const blk = reg + (i - i0) * 16 * RBY;
+      f32x4 v[FN];
+#pragma unroll
+      for (int j = 0; j < FN; ++j) v[j] = acc[i][j] + bias[j];
+      // What is not finite in the banks, times the first piece, for its own rows (-0 elsewhere,
+      // which adds nothing).  Rare, and so a plain loop over the ranks.
+      if (__builtin_expect(odd, 0)) {
+#pragma unroll 1
+        for (int q = lane; q < 256 * FN; q += 64) {
+          const i32x2 t = s_order[w0 + 16 * i + q / (16 * FN)];
+          const int c = wn * 16 * FN + q % (16 * FN);
+          float sum = -0.f;
+          if (t.x >= 0 && t.y < p.L && c < cols) {
+            const uint16_t* const bank = static_cast<const uint16_t*>(p.bank) + static_cast<int64_t>(t.y) * R * n;
+            const uint16_t* const piece = p.pieces + static_cast<int64_t>(t.x) * 3 * RP;
+#pragma unroll 1
+            for (int rk = 0; rk < R; ++rk) {
+              const float f = lm_half<F16>(gld<uint16_t>(
+                  bank + (BT ? static_cast<int64_t>(rk) * n + n0 + c : static_cast<int64_t>(n0 + c) * R + rk)));
+              if (!__builtin_isfinite(f)) sum += bf16_bits_to_f32(gld<uint16_t>(piece + rk)) * f;
+            }
+          }
+          reinterpret_cast<uint16_t*>(blk)[q] = static_cast<uint16_t>(sum != sum ? 0x7fc0u : __float_as_uint(sum) >> 16);
+        }
+        asm volatile("" ::: "memory");  // LDS operations of one wavefront complete in order
+        u32x2 c[FN];
+#pragma unroll
+        for (int j = 0; j < FN; ++j) c[j] = *reinterpret_cast<const u32x2*>(blk + (r * 16 * FN + 16 * j + 4 * g) * 2);
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[j][e] += bf16_bits_to_f32(c[j][e >> 1] >> (16 * (e & 1)) & 0xffffu);
+      }
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
-        const f32x4 v = acc[i][j] + bias[j];
-        uint8_t* const at = reg + ((i - i0) * 16 + r) * RBY;
+        uint8_t* const at = blk + r * RBY;
         if constexpr (ES == 4) {
-          *reinterpret_cast<f32x4*>(at + ((4 * j + g) ^ (r % CPR)) * 16) = v;
+          *reinterpret_cast<f32x4*>(at + ((4 * j + g) ^ (r % CPR)) * 16) = v[j];
         } else {
           typedef OutT t4 __attribute__((ext_vector_type(4)));
           *reinterpret_cast<t4*>(at + ((2 * j + (g >> 1)) ^ (r % CPR)) * 16 + (g & 1) * 8) =
-              __builtin_convertvector(v, t4);
+              __builtin_convertvector(v[j], t4);
         }
       }
+    }
     // LDS operations of one wavefront complete in order
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
@@ -1056,10 +1132,6 @@ __device__ __forceinline__ void lm_unpack(u32x4 q, float (&o)[8]) {
       o[2 * i + 1] = __uint_as_float(q[i] & 0xffff0000u);
     }
   }
-}
-template <bool F16>
-__device__ __forceinline__ float lm_half(uint16_t h) {
-  return F16 ? static_cast<float>(__builtin_bit_cast(_Float16, h)) : bf16_bits_to_f32(h);
 }
 __device__ __forceinline__ float lm_wave_sum(float v) {
 #pragma unroll
@@ -1465,17 +1537,29 @@ __device__ __forceinline__ void lm_grad(const LmGrad& a, uint8_t* st0, uint8_t* 
         fx[j] = lm_column(at, at + 4 * GR_BN * 2);
         if constexpr (F16) lm_split(fx[j], fx[j], fl[j]);
       }
+      auto pieces = [&](int b, int c) {
+        return *reinterpret_cast<const u32x4*>(st + GR_X + (b * 3 + c) * 2048 + r * 128 + (ck ^ lm_swz(r)) * 16);
+      };
+      auto mfma = [](u32x4 x, u32x4 p, f32x4 c) { return ROWS ? lm_mfma<false>(p, x, c) : lm_mfma<false>(x, p, c); };
+      if (__builtin_expect(__any(lm_odd(lm_top(fx[1], lm_top(fx[0], u16x2{0, 0})))), 0)) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const LmOdd o = lm_part(fx[j]);
+          fx[j] = o.rest;
+#pragma unroll
+          for (int b = 0; b < NB; ++b) acc[b][j] = mfma(o.odd, pieces(b, 0), acc[b][j]);
+        }
+      }
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int c = 0; c < 3; ++c) {
-          const u32x4 fp = *reinterpret_cast<const u32x4*>(st + GR_X + (b * 3 + c) * 2048 + r * 128 + (ck ^ lm_swz(r)) * 16);
+          const u32x4 fp = pieces(b, c);
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            acc[b][j] = ROWS ? lm_mfma<false>(fp, fx[j], acc[b][j]) : lm_mfma<false>(fx[j], fp, acc[b][j]);
+            acc[b][j] = mfma(fx[j], fp, acc[b][j]);
             if constexpr (F16) {
-              if (c < 2)
-                acc[b][j] = ROWS ? lm_mfma<false>(fp, fl[j], acc[b][j]) : lm_mfma<false>(fl[j], fp, acc[b][j]);
+              if (c < 2) acc[b][j] = mfma(fl[j], fp, acc[b][j]);
             }
           }
         }
