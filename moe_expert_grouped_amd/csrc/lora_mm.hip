@@ -44,7 +44,6 @@ struct LmPlan {
   int* rank;        // [T] of a row among its chunk's rows of its adapter
   int* counts;      // [chunks, L + 1] of adapters' rows
   i32x2* order;     // [T] {row, adapter}; rows without one last, adapter L
-  int* seg;         // [L + 1] first position of every adapter
   int* item_id;     // adapter of every item
   int* slot_row;    // [LM_ITEM * items] row of every slot of an item, -1: none
   i32x4* chunks;     // {adapter, first item, items, place of its partial sums or -1}
@@ -217,7 +216,6 @@ __global__ __launch_bounds__(PL_T) void lm_place_kernel(const int32_t* __restric
     s_seg[tid] = seg;
     s_item0[tid] = item0;
     if (lists) {
-      gst<int>(p.seg + tid, seg);
 #pragma unroll 1
       for (int c = 0; c < chunks; ++c)
         gst<i32x4>(p.chunks + chunk0 + c,
@@ -237,7 +235,6 @@ __global__ __launch_bounds__(PL_T) void lm_place_kernel(const int32_t* __restric
     s_item0[L] = real;
     s_item0[L + 1] = real + more;
     if (lists) {
-      gst<int>(p.seg + L, in);
       gst<i32x4>(p.totals, i32x4{real, static_cast<int>(all.b), real + more, 0});
       gst<u32x4>(p.zeros, u32x4{0, 0, 0, 0});
 #pragma unroll 1
@@ -862,25 +859,32 @@ __device__ __forceinline__ void lm_tile(const LmMm& p, const LmPlace& t, LmStage
   // the loads of the steps past the last have written their zeros
   lm_wait_barrier<0>();
 
-  // The adapters, one run of rows after another, in steps of the same kind: the reduction
-  // runs over the NP pieces of v (RP ranks each), 64 at a time, x's place taken by a
-  // row's pieces and w's by the bank's ranks, once for every piece.  A step's loads
-  // go out one step ahead.  All three pieces, for 16-bit outputs too: where the two parts
-  // cancel, what two leave, 2^-17 of the adapters' part, may be more than the sum's half step.
-  constexpr int NP = 3;
-  const int RP = p.RP, R = p.R, E = NP * RP;
-  struct Run { int l, at, end, e; };  // rows [at, end) of adapter l, from reduction index e on
+  // The adapters, one run of rows after another and 64 ranks of an adapter at a time, in two
+  // stages: the bank's ranks take w's place in the first, and the three pieces of v x's place
+  // there and both places of the second.  Ranks up to 16 need one stage, with the pieces side by
+  // side in a row's 64 places and the bank's ranks once for each; the second stage has the next
+  // run.  (The bank's ranks staged again for every piece, us a call: 8192 rows, n = k = 4096, 16
+  // adapters of rank 64, 244 for 237; 1111 rows fp16, rank 40, with gradients 106 for 96.)  All
+  // three pieces, for 16-bit outputs too: where the two parts cancel, what two leave, 2^-17 of
+  // the adapters' part, may be more than the sum's half step.
+  const int RP = p.RP, R = p.R;
+  const bool one = RP == 16;
+  const int E = one ? 3 * RP : RP, mask = one ? 15 : -1;
+  struct Run { int l, at, end, e; };  // rows [at, end) of adapter l, from rank e on
   auto run_at = [&](int at) {
     const int l = at < rows ? __builtin_amdgcn_readfirstlane(s_order[at].y) : p.L;
     // the rows without an adapter are last
     if (l >= p.L) return Run{p.L, rows, rows, 0};
-    const int end = __builtin_amdgcn_readfirstlane(gld<int>(p.plan.seg + l + 1)) - m0;
-    return Run{l, at, max(min(end, rows), at + 1), 0};
+    int end = at;
+#pragma unroll
+    for (int i = 0; i < BM; i += 64) end += __popcll(__ballot(s_order[i + lane].y == l));
+    return Run{l, at, end, 0};
   };
-  auto after = [&](const Run& u) { return u.e + LM_BK < E ? Run{u.l, u.at, u.end, u.e + LM_BK} : run_at(u.end); };
+  auto after = [&](const Run& u) { return u.e + LM_BK < RP ? Run{u.l, u.at, u.end, u.e + LM_BK} : run_at(u.end); };
   const __amdgpu_buffer_rsrc_t pr_ =
       buf_rsrc(p.pieces, static_cast<uint32_t>(p.T) * static_cast<uint32_t>(RP) * 6u);
-  auto fetch = [&](const LmStage& st, const Run& u) {
+  auto last_piece = [](const LmStage& st) { return LmStage{nullptr, st.w, st.w + BM * 64}; };
+  auto fetch = [&](const LmStage& st, const LmStage& next, const Run& u) {
     if (u.l >= p.L) return;
     const __amdgpu_buffer_rsrc_t lr_ =
         buf_rsrc(static_cast<const uint16_t*>(p.bank) + static_cast<int64_t>(u.l) * R * n,
@@ -890,18 +894,21 @@ __device__ __forceinline__ void lm_tile(const LmMm& p, const LmPlace& t, LmStage
     for (int i = 0; i < NIA; ++i) {
       const int row = 8 * (NW * i + wave) + lr;
       const bool own = row >= u.at && row < u.end && e < E;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          pr_, lm_lds(to_x(st, i)), 16,
-          own ? (static_cast<uint32_t>(s_order[row].x) * 3 * RP + e) * 2 : LM_OUT, 0, 0, 0);
+      const uint32_t at = own ? (static_cast<uint32_t>(s_order[row].x) * 3 * RP + e) * 2 : LM_OUT;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(pr_, lm_lds(to_x(st, i)), 16, at, 0, 0, 0);
+      if (!one) {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(pr_, lm_lds(to_x(next, i)), 16, at, RP * 2, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(pr_, lm_lds(to_x(last_piece(next), i)), 16, at, RP * 4, 0, 0);
+      }
     }
 #pragma unroll
     for (int i = 0; i < NIB; ++i) {
       uint32_t at;
       if constexpr (!BT) {
-        const int row = 8 * (NW * i + wave) + lr, rk = e % RP;
+        const int row = 8 * (NW * i + wave) + lr, rk = e & mask;
         at = row < cols && e < E && rk < R ? (static_cast<uint32_t>(n0 + row) * R + rk) * 2 : LM_OUT;
       } else {
-        const int row = brow(i), c = lane % CPW, rk = (u.e + row) % RP;
+        const int row = brow(i), c = lane % CPW, rk = (u.e + row) & mask;
         const int col = (((c >> 1) ^ lm_tswz<BN>(row)) * 2 + (c & 1)) * 8;
         at = col < cols && u.e + row < E && rk < R ? (static_cast<uint32_t>(rk) * n + n0 + col) * 2 : LM_OUT;
       }
@@ -912,60 +919,90 @@ __device__ __forceinline__ void lm_tile(const LmMm& p, const LmPlace& t, LmStage
   // bank is left for the end.
   const int w0 = wm * FM * 16;
   bool odd = false;
-  auto adapt = [&](const LmStage& st, const Run& u) {
+  auto adapt = [&](auto pieces, const LmStage& st, const LmStage& next, const Run& u) {
     if (u.at >= w0 + FM * 16 || u.end <= w0) return;
+    u32x4 b[FN], lo[FN];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (h == 1 && u.e + 32 >= E) break;
-      auto half_a = [&](int i) { return *reinterpret_cast<const u32x4*>(block_x(st, i) + fo[h]); };
-      u32x4 b[FN], lo[FN];
+      if (h == 0 || !one) {  // side by side, both halves meet the same ranks
+        u16x2 top = {0, 0};
 #pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        if constexpr (BT) b[j] = column(st.w, wn * FN + j, ck * 8 + 32 * h);
-        else b[j] = *reinterpret_cast<const u32x4*>(st.w + (wn * FN + j) * 2048 + fo[h]);
+        for (int j = 0; j < FN; ++j) {
+          if constexpr (BT) b[j] = column(st.w, wn * FN + j, ck * 8 + 32 * h);
+          else b[j] = *reinterpret_cast<const u32x4*>(st.w + (wn * FN + j) * 2048 + fo[h]);
+        }
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          if constexpr (F16) lm_split(b[j], b[j], lo[j]);
+          top = lm_top(b[j], top);
+        }
+        if (__builtin_expect(__any(lm_odd(top)), 0)) {
+          odd = true;
+#pragma unroll
+          for (int j = 0; j < FN; ++j) b[j] = lm_part(b[j]).rest;
+        }
       }
-      u32x4 a0 = half_a(0), a1 = half_a(1);
-      u16x2 top = {0, 0};
 #pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        if constexpr (F16) lm_split(b[j], b[j], lo[j]);
-        top = lm_top(b[j], top);
-      }
-      if (__builtin_expect(__any(lm_odd(top)), 0)) {
-        odd = true;
+      for (int c = 0; c < pieces.value; ++c) {
+        if (c > 0 && one) break;
+        const LmStage& xs = c == 0 ? st : c == 1 ? next : last_piece(next);
+        auto half_a = [&](int i) { return *reinterpret_cast<const u32x4*>(block_x(xs, i) + fo[h]); };
+        // fp16's second piece with the first two of v
+        const bool two = F16 && (c == 0 ? !one || h == 0 : c == 1);
+        u32x4 a0 = half_a(0), a1 = half_a(1);
 #pragma unroll
-        for (int j = 0; j < FN; ++j) b[j] = lm_part(b[j]).rest;
-      }
-      // fp16's second piece with the first two of v; the halves do not mix the second and the last
-      const bool two = F16 && u.e + 32 * h < 2 * RP;
+        for (int i = 0; i < FM; ++i) {
+          const u32x4 a = a0;
+          a0 = a1;
+          if (i + 2 < FM) a1 = half_a(i + 2);
+          if (w0 + 16 * i + 16 <= u.at || w0 + 16 * i >= u.end) continue;
 #pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        const u32x4 a = a0;
-        a0 = a1;
-        if (i + 2 < FM) a1 = half_a(i + 2);
-        if (w0 + 16 * i + 16 <= u.at || w0 + 16 * i >= u.end) continue;
+          for (int j = 0; j < FN; ++j) acc[i][j] = lm_mfma<false>(b[j], a, acc[i][j]);
+          if (two)
 #pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = lm_mfma<false>(b[j], a, acc[i][j]);
-        if (two)
-#pragma unroll
-          for (int j = 0; j < FN; ++j) acc[i][j] = lm_mfma<false>(lo[j], a, acc[i][j]);
+            for (int j = 0; j < FN; ++j) acc[i][j] = lm_mfma<false>(lo[j], a, acc[i][j]);
+        }
       }
     }
   };
   // of a k axis in splits, the last one has the adapters
   if (!PART && k0 + KT == last + 1) {
+    constexpr std::integral_constant<int, 3> three{};
+    constexpr std::integral_constant<int, 1> first{};
     Run u = run_at(0);
-    fetch(s0, u);
-    while (u.l < p.L) {
-      const Run v = after(u);
-      lm_wait_barrier<0>();
-      fetch(s1, v);
-      adapt(s0, u);
-      if (v.l >= p.L) break;
-      u = after(v);
-      lm_wait_barrier<0>();
-      fetch(s0, u);
-      adapt(s1, v);
+    if constexpr (NST == 4) {
+      while (u.l < p.L) {  // as many as the stages hold at once
+        Run q[NST];
+#pragma unroll
+        for (int i = 0; i < NST; ++i) {
+          const bool more = i % 2 == 0 || one;
+          q[i] = more ? u : Run{p.L, rows, rows, 0};
+          if (more) u = after(u);
+        }
+#pragma unroll
+        for (int i = 0; i < NST; ++i) fetch(*sts[i], *sts[i ^ 1], q[i]);
+        lm_wait_barrier<0>();
+#pragma unroll
+        for (int i = 0; i < NST; i += 2) {
+          adapt(three, *sts[i], *sts[i + 1], q[i]);
+          if (one) adapt(first, *sts[i + 1], *sts[i], q[i + 1]);
+        }
+        if (u.l < p.L) lm_wait_barrier<0>();  // all have read what is there
+      }
+    } else {
+      fetch(s0, s1, u);
+      while (u.l < p.L) {  // of runs with one stage, the next one's loads beside this one's sums
+        lm_wait_barrier<0>();
+        const Run v = after(u);
+        if (one) fetch(s1, s0, v);
+        adapt(three, s0, s1, u);
+        if (v.l >= p.L) break;
+        lm_wait_barrier<0>();
+        u = one ? after(v) : v;
+        fetch(s0, s1, u);
+        if (one) adapt(first, s1, s0, v);
+      }
     }
   }
   // acc[i][j][q]: row 16 i + r, column 16 j + 4 g + q of the wavefront's.  The outputs go
@@ -1468,8 +1505,9 @@ __global__ __launch_bounds__(64 * ONE_W) void lm_one_kernel(LmSmall p) {
 //   ROWS == true:  gb[l, c, r] = sum_t v[t, r] go[t, c]
 // A step is 64 rows: those of x, and 64 slots of the transposed pieces, both by loads
 // straight into LDS; x is read down its columns.  A wavefront has 32 columns.  Bound by the
-// reads of x and go, once for all ranks up to 64: 8192 rows, n = k = 4096, rank 16: 29 us (134 MB:
-// 4.7 TB/s; the L2s fetch 148) and 5 for the partial sums.
+// reads of x and go, once for all ranks up to 64: 8192 rows, n = k = 4096, rank 16: 31 us (134 MB:
+// 4.3 TB/s; the L2s fetch 148; 2 us are the look at every value of x for one that is not finite)
+// and 5 for the partial sums.
 // ---------------------------------------------------------------------------
 struct LmGrad {
   const void* x;             // [T, C]
@@ -1757,7 +1795,6 @@ LmSpace lm_space(const LmSizes& s, bool backward, void* base) {
   o.plan.rank = c.take<int>(s.T);
   o.plan.counts = c.take<int>(64 * (s.L + 1));
   o.plan.order = c.take<i32x2>(s.T);
-  o.plan.seg = c.take<int>(s.L + 1);
   o.plan.item_id = c.take<int>(items);
   o.plan.slot_row = c.take<int>(items * LM_ITEM);
   o.plan.chunks = c.take<i32x4>(s.chunks());
