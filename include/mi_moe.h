@@ -609,7 +609,7 @@ MI_API mi_status mi_moe_combine_rows_backward(
  *   act         fp32 [m, rank] or NULL: v, 0 for rows without an adapter, which
  *               mi_mm_lora_backward takes
  *   workspace   at least mi_mm_lora_workspace_size(..., 0) bytes, 256-byte aligned, no
- *               initialisation needed
+ *               initialisation needed; what m rows need is enough for fewer, too
  * v is kept to 24 bits for the second product, and all sums are fp32.  What one
  * request's rows or adapter hold, NaN and infinities among it, changes no other request's
  * rows, and gives in its own what the formula gives.

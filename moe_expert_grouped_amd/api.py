@@ -959,7 +959,8 @@ def _lora_mm_bytes(m, n, k, num_adapters, rank, backward):
 
 
 def lora_mm_workspace_bytes(m, n, k, num_adapters, rank, *, backward: bool = False) -> int:
-    """Workspace of :func:`mm_lora` (or of :func:`mm_lora_backward`); 0 for sizes they refuse."""
+    """Workspace of :func:`mm_lora` (or of :func:`mm_lora_backward`) for ``m`` rows or fewer; 0 for
+    sizes they refuse."""
     return _lora_mm_bytes(m, n, k, num_adapters, rank, int(backward))
 
 

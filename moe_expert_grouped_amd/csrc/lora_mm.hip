@@ -1781,44 +1781,97 @@ struct LmSpace {
   size_t bytes;
 };
 
-LmSpace lm_space(const LmSizes& s, bool backward, void* base) {
+// what of many rows' space is not proportional to them
+struct LmMany {
+  int64_t parts;           // of a split k axis
+  int64_t chunks, places;  // of the gradients
+};
+
+// fp32 partial sums of a pass of `rows`; few where the k axis is not split
+int64_t lm_parts(int64_t rows, int64_t on, int64_t in) {
+  const int64_t sp = rows > 0 ? lm_wide_splits(rows, on, in) : 1;
+  return sp > 1 ? sp * rows * on : 0;
+}
+
+LmSpace lm_space_many(const LmSizes& s, bool backward, const LmMany& m, void* base) {
   LmCarve c{static_cast<uint8_t*>(base)};
   LmSpace o{};
-  if (s.T > 0 && lm_small(s, backward)) {
-    o.v = c.take<float>(s.T * s.R);
-    o.u = c.take<float>(backward ? s.T * s.R : 0);
-    o.parts = c.take<float>(s.T * (backward ? lm_splits(s.T, s.K, s.N) * s.K : lm_splits(s.T, s.N, s.K) * s.N));
-    o.bytes = c.used;
-    return o;
-  }
   const int64_t items = LmSizes::items(s.T, s.L);
   o.plan.rank = c.take<int>(s.T);
   o.plan.counts = c.take<int>(64 * (s.L + 1));
   o.plan.order = c.take<i32x2>(s.T);
   o.plan.item_id = c.take<int>(items);
   o.plan.slot_row = c.take<int>(items * LM_ITEM);
-  o.plan.chunks = c.take<i32x4>(s.chunks());
+  o.plan.chunks = c.take<i32x4>(m.chunks);
   o.plan.spans = c.take<i32x4>(s.L);
   o.plan.totals = c.take<int>(4);
   o.plan.zeros = c.take<uint16_t>(8);
   o.pieces = c.take<uint16_t>(s.T * 3 * s.rp());
-  // the passes over the rows: all of one size but the last, which may have more splits
-  const int64_t pass = s.T > 0 ? s.pass() : 1, rest = s.T % pass, on = backward ? s.K : s.N, in = backward ? s.N : s.K;
-  int64_t parts = 0;
-  for (const int64_t rows : {pass, rest}) {
-    const int64_t sp = rows > 0 ? lm_wide_splits(rows, on, in) : 1;
-    if (sp > 1 && sp * rows * on > parts) parts = sp * rows * on;
-  }
-  o.parts = c.take<float>(parts);
+  o.parts = c.take<float>(m.parts);
   if (backward) {
     o.ut = c.take<uint16_t>(items * LM_ITEM * 3 * s.rp());
     o.vt = c.take<uint16_t>(items * LM_ITEM * 3 * s.rp());
     o.act = c.take<float>(s.T * s.R);
-    o.part_a = c.take<float>(s.places() * s.R * s.K);
-    o.part_b = c.take<float>(s.places() * s.R * s.N);
+    o.part_a = c.take<float>(m.places * s.R * s.K);
+    o.part_b = c.take<float>(m.places * s.R * s.N);
   }
   o.bytes = c.used;
   return o;
+}
+
+LmSpace lm_space(const LmSizes& s, bool backward, void* base) {
+  if (s.T > 0 && lm_small(s, backward)) {
+    LmCarve c{static_cast<uint8_t*>(base)};
+    LmSpace o{};
+    o.v = c.take<float>(s.T * s.R);
+    o.u = c.take<float>(backward ? s.T * s.R : 0);
+    o.parts = c.take<float>(s.T * (backward ? lm_splits(s.T, s.K, s.N) * s.K : lm_splits(s.T, s.N, s.K) * s.N));
+    o.bytes = c.used;
+    return o;
+  }
+  // the passes over the rows: all of one size but the last, which may have more splits
+  const int64_t pass = s.T > 0 ? s.pass() : 1, on = backward ? s.K : s.N, in = backward ? s.N : s.K;
+  const int64_t parts = lm_parts(pass, on, in), rest = lm_parts(s.T % pass, on, in);
+  return lm_space_many(s, backward, {parts > rest ? parts : rest, s.chunks(), s.places()}, base);
+}
+
+// Bytes that are enough for s.T rows and for every smaller number: a caller has one workspace
+// for its largest batch.  The need itself falls where the way of computing changes.
+size_t lm_space_upto(const LmSizes& s, bool backward) {
+  LmSizes a = s;
+  size_t most = 0;
+  auto also = [&](size_t bytes) { most = bytes > most ? bytes : most; };
+  a.T = 0;
+  if (backward) also(lm_space(a, backward, nullptr).bytes);
+  // few rows: up to the end of every 64, whose splits are the same, and the last of them
+  for (int64_t t = 0; t < s.T; t += 64) {
+    a.T = t + 64 < s.T ? t + 64 : s.T;
+    while (a.T > t && !lm_small(a, backward)) --a.T;
+    if (a.T == t) break;
+    also(lm_space(a, backward, nullptr).bytes);
+  }
+  a.T = s.T;
+  if (s.T == 0 || lm_small(a, backward)) return most;
+  // many: the proportional part at the most rows, the rest each where it is the largest
+  const int64_t on = backward ? s.K : s.N, in = backward ? s.N : s.K;
+  LmMany m{lm_parts(s.pass(), on, in), s.chunks(), s.places()};
+  for (int64_t t = 64; t < s.pass() && t <= 64 * 256; t += 64) {
+    const int64_t parts = lm_parts(t, on, in);
+    if (parts > m.parts) m.parts = parts;
+  }
+  for (int64_t c = s.chunk_items() - 1; c > 0; --c) {  // the most rows with chunks of c items
+    int64_t low = 0, high = s.T;  // chunk_items() <= c at low, > c at high
+    while (high - low > 1) {
+      a.T = low + (high - low) / 2;
+      (a.chunk_items() > c ? high : low) = a.T;
+    }
+    a.T = low;
+    if (low == 0 || a.chunk_items() < c) continue;
+    if (a.chunks() > m.chunks) m.chunks = a.chunks();
+    if (a.places() > m.places) m.places = a.places();
+  }
+  also(lm_space_many(s, backward, m, nullptr).bytes);
+  return most;
 }
 
 mi_status lm_check(const char* what, const LmSizes& s, mi_dtype dt) {
@@ -1953,7 +2006,7 @@ extern "C" size_t mi_mm_lora_workspace_size(int64_t m, int64_t n, int64_t k, int
                                             int64_t rank, int backward) {
   const mi::LmSizes s{m, n, k, num_adapters, rank};
   if (mi::lm_check("mm_lora_workspace_size", s, MI_BF16) != MI_OK) return 0;
-  return mi::lm_space(s, backward != 0, nullptr).bytes;
+  return mi::lm_space_upto(s, backward != 0);
 }
 
 extern "C" mi_status mi_mm_lora(const void* x, int64_t m, int64_t k, mi_dtype dtype, const void* w,
