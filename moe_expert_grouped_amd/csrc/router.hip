@@ -142,6 +142,14 @@ struct RtRow {
   }
 };
 
+// p / sum, rounded once as a division is, from the sum's reciprocal (0 for a sum of 0): the
+// product's error is exact and corrects it (32768 tokens of 256 experts in bf16, balance and
+// gradient: 38.7 us, the product alone 38.2)
+__device__ __forceinline__ float rt_over(float p, float sum, float inv) {
+  const float q = p * inv;
+  return __builtin_fmaf(__builtin_fmaf(-sum, q, p), inv, q);
+}
+
 // order of a logit: larger is larger, -0 is 0, -inf is 0 (never chosen), NaN the largest
 __device__ __forceinline__ uint32_t rt_order(float z) {
   if (z != z) return 0xffffffffu;
@@ -371,7 +379,7 @@ __global__ __launch_bounds__(RT_BT) void rt_balance_kernel(RtBalance a) {
     const float sum = row.exps(p, top);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) acc[v] = __builtin_fmaf(p[v], inv, acc[v]);
+    for (int v = 0; v < VPL; ++v) acc[v] += rt_over(p[v], sum, inv);
     for (int j = g; j < a.k; j += G) {
       const int id = j == g ? first : gld<int32_t>(a.ids + t * a.k + j);
       if (id >= 0 && id < a.E) atomicAdd(&s_c[id], 1);
@@ -556,7 +564,7 @@ __global__ __launch_bounds__(256) void rt_backward_kernel(RtBackward a) {
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
       for (int v = 0; v < VPL; ++v) {
-        p[v] *= inv;
+        p[v] = rt_over(p[v], sum, inv);
         q[v] = b[v];
         d[v] = 0.f;
       }
