@@ -669,10 +669,15 @@ unsigned rt_blocks(int64_t T, int rows) {
   return static_cast<unsigned>(b < 4096 ? b : 4096);
 }
 
-// One workgroup, and one launch, while it reads no more than 32768 logits (512 tokens of 64
-// experts: 10 us for the two launches); else up to 256 of 64 rows at least.
+// One workgroup, and one launch, while its rows go in four rounds at most (as many lanes a row as
+// rt_shape gives it); else up to 256 of 64 rows at least.  us in a graph, one workgroup and two
+// launches: 64 experts, 256 tokens (two rounds) 7.9 and 8.9, 512 tokens 10.5 and 8.9, where the
+// second launch costs the host more than that, 1024 tokens 16.1 and 9.1; 256 experts, 128 tokens
+// (four) 10.3 and 11.5, 256 tokens 16.2 and 11.3; 8 experts, 512 tokens (four) 9.7 and 8.6, 4096
+// tokens 42 and 9.2.
 int rt_balance_blocks(int64_t T, int64_t E) {
-  if (T * E <= 32768) return 1;
+  const int64_t lanes = E <= 64 ? 8 : E <= 128 ? 16 : E <= 256 ? 32 : 64;
+  if (T <= 4 * (RT_BT / lanes)) return 1;
   const int64_t b = (T + 63) / 64;
   return static_cast<int>(b < RT_BLOCKS ? b : RT_BLOCKS);
 }
