@@ -1737,12 +1737,15 @@ int lm_splits(int64_t T, int64_t n, int64_t k) {
   return static_cast<int>(s < 1 ? 1 : s);
 }
 
-// The same of many rows and a narrow result, 16 steps at least (3817 rows, n 96, k 4760: the
-// product 25.8 us unsplit)
+// The same of many rows and a narrow result, 16 steps at least: the parts are written and read
+// once more.  us a call, unsplit and in 2, 3 and 4: 3817 rows, n 96, k 4760 (120 tiles, 75 steps)
+// 46, 40, 45, 42; 4096 rows, n 64, k 8192 (64, 128) 51, 44, 43, 43; 1100 rows, n 256, k 4096 (72, 64)
+// 30, 28, 28, 31; 2100 rows, n 72, k 2056 (66, 33) 28, 27, 26, 28; 2000 rows, n 128, k 2048 (64, 32)
+// 24, 25, 25, 25; with more tiles 1100 rows, n 512, k 8192 (144, 128) 46, 50, 44, 48; 1500 rows, n
+// 576, k 4096 (216, 64) 31, 35, 37, 39.
 int lm_wide_splits(int64_t T, int64_t n, int64_t k) {
   const int64_t tiles = (T + 63) / 64 * ((n + 63) / 64), steps = (k + LM_BK - 1) / LM_BK;
-  if (tiles > 256) return 1;
-  int64_t s = 512 / tiles;
+  int64_t s = 256 / tiles;
   if (s > steps / 16) s = steps / 16;
   return static_cast<int>(s < 1 ? 1 : s);
 }
@@ -1855,7 +1858,7 @@ size_t lm_space_upto(const LmSizes& s, bool backward) {
   // many: the proportional part at the most rows, the rest each where it is the largest
   const int64_t on = backward ? s.K : s.N, in = backward ? s.N : s.K;
   LmMany m{lm_parts(s.pass(), on, in), s.chunks(), s.places()};
-  for (int64_t t = 64; t < s.pass() && t <= 64 * 256; t += 64) {
+  for (int64_t t = 64; t < s.pass() && t <= 64 * 128; t += 64) {  // beyond, two parts are too many
     const int64_t parts = lm_parts(t, on, in);
     if (parts > m.parts) m.parts = parts;
   }

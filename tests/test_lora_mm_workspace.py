@@ -65,3 +65,9 @@ def test_one_workspace_for_all_batches(gpu, dtype):
         out, act = mi.mm_lora(*args, with_act=True)
         ref = (out, act, *mi.mm_lora_backward(go[:m], *args))
         assert all(torch.equal(p, q) for p, q in zip(got, ref)), m
+
+
+@pytest.mark.parametrize("m,n,k", [(8192, 128, 4096), (1500, 576, 4096), (1100, 896, 4096)])
+def test_no_parts_where_the_tiles_fill_the_card(m, n, k):
+    """Unsplit, a call needs no fp32 partial sums of its result."""
+    assert _need(m, n, k, 4, 16, False) < m * n * 4 + m * 250
