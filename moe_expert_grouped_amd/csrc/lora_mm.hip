@@ -291,14 +291,9 @@ __device__ __forceinline__ float lm_half(uint16_t h) {
 struct LmPieces { uint16_t p[3]; };
 __device__ __forceinline__ LmPieces lm_pieces(float v) {
   const uint32_t bits = __float_as_uint(v);
+  const bool odd = (bits & 0x7f800000u) == 0x7f800000u;
   LmPieces o;
-  if ((bits & 0x7f800000u) == 0x7f800000u) {
-    o.p[0] = static_cast<uint16_t>((bits >> 16 & 0x8000u) | 0x3f80u);
-    o.p[1] = 0;
-    o.p[2] = static_cast<uint16_t>(bits >> 16 | (bits & 0xffffu ? 1u : 0u));
-    return o;
-  }
-  float rest = v;
+  float rest = odd ? __builtin_copysignf(1.f, v) : v;
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
     uint16_t h = __builtin_bit_cast(uint16_t, static_cast<__bf16>(rest));
@@ -306,6 +301,7 @@ __device__ __forceinline__ LmPieces lm_pieces(float v) {
     o.p[i] = h;
     rest -= bf16_bits_to_f32(h);
   }
+  if (odd) o.p[2] = static_cast<uint16_t>(bits >> 16 | (bits & 0xffffu ? 1u : 0u));
   return o;
 }
 
@@ -1505,9 +1501,8 @@ __global__ __launch_bounds__(64 * ONE_W) void lm_one_kernel(LmSmall p) {
 //   ROWS == true:  gb[l, c, r] = sum_t v[t, r] go[t, c]
 // A step is 64 rows: those of x, and 64 slots of the transposed pieces, both by loads
 // straight into LDS; x is read down its columns.  A wavefront has 32 columns.  Bound by the
-// reads of x and go, once for all ranks up to 64: 8192 rows, n = k = 4096, rank 16: 31 us (134 MB:
-// 4.3 TB/s; the L2s fetch 148; 2 us are the look at every value of x for one that is not finite)
-// and 5 for the partial sums.
+// reads of x and go, once for all ranks up to 64: 8192 rows, n = k = 4096, rank 16: 29 us (134 MB:
+// 4.7 TB/s; the L2s fetch 148) and 5 for the partial sums.
 // ---------------------------------------------------------------------------
 struct LmGrad {
   const void* x;             // [T, C]
@@ -1534,8 +1529,8 @@ __device__ __forceinline__ void lm_grad(const LmGrad& a, uint8_t* st0, uint8_t* 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4, lr = lane >> 3;
-  const int C = a.C, R = a.R, RP = a.RP;
-  const int s0 = ch.y * LM_ITEM, n = ch.z * LM_ITEM, KT = (n + GR_BK - 1) / GR_BK;  // slots
+  int C = a.C, RP = a.RP, s0 = ch.y * LM_ITEM, n = ch.z * LM_ITEM;  // slots
+  const int R = a.R, KT = (n + GR_BK - 1) / GR_BK;
   constexpr int CPW = GR_BN / 8, NX = GR_X / 1024 / 4, PI = Shape::PI, ST = Shape::ST;
   const uint16_t* const x = static_cast<const uint16_t*>(a.x);
   const int chunk = (lane & 7) ^ lr;
@@ -1563,41 +1558,38 @@ __device__ __forceinline__ void lm_grad(const LmGrad& a, uint8_t* st0, uint8_t* 
   for (int b = 0; b < NB; ++b)
 #pragma unroll
     for (int j = 0; j < 2; ++j) acc[b][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  auto add = [&](const uint8_t* st) {
+  // apart: what is not finite in x taken on its own
+  auto add = [&](auto apart, const uint8_t* st) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int ck = (((g & 1) << 1) | (g >> 1)) + 4 * h;  // this lane's 8 slots
       u32x4 fx[2], fl[2];
+      LmOdd part[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int row = 8 * ck + (r >> 2);
         const uint8_t* at = st + row * (GR_BN * 2) + ((wave * 2 + j) ^ lm_tswz<GR_BN>(row)) * 32 + (r & 3) * 8;
         fx[j] = lm_column(at, at + 4 * GR_BN * 2);
         if constexpr (F16) lm_split(fx[j], fx[j], fl[j]);
-      }
-      auto pieces = [&](int b, int c) {
-        return *reinterpret_cast<const u32x4*>(st + GR_X + (b * 3 + c) * 2048 + r * 128 + (ck ^ lm_swz(r)) * 16);
-      };
-      auto mfma = [](u32x4 x, u32x4 p, f32x4 c) { return ROWS ? lm_mfma<false>(p, x, c) : lm_mfma<false>(x, p, c); };
-      if (__builtin_expect(__any(lm_odd(lm_top(fx[1], lm_top(fx[0], u16x2{0, 0})))), 0)) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const LmOdd o = lm_part(fx[j]);
-          fx[j] = o.rest;
-#pragma unroll
-          for (int b = 0; b < NB; ++b) acc[b][j] = mfma(o.odd, pieces(b, 0), acc[b][j]);
+        if constexpr (apart.value) {
+          part[j] = lm_part(fx[j]);
+          fx[j] = part[j].rest;
         }
       }
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int c = 0; c < 3; ++c) {
-          const u32x4 fp = pieces(b, c);
+          const u32x4 fp = *reinterpret_cast<const u32x4*>(st + GR_X + (b * 3 + c) * 2048 + r * 128 + (ck ^ lm_swz(r)) * 16);
+          auto mfma = [&](u32x4 x, f32x4 to) { return ROWS ? lm_mfma<false>(fp, x, to) : lm_mfma<false>(x, fp, to); };
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            acc[b][j] = mfma(fx[j], fp, acc[b][j]);
+            acc[b][j] = mfma(fx[j], acc[b][j]);
             if constexpr (F16) {
-              if (c < 2) acc[b][j] = mfma(fl[j], fp, acc[b][j]);
+              if (c < 2) acc[b][j] = mfma(fl[j], acc[b][j]);
+            }
+            if constexpr (apart.value) {
+              if (c == 0) acc[b][j] = mfma(part[j].odd, acc[b][j]);
             }
           }
         }
@@ -1605,33 +1597,58 @@ __device__ __forceinline__ void lm_grad(const LmGrad& a, uint8_t* st0, uint8_t* 
   };
   // a step past the last loads zeros
   constexpr int NI = NX + PI;
-  load(st0, 0);
-  if constexpr (ST == 3) load(st1, 1);
-  auto step = [&](const uint8_t* st, uint8_t* to, int kt) {
-    lm_wait_barrier<(ST - 2) * NI>();
-    load(to, kt + ST - 1);
-    add(st);
-  };
-  // whole rounds of the stages, then the rest
   const int rounds = KT / ST * ST;
-  if constexpr (ST == 3) {
-    for (int kt = 0; kt < rounds; kt += ST) {
-      step(st0, st2, kt);
-      step(st1, st0, kt + 1);
-      step(st2, st1, kt + 2);
+  auto all = [&](auto apart) {
+    load(st0, 0);
+    if constexpr (ST == 3) load(st1, 1);
+    auto step = [&](const uint8_t* st, uint8_t* to, int kt) {
+      lm_wait_barrier<(ST - 2) * NI>();
+      load(to, kt + ST - 1);
+      add(apart, st);
+    };
+    // whole rounds of the stages, then the rest
+    if constexpr (ST == 3) {
+      for (int kt = 0; kt < rounds; kt += ST) {
+        step(st0, st2, kt);
+        step(st1, st0, kt + 1);
+        step(st2, st1, kt + 2);
+      }
+      if (KT - rounds >= 1) {
+        step(st0, st2, rounds);
+        if (KT - rounds == 2) step(st1, st0, rounds + 1);
+      }
+    } else {
+      for (int kt = 0; kt < rounds; kt += ST) {
+        step(st0, st1, kt);
+        step(st1, st0, kt + 1);
+      }
+      if (KT - rounds == 1) step(st0, st1, rounds);
     }
-    if (KT - rounds >= 1) {
-      step(st0, st2, rounds);
-      if (KT - rounds == 2) step(st1, st0, rounds + 1);
-    }
-  } else {
-    for (int kt = 0; kt < rounds; kt += ST) {
-      step(st0, st1, kt);
-      step(st1, st0, kt + 1);
-    }
-    if (KT - rounds == 1) step(st0, st1, rounds);
+    lm_wait_barrier<0>();  // no load writes to LDS after the end
+  };
+  all(std::false_type{});
+  // Where a wavefront's sums are not all finite, they are taken again with what is not finite in x
+  // apart.  (A look at the values of x instead: 31 us for 29.)  The vote lies in a stage: more LDS
+  // would leave a CU one workgroup.
+  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) sum += acc[b][j] * 0.f;
+  const bool mine = __any(!(sum[0] + sum[1] + sum[2] + sum[3] == 0.f));
+  int* const vote = reinterpret_cast<int*>(st0);
+  if (lane == 0) vote[wave] = mine;
+  __syncthreads();
+  if (__builtin_expect(__builtin_amdgcn_readfirstlane(vote[0] | vote[1] | vote[2] | vote[3]), 0)) {
+    lm_wait_barrier<0>();  // all have read the votes
+    // nothing that the second pass derives from these is kept over the first
+    asm volatile("" : "+s"(C), "+s"(RP), "+s"(s0), "+s"(n), "+s"(c0), "+s"(rank0));
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) acc[b][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    all(std::true_type{});
   }
-  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): no load writes to LDS after the end
   // four ranks of column r (ROWS), or four columns of rank r
 #pragma unroll
   for (int b = 0; b < NB; ++b)
