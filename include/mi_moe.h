@@ -603,7 +603,8 @@ MI_API mi_status mi_moe_combine_rows_backward(
  *   x           dtype [m, k] (MI_BF16 or MI_F16);  w dtype [n, k]
  *   lora_a      dtype [num_adapters, rank, k];  lora_b dtype [num_adapters, n, rank].
  *               Adapters of lower rank are padded with zeros
- *   lora_ids    int32 [m], in any order;  lora_scale fp32 [num_adapters], NULL: 1
+ *   lora_ids    int32 [m], in any order;  lora_scale fp32 [num_adapters], NULL: 1; finite, and
+ *               lora_scale[l] * v[t] in fp32's range
  *   bias        dtype [n] or NULL
  *   out         out_dtype [m, n] (dtype or MI_F32)
  *   act         fp32 [m, rank] or NULL: v, 0 for rows without an adapter, which

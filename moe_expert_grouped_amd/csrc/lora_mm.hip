@@ -365,8 +365,8 @@ __device__ __forceinline__ int lm_swz(int row) { return (row & 7) ^ ((row >> 3) 
 //   BT == true:  bank [L, C, R], v[t, r] = sum_c x[t, c] bank[l, c, r]
 // A workgroup has the item's rows and 16 NB ranks; its wavefronts take steps of 64 columns
 // in turn, and their sums are added in order in LDS.  Bound by the reads of x, once, beside the
-// bank's from the L2: 8192 rows of 4096 columns, rank 16: 21 us (67 MB: 3.2 TB/s), transposed 28;
-// 16 adapters of rank 64 25 us.
+// bank's from the L2: 8192 rows of 4096 columns, rank 16: 21 us (67 MB: 3.3 TB/s), transposed, with
+// the pieces of both orders, 27; 16 adapters of rank 64 24 us.
 // ---------------------------------------------------------------------------
 struct LmShrink {
   const void* x;          // [T, C]
@@ -581,9 +581,10 @@ __global__ __launch_bounds__(64 * LmShape<NB>::W) void lm_shrink_kernel(LmShrink
 // mm: out = x w^T (BT: x w) plus the pieces times the adapters' matrix
 //   BT == false: w [n, k], bank [L, n, R]
 //   BT == true:  w [k, n], bank [L, R, n]
-// Bound by the MFMAs of the dense part: 8192 rows, n = k = 4096, rank 16: 201 us (1.37 PFLOP/s,
-// 177 us for a library product without adapters), transposed 212; 16 adapters of rank 64 237 us;
-// 4096 rows, n = k = 8192, a call with its plan and first product 369 us (library 335).
+// Bound by the MFMAs of the dense part, in the trace of a warm card: 8192 rows, n = k = 4096, rank
+// 16: 201 us (1.37 PFLOP/s; 181 a library product without adapters), transposed 211 (209); 16
+// adapters of rank 64 211.  4096 rows, n = k = 8192, a call with its plan and first product 408 us
+// (library 347).
 // ---------------------------------------------------------------------------
 struct LmMm {
   const void* x;          // [T, k]
@@ -860,7 +861,7 @@ __device__ __forceinline__ void lm_tile(const LmMm& p, const LmPlace& t, LmStage
   // there and both places of the second.  Ranks up to 16 need one stage, with the pieces side by
   // side in a row's 64 places and the bank's ranks once for each; the second stage has the next
   // run.  (The bank's ranks staged again for every piece, us a call: 8192 rows, n = k = 4096, 16
-  // adapters of rank 64, 244 for 237; 1111 rows fp16, rank 40, with gradients 106 for 96.)  All
+  // adapters of rank 64, 244 for 238; 1111 rows fp16, rank 40, with gradients 106 for 97.)  All
   // three pieces, for 16-bit outputs too: where the two parts cancel, what two leave, 2^-17 of
   // the adapters' part, may be more than the sum's half step.
   const int RP = p.RP, R = p.R;
@@ -1131,7 +1132,7 @@ __global__ __launch_bounds__(64 * WM * WN)
 //           launch sum gA and gB over the rows, which are few
 //
 // Bound by w's reads and a launch's start and end: 64 rows of 64 adapters, n = k = 4096, rank 16:
-// 11 and 5 us (51 MB; a read of that takes 8).
+// 12 and 5 us (45 MB; a read of that takes 7).
 // ---------------------------------------------------------------------------
 struct LmSmall {
   LmMm mm;                // w, x of the dense product; out: the partial sums [S, T, n]
@@ -1776,6 +1777,11 @@ int lm_wide_splits(int64_t T, int64_t n, int64_t k) {
 // rows 30 and 36; past the balance n 2048, k 8192, rank 16, 480 rows 52 and 49.  With the backward pass: n = k
 // = 4096, rank 16, 256 rows 69 and 80; rank 64, 128 rows (84M) 71 and 84, 192 rows (126M) 96
 // and 87; n 1024, k 2048, rank 16, 256 rows 31 and 52.
+// Up to 32 rows the adapters decide, which the call cannot see: many rows pay for each by itself.
+// Forward, k 4096: n 4096, rank 16, 32 rows of one adapter 14 and 26, of 32 adapters 15 and 45;
+// rank 256, one 38 and 30, 32 adapters 51 and 176; n 28672, rank 64, one 62 and 49, 32 adapters
+// 109 and 107; rank 256, one 127 and 57, 32 adapters 295 and 243, 8 rows of 8 adapters 88 and 106.
+// Backward alone: n 28672, rank 256, one 156 and 153, 32 adapters 511 and 1181.
 bool lm_small(const LmSizes& s, bool backward) {
   if (s.T <= 32) return true;
   if (backward) return s.T <= 256 && s.T * (s.N + s.K) * (s.R + 16) <= 100000000;

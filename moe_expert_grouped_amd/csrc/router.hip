@@ -245,7 +245,8 @@ struct RtRoute {
 // top_k.  A lane sorts its own values; then k times the largest of the lanes' heads is
 // taken and its lane moves on.  Keys are unique, so no choice depends on the layout.
 // Lane j keeps choice j and computes its weight from the logit that the key holds.
-// Bound by the VALU: 32768 tokens, 128 experts, top 8, bf16: 8.8 us (10.5 MB), 13.3 with the
+// Bound by the VALU (the row's exponentials among it, which renormalised weights do not need):
+// 32768 tokens, 128 experts, top 8, bf16: 8.3 us (10.5 MB), 13.3 with the
 // values left unsorted and three butterflies a choice.
 // ---------------------------------------------------------------------------
 template <typename T, int G, int VPL>
@@ -301,7 +302,7 @@ __global__ __launch_bounds__(256) void rt_route_kernel(RtRoute a) {
 // launch, whose workgroups have 64 experts each and leave the loss's terms to the last
 // of them to end.  One workgroup does it all for a small batch.  No atomic adds floats.  Bound by
 // latency, of a few rows' loads for every wavefront, then of the second launch's: 16411 tokens
-// of 256 experts in fp32: 9.6 and 7.5 us (17 MB); 512 tokens of 64 in one launch 9.8.
+// of 256 experts in fp32: 9.7 and 7.9 us (17 MB); 512 tokens of 64 in one launch 10.4.
 // ---------------------------------------------------------------------------
 struct RtBalance {
   const void* logits;
@@ -505,7 +506,7 @@ __global__ __launch_bounds__(RT_BT) void rt_balance_finish_kernel(RtBalance a) {
 // ---------------------------------------------------------------------------
 // backward.  A row is read and written once: 16411 tokens of 256 experts in fp32, of the
 // loss: 12.7 us (34 MB: 2.6 TB/s, the grid's start and end among it); through the weights of
-// 6 choices as well, 16384 tokens of 64: 6.4 us.
+// 6 choices as well, 16384 tokens of 64: 6.3 us.
 // ---------------------------------------------------------------------------
 struct RtBackward {
   const void* logits;
