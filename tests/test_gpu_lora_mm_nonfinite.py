@@ -19,10 +19,11 @@ pytestmark = pytest.mark.gpu
 INF = float("inf")
 HALVES = [torch.bfloat16, torch.float16]
 # one launch, few rows, 64 x 64 tiles, 128 x 128 (forward, backward), 256 x 256 (forward, backward),
-# a split k axis (forward, backward)
+# a split k axis (forward, backward); ranks up to 16 on the large tiles
 SIZES = [(1, 136, 264, 3, 32), (20, 136, 264, 3, 16), (1100, 264, 520, 4, 40), (1100, 2056, 136, 3, 24),
          (1100, 72, 2056, 3, 16), (4100, 2056, 72, 3, 72), (4100, 72, 2056, 3, 56),
-         (1100, 72, 4680, 3, 16), (1100, 4680, 72, 3, 40)]
+         (1100, 72, 4680, 3, 16), (1100, 4680, 72, 3, 40),
+         (1100, 2056, 136, 3, 16), (4100, 2056, 72, 3, 8), (4100, 72, 2056, 3, 16)]
 
 
 def _case(T, N, K, L, R, dtype, seed):

@@ -17,7 +17,8 @@ pytestmark = pytest.mark.gpu
 HALVES = [torch.bfloat16, torch.float16]
 # one launch, few rows, 64 x 64, 128 x 128 and 256 x 256 tiles, a split k axis
 SIZES = [(1, 136, 264, 2, 16), (20, 136, 264, 3, 16), (1100, 264, 520, 4, 40), (1100, 2056, 136, 3, 24),
-         (4100, 2056, 136, 3, 64), (1100, 72, 2056, 3, 16), (1100, 72, 4680, 3, 16)]
+         (4100, 2056, 136, 3, 64), (1100, 72, 2056, 3, 16), (1100, 72, 4680, 3, 16),
+         (1100, 2056, 136, 3, 16), (4100, 2056, 136, 3, 16)]
 
 
 def _whole(g, *shape, share=1.0):

@@ -23,6 +23,8 @@ SHAPES = [(4100, 2056, 520, 5, 72), (4100, 2056, 584, 9, 64), (4100, 520, 2056, 
           (1100, 2056, 520, 5, 72), (1100, 2056, 584, 9, 64), (1100, 520, 2056, 5, 72), (1100, 584, 2056, 9, 24),
           (4200, 264, 1000, 7, 40), (4200, 1000, 264, 7, 64), (4128, 136, 1096, 3, 136), (4128, 1096, 136, 3, 72),
           (2500, 200, 1608, 4, 32), (2500, 1608, 200, 4, 32),
+          # ranks up to 16, whose pieces lie side by side, in each tile
+          (4100, 2056, 520, 9, 16), (4100, 584, 2056, 40, 8), (1100, 2056, 584, 40, 16), (4128, 584, 1096, 5, 8), (1100, 264, 520, 70, 16),
           # narrow results over 74 steps, in four parts
           (1100, 72, 4680, 3, 40), (1100, 4680, 72, 3, 40)]
 
